@@ -518,7 +518,7 @@ def _own_pages_step(s):
     sbt, ctx, m, ws = s["sbt"], s["ctx"], s["map"], (s["workspace"], s["workspace_bytes"])
     sbt.pages_free(ctx, m, s["fork_to"], s["fork_to"].numel())
     sbt.pages_free(ctx, m, s["parents"], s["parents"].numel(), keep=s["keep"])
-    sbt.pages_reserve(ctx, m, s["target"], *ws)
+    sbt.pages_reserve(ctx, m, s["handles"], s["target"], *ws)
     sbt.pages_fork(ctx, m, s["handles"], s["fork_from"], s["fork_to"], s["fork_to"].numel(), *ws)
     return {"table": s["table"], "refs": s["refs"], "lens": s["lens"], "pools": s["pools"]}
 
