@@ -1,6 +1,7 @@
 /*
- * sbt.h -- bounds-checked tile movement and a boundary-tile bf16 GEMM on one
- * NVIDIA GB300 (sm_103a).  C ABI of libsbt.so.
+ * sbt.h -- bounds-checked tile movement, a boundary-tile bf16 GEMM and the
+ * operators of a paged key-value cache on one NVIDIA GB300 (sm_103a).  C ABI
+ * of libsbt.so.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -363,6 +364,219 @@ SBT_API sbt_status sbt_gemm_block_scaled(sbt_context* ctx, sbt_lowp_format a_fmt
 SBT_API sbt_status sbt_gemm_bounded_noalloc(sbt_context* ctx, const void* A, int64_t lda, const void* B, int64_t ldb,
                                             void* C, int64_t ldc, sbt_dtype c_dtype, int64_t M, int64_t N, int64_t K,
                                             void* stream);
+
+/*
+ * A paged key-value cache, the attention that reads it, and the pass that
+ * fills it.
+ *
+ * The cache holds, for every sequence, the keys and values of its positions
+ * 0 .. len - 1 in fixed-size pages drawn from a common pool.  Position t of
+ * sequence s lies in slot t % page_size of page page_table[s*ld_table +
+ * t / page_size].  A page number outside [0, n_pages) (such as the -1 of a row
+ * not yet filled) is no page: its positions are masked on a read and dropped
+ * on a write, as out-of-range indices are by the gather and the scatter.
+ */
+
+/* Pages of the sequences, and who holds them.  All arrays are device memory. */
+typedef struct {
+    int32_t* page_table;  /* [n_seq][ld_table], the first max_pages columns are used */
+    int64_t ld_table;     /* >= max_pages */
+    int32_t n_seq, max_pages;
+    int32_t* lens;        /* [n_seq] positions held; taken as min(max(len, 0), max_pages * page_size) */
+    int64_t n_pages;      /* pages of the pool, < 2^31 */
+    int32_t page_size;    /* positions per page, >= 1 */
+    int32_t* refs;        /* [n_pages] holders of each page, 0: free; may be NULL where a call does not need it */
+} sbt_page_map;
+
+/* Keys and values of one layer.  Element (page, slot, head, d) of either lies
+ * at page*ld_page + slot*ld_slot + head*ld_head + d: any order of slots and
+ * heads within a page, and pages spaced at will. */
+typedef struct {
+    void *k, *v;               /* device, `dtype` of the call */
+    int32_t heads, head_dim;   /* key-value heads; elements of a head */
+    int64_t ld_page, ld_slot, ld_head;
+} sbt_kv_cache;
+
+/*
+ * Attention of one new token per sequence over the cache.
+ *
+ *   visible(b) = positions t of sequence s = seq[b] (s = b if seq is NULL) with
+ *                max(0, len - window) <= t < len (0 <= t < len if window is 0)
+ *                on a page of the pool
+ *   score[t]   = scale * sum_d q[b][h][d] * K[t][h / (q_heads / heads)][d]
+ *   out[b][h]  = sum_t softmax(score)[t] * V[t][h / (q_heads / heads)]
+ *   lse[b][h]  = log(sum_t exp(score[t]))
+ *
+ * for b < batch, h < q_heads.  A row that sees no position (length 0, seq[b]
+ * outside [0, n_seq), no mapped page), or whose scores are all minus infinity,
+ * gets out = 0 and lse = minus infinity.  Cache contents at positions that are
+ * not visible are never read: NaN there reaches nothing.
+ *
+ * dtype: of q, the cache and out.  Products and sums are fp32; with SBT_BF16
+ * and SBT_F16 the probabilities enter the second product with 16 and 11
+ * significant bits.  1 <= head_dim <= 256; cache->heads divides q_heads.
+ * q, out: strides in elements per batch entry (ld_q, ld_out) and head (ld_qh,
+ * ld_oh).  lse: device fp32, dense [batch][q_heads], or NULL.
+ * workspace: device scratch of sbt_paged_attention_workspace_size() bytes,
+ * 256-byte aligned, owned by the caller and free again once the call has
+ * completed on `stream`; its size depends on neither the batch nor the
+ * lengths.  refs may be NULL.
+ */
+SBT_API sbt_status sbt_paged_attention_workspace_size(sbt_context* ctx, int32_t q_heads, int32_t kv_heads,
+                                                      int32_t head_dim, size_t* bytes);
+SBT_API sbt_status sbt_paged_attention(sbt_context* ctx, sbt_dtype dtype, const void* q, int64_t ld_q, int64_t ld_qh,
+                                       int32_t batch, int32_t q_heads, const sbt_kv_cache* cache,
+                                       const sbt_page_map* map, const int32_t* seq, float scale, int32_t window,
+                                       void* out, int64_t ld_out, int64_t ld_oh, float* lse, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/* Pairs that a rotation turns: (i, i + rot_dim/2), or (2i, 2i + 1). */
+typedef enum { SBT_ROPE_HALF = 0, SBT_ROPE_INTERLEAVED = 1 } sbt_rope_layout;
+/* How the frequencies f_i = base^(-2i/rot_dim) are stretched by `factor` s for
+ * contexts longer than the model was trained on:
+ *   SBT_ROPE_NONE      f_i
+ *   SBT_ROPE_LINEAR    f_i / s
+ *   SBT_ROPE_NTK       (base * s^(rot_dim/(rot_dim-2)))^(-2i/rot_dim)
+ *   SBT_ROPE_BY_PARTS  (1-g) f_i / s + g f_i with g = clamp((n_i - low)/(high - low), 0, 1)
+ *                      and n_i = orig_len * f_i / (2 pi), the turns made within the trained length */
+typedef enum { SBT_ROPE_NONE = 0, SBT_ROPE_LINEAR = 1, SBT_ROPE_NTK = 2, SBT_ROPE_BY_PARTS = 3 } sbt_rope_scaling;
+
+/* Rotations of the positions [0, n_pos): pair i at position t by the angle
+ * whose cosine and sine are table[(t*rot_dim/2 + i)*2 + {0, 1}] (device fp32,
+ * 8-byte aligned).  rot_dim = 0 (or a NULL sbt_rope): nothing is turned and
+ * any position >= 0 is legal. */
+typedef struct {
+    const float* table;
+    int64_t n_pos;
+    int32_t rot_dim;   /* even, <= head_dim: the first rot_dim elements of a head are turned */
+    int32_t layout;    /* sbt_rope_layout */
+} sbt_rope;
+
+/* Fills table[n_pos][rot_dim/2][2] with amplitude * (cos, sin)(t * f_i), angles
+ * formed in 64 bits and rounded once.  base > 0, factor > 0; low, high and
+ * orig_len are read by SBT_ROPE_BY_PARTS only (high > low, orig_len > 0). */
+SBT_API sbt_status sbt_rope_table(sbt_context* ctx, float* table, int64_t n_pos, int32_t rot_dim, double base,
+                                  sbt_rope_scaling scaling, double factor, int64_t orig_len, double low, double high,
+                                  double amplitude, void* stream);
+
+/*
+ * Per-head norm of queries and keys with the position rotation in the same
+ * pass, and the append of keys and values to the cache.
+ *
+ * For each head row x (head_dim elements) of q with weight w = q_weight, and
+ * of k with w = k_weight:
+ *   n = x * w / sqrt(mean(x^2) + eps)     (n = x where the weight is NULL)
+ *   y = n with its first rot_dim elements turned by the table at positions[t]
+ * computed in fp32 and rounded once.  y of q goes to q_out, y of k to k_out
+ * (may be NULL with a cache) and, with a cache, to position positions[t] of
+ * sequence seq[t] (t if seq is NULL); the rows of v (NULL: none) go there as
+ * they are.  A token whose position is negative or, where something is turned,
+ * at or past n_pos is padding: its rows of q_out and k_out are zero and the
+ * cache is not written.  A position without a page (or past max_pages *
+ * page_size, or a sequence outside [0, n_seq)) is not written to the cache.
+ * Two tokens of one call at the same place get one of the candidate values.
+ * map->lens and map->refs are neither read nor written (may be NULL).
+ *
+ * q, k, v: device [tokens] rows with element strides (ld_*, ld_*h) per token
+ * and head, so that they may be parts of one packed projection; k and v have
+ * k_heads heads.  q_out may be q and k_out may be k (same strides).
+ * 1 <= head_dim <= 512; with a cache, cache->heads = k_heads and
+ * cache->head_dim = head_dim.  k_heads = 0 or q_heads = 0 leaves that part out.
+ */
+SBT_API sbt_status sbt_qk_norm_rope(sbt_context* ctx, sbt_dtype dtype, const void* q, int64_t ld_q, int64_t ld_qh,
+                                    const void* k, int64_t ld_k, int64_t ld_kh, int64_t tokens, int32_t q_heads,
+                                    int32_t k_heads, int32_t head_dim, const int32_t* positions, const sbt_rope* rope,
+                                    const void* q_weight, const void* k_weight, float eps, void* q_out,
+                                    int64_t ld_qo, int64_t ld_qoh, void* k_out, int64_t ld_ko, int64_t ld_koh,
+                                    const void* v, int64_t ld_v, int64_t ld_vh, const sbt_kv_cache* cache,
+                                    const sbt_page_map* map, const int32_t* seq, void* stream);
+
+/*
+ * Gradient of sbt_qk_norm_rope.  gq, gk: gradients of q_out and k_out; q, k:
+ * the forward call's inputs (not read, and may be NULL, where the weight is
+ * NULL).  dq, dk get the gradients of q and k in `dtype` (rows of padding
+ * tokens are zero; dq may be gq and dk may be gk); dq_weight, dk_weight (fp32
+ * [head_dim], required exactly where the weight is given) the weights', summed
+ * over tokens and heads in fp32 in an order that is fixed on one device.
+ * workspace as elsewhere, of sbt_qk_norm_rope_backward_workspace_size() bytes.
+ */
+SBT_API sbt_status sbt_qk_norm_rope_backward_workspace_size(sbt_context* ctx, int32_t head_dim, size_t* bytes);
+SBT_API sbt_status sbt_qk_norm_rope_backward(sbt_context* ctx, sbt_dtype dtype, const void* gq, int64_t ld_gq,
+                                             int64_t ld_gqh, const void* gk, int64_t ld_gk, int64_t ld_gkh,
+                                             const void* q, int64_t ld_q, int64_t ld_qh, const void* k, int64_t ld_k,
+                                             int64_t ld_kh, int64_t tokens, int32_t q_heads, int32_t k_heads,
+                                             int32_t head_dim, const int32_t* positions, const sbt_rope* rope,
+                                             const void* q_weight, const void* k_weight, float eps, void* dq,
+                                             int64_t ld_dq, int64_t ld_dqh, void* dk, int64_t ld_dk, int64_t ld_dkh,
+                                             float* dq_weight, float* dk_weight, void* workspace,
+                                             size_t workspace_bytes, void* stream);
+
+/*
+ * Pages of a cache: copy, reserve, fork, free, compact.
+ *
+ * A pool is where pages of one kind lie: page p of plane i (a layer, say) is
+ * the page_bytes bytes at base + i*plane_stride + p*page_stride.  A page number
+ * stands for that page in every plane of every pool of the call, so one page
+ * map can serve all layers' keys and values.  Strides and sizes are in bytes;
+ * pages of 16-byte-aligned addresses and sizes move as 16-byte vectors.
+ *
+ * All state is on the device, and what a call does follows from it alone: free
+ * pages (refs 0 or less) are given lowest number first, and requests are
+ * served in their order.  Requests that are not legal (numbers out of range,
+ * no page left) are left out; nothing faults.
+ */
+#define SBT_MAX_PAGE_POOLS 64
+typedef struct {
+    void* base;
+    int64_t n_planes, plane_stride, page_stride, page_bytes;
+} sbt_page_pool;
+
+/* Scratch of reserve, fork and compact (256-byte aligned, the caller's). */
+SBT_API sbt_status sbt_pages_workspace_size(sbt_context* ctx, int32_t n_seq, int64_t n_pages, size_t* bytes);
+
+/* Copies page src[i] to page dst[i], i < n.  Pairs with a number outside
+ * [0, n_pages) are left out.  A page that is both a source and a destination,
+ * or twice a destination, holds one of the candidates per 16 bytes. */
+SBT_API sbt_status sbt_pages_copy(sbt_context* ctx, const sbt_page_pool* pools, int32_t n_pools, int64_t n_pages,
+                                  const int32_t* src, const int32_t* dst, int64_t n, void* stream);
+
+/* Grows every sequence s with target[s] > lens[s] to target[s] positions (lens
+ * is set): the table's next entries get free pages with one holder each.
+ * Where the last page held is part full and has other holders, the sequence
+ * first gets a copy of its own (of pools' bytes), so that what it appends
+ * reaches no other sequence.  Pages go to sequences in their order; one whose
+ * pages do not all fit after those of the sequences before it, or that has no
+ * room in its row, keeps its length (as lens then shows). */
+SBT_API sbt_status sbt_pages_reserve(sbt_context* ctx, const sbt_page_map* map, const sbt_page_pool* pools,
+                                     int32_t n_pools, const int32_t* target, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* Forks sequence from[i] into sequence to[i], i < n <= n_seq: the child shares
+ * the full pages and gets a copy of a part-full last page.  Left out (the
+ * child stays as it is): numbers out of range, from[i] = to[i], an empty
+ * parent, a child that is not empty or that an earlier pair took, and pairs
+ * that no free page is left for. */
+SBT_API sbt_status sbt_pages_fork(sbt_context* ctx, const sbt_page_map* map, const sbt_page_pool* pools,
+                                  int32_t n_pools, const int32_t* from, const int32_t* to, int32_t n,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Cuts sequence seqs[i] to at most keep[i] positions (0 if keep is NULL): the
+ * pages past them lose a holder, their table entries become -1, lens is set. */
+SBT_API sbt_status sbt_pages_free(sbt_context* ctx, const sbt_page_map* map, const int32_t* seqs, const int32_t* keep,
+                                  int32_t n, void* stream);
+
+/* Packs the held pages (refs > 0) into the lowest numbers: with L of them, the
+ * k-th held page at L or above moves to the k-th hole below L.  page_to[p]
+ * (int32 [n_pages]) gets p's new number or -1, n_live (int32 [1]) gets L,
+ * refs_out ([n_pages]) the holders by new number and table_out ([n_seq]
+ * [ld_out]) the entries within each length by new number (entries past it are
+ * not written).  table_out may be the map's table (then ld_out = ld_table) and
+ * refs_out the map's refs; otherwise the map is left as it was.  Bytes of pages
+ * that move stay at their old place too. */
+SBT_API sbt_status sbt_pages_compact(sbt_context* ctx, const sbt_page_map* map, const sbt_page_pool* pools,
+                                     int32_t n_pools, int32_t* table_out, int64_t ld_out, int32_t* refs_out,
+                                     int32_t* page_to, int32_t* n_live, void* workspace, size_t workspace_bytes,
+                                     void* stream);
 
 #ifdef __cplusplus
 }

@@ -35,8 +35,14 @@ EXPORTS = ("sbt_create", "sbt_destroy", "sbt_set_path", "sbt_set_wait_limit_ns",
            "sbt_check_status", "sbt_last_error_message", "sbt_tile_load_padded", "sbt_tile_store_clipped",
            "sbt_gather_rows", "sbt_gather_cols", "sbt_scatter_rows_masked", "sbt_scatter_add_rows", "sbt_ragged_tile_load", "sbt_ragged_tile_store", "sbt_gemm_bounded_workspace_size",
            "sbt_gemm_bounded", "sbt_gemm_block_scaled_workspace_size", "sbt_gemm_block_scaled",
-           "sbt_gemm_bounded_noalloc")
+           "sbt_gemm_bounded_noalloc", "sbt_paged_attention_workspace_size", "sbt_paged_attention", "sbt_rope_table",
+           "sbt_qk_norm_rope", "sbt_qk_norm_rope_backward_workspace_size", "sbt_qk_norm_rope_backward",
+           "sbt_pages_workspace_size", "sbt_pages_copy", "sbt_pages_reserve", "sbt_pages_fork", "sbt_pages_free",
+           "sbt_pages_compact")
 LOWP_FORMATS = {"e4m3": 0, "e5m2": 1, "e8m0": 2, "e2m1": 3}  # sbt_lowp_format
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}  # sbt_rope_layout
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}  # sbt_rope_scaling
+MAX_PAGE_POOLS = 64  # SBT_MAX_PAGE_POOLS in include/sbt.h
 GEMM_NOALLOC_SCRATCH_BYTES = 16 << 20  # SBT_GEMM_NOALLOC_SCRATCH_BYTES in include/sbt.h
 
 
@@ -44,6 +50,32 @@ class SbtError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {message}")
         self.status = status
+
+
+class KvCache(ctypes.Structure):
+    """``sbt_kv_cache``: keys and values of one layer in pages (made by ``kv_cache``)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("ld_page", ctypes.c_int64), ("ld_slot", ctypes.c_int64),
+                ("ld_head", ctypes.c_int64)]
+
+
+class PageMap(ctypes.Structure):
+    """``sbt_page_map``: the sequences' pages, lengths and the pages' holders (made by ``page_map``)."""
+    _fields_ = [("page_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("n_seq", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("lens", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("refs", ctypes.c_void_p)]
+
+
+class Rope(ctypes.Structure):
+    """``sbt_rope``: a table of rotations and which elements they turn (made by ``rope``)."""
+    _fields_ = [("table", ctypes.c_void_p), ("n_pos", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32)]
+
+
+class PagePool(ctypes.Structure):
+    """``sbt_page_pool`` (arrays of them are made by ``page_pools``)."""
+    _fields_ = [("base", ctypes.c_void_p), ("n_planes", ctypes.c_int64), ("plane_stride", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("page_bytes", ctypes.c_int64)]
 
 
 _lib = None
@@ -82,6 +114,25 @@ def load_library(path: str = LIB_PATH):
             "sbt_gemm_block_scaled": [p, ci, p, i64, ci, p, i64, ci, p, i64, p, i64, i64, p, i64, p, i64, i64, i64,
                                       i64, p, ctypes.c_size_t, p],
         }
+        pp, sz, f32, f64 = ctypes.POINTER, ctypes.c_size_t, ctypes.c_float, ctypes.c_double
+        cache, pmap, turn, pool = pp(KvCache), pp(PageMap), pp(Rope), pp(PagePool)
+        rows = [p, i64, i64]
+        sig.update({
+            "sbt_paged_attention_workspace_size": [p, i32, i32, i32, pp(sz)],
+            "sbt_paged_attention": [p, ci, *rows, i32, i32, cache, pmap, p, f32, i32, *rows, p, p, sz, p],
+            "sbt_rope_table": [p, p, i64, i32, f64, ci, f64, i64, f64, f64, f64, p],
+            "sbt_qk_norm_rope": [p, ci, *rows, *rows, i64, i32, i32, i32, p, turn, p, p, f32, *rows, *rows, *rows,
+                                 cache, pmap, p, p],
+            "sbt_qk_norm_rope_backward_workspace_size": [p, i32, pp(sz)],
+            "sbt_qk_norm_rope_backward": [p, ci, *rows, *rows, *rows, *rows, i64, i32, i32, i32, p, turn, p, p, f32,
+                                          *rows, *rows, p, p, p, sz, p],
+            "sbt_pages_workspace_size": [p, i32, i64, pp(sz)],
+            "sbt_pages_copy": [p, pool, i32, i64, p, p, i64, p],
+            "sbt_pages_reserve": [p, pmap, pool, i32, p, p, sz, p],
+            "sbt_pages_fork": [p, pmap, pool, i32, p, p, i32, p, sz, p],
+            "sbt_pages_free": [p, pmap, p, p, i32, p],
+            "sbt_pages_compact": [p, pmap, pool, i32, p, i64, p, p, p, p, sz, p],
+        })
         for name, args in sig.items():
             f = getattr(lib, name)
             f.argtypes = args
@@ -292,3 +343,129 @@ def gemm_bounded_noalloc(ctx, A, lda, B, ldb, C, ldc, M, N, K, c_dtype="bf16", s
     code = {"bf16": SBT_BF16, "f32": SBT_F32}[c_dtype] if isinstance(c_dtype, str) else int(c_dtype)
     _check(load_library().sbt_gemm_bounded_noalloc(ctx.handle, _ptr(A), lda, _ptr(B), ldb, _ptr(C), ldc, code, M, N,
                                                    K, _stream(stream)))
+
+
+# --------------------------------------------------------------------------- paged key-value cache
+# The handles below are plain structs of addresses and sizes, made once and passed to every call;
+# they keep the tensors they were made of alive.
+
+def kv_cache(k, v, heads, head_dim, ld_page, ld_slot, ld_head) -> KvCache:
+    """sbt_kv_cache: element (page, slot, head, d) at page*ld_page + slot*ld_slot + head*ld_head + d of k and of v."""
+    c = KvCache(_ptr(k), _ptr(v), heads, head_dim, ld_page, ld_slot, ld_head)
+    c.tensors = (k, v)
+    return c
+
+
+def page_map(page_table, ld_table, n_seq, max_pages, lens, n_pages, page_size, refs=None) -> PageMap:
+    """sbt_page_map: int32 page_table [n_seq][ld_table], lens [n_seq] and refs [n_pages] (where a call needs them)."""
+    m = PageMap(_ptr(page_table), ld_table, n_seq, max_pages, _ptr(lens), n_pages, page_size, _ptr(refs))
+    m.tensors = (page_table, lens, refs)
+    return m
+
+
+def rope(table, n_pos, rot_dim, layout="half") -> Rope:
+    """sbt_rope: fp32 table [n_pos][rot_dim/2][2] of (cos, sin), as rope_table fills it."""
+    r = Rope(_ptr(table), n_pos, rot_dim, ROPE_LAYOUTS[layout] if isinstance(layout, str) else int(layout))
+    r.tensors = (table,)
+    return r
+
+
+def page_pools(pools):
+    """Array of sbt_page_pool from tuples (base, n_planes, plane_stride, page_stride, page_bytes), in bytes."""
+    a = (PagePool * len(pools))(*[PagePool(_ptr(b), n, ps, gs, nb) for b, n, ps, gs, nb in pools])
+    a.tensors = tuple(t[0] for t in pools)
+    return a
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def paged_attention_workspace_size(ctx, q_heads, kv_heads, head_dim) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().sbt_paged_attention_workspace_size(ctx.handle, q_heads, kv_heads, head_dim, ctypes.byref(n)))
+    return int(n.value)
+
+
+def paged_attention(ctx, q, ld_q, ld_qh, batch, q_heads, cache, map, scale, out, ld_out, ld_oh, lse=None, window=0,
+                    seq=None, workspace=None, workspace_bytes=0, dtype=None, stream=None):
+    """sbt_paged_attention: one new token per batch entry over the first lens positions of its sequence."""
+    code = _dtype_code(q, dtype)
+    _check(load_library().sbt_paged_attention(ctx.handle, code, _ptr(q), ld_q, ld_qh, batch, q_heads, _ref(cache),
+                                              _ref(map), _ptr(seq), scale, window, _ptr(out), ld_out, ld_oh, _ptr(lse),
+                                              _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def rope_table(ctx, table, n_pos, rot_dim, base=10000.0, scaling="none", factor=1.0, orig_len=0, low=1.0, high=32.0,
+               amplitude=1.0, stream=None):
+    """sbt_rope_table: fills the fp32 table [n_pos][rot_dim/2][2]; scalings by name (see ROPE_SCALINGS)."""
+    code = ROPE_SCALINGS[scaling] if isinstance(scaling, str) else int(scaling)
+    _check(load_library().sbt_rope_table(ctx.handle, _ptr(table), n_pos, rot_dim, base, code, factor, orig_len, low,
+                                         high, amplitude, _stream(stream)))
+
+
+def qk_norm_rope(ctx, q, ld_q, ld_qh, k, ld_k, ld_kh, tokens, q_heads, k_heads, head_dim, positions, rope, q_out,
+                 ld_qo, ld_qoh, k_out=None, ld_ko=0, ld_koh=0, q_weight=None, k_weight=None, eps=1e-6, v=None, ld_v=0,
+                 ld_vh=0, cache=None, map=None, seq=None, dtype=None, stream=None):
+    """sbt_qk_norm_rope: norm and rotation of q and k; with a cache, k and v are appended at `positions`."""
+    code = _dtype_code(k if q is None else q, dtype)
+    _check(load_library().sbt_qk_norm_rope(ctx.handle, code, _ptr(q), ld_q, ld_qh, _ptr(k), ld_k, ld_kh, tokens,
+                                           q_heads, k_heads, head_dim, _ptr(positions), _ref(rope), _ptr(q_weight),
+                                           _ptr(k_weight), eps, _ptr(q_out), ld_qo, ld_qoh, _ptr(k_out), ld_ko, ld_koh,
+                                           _ptr(v), ld_v, ld_vh, _ref(cache), _ref(map), _ptr(seq), _stream(stream)))
+
+
+def qk_norm_rope_backward_workspace_size(ctx, head_dim) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().sbt_qk_norm_rope_backward_workspace_size(ctx.handle, head_dim, ctypes.byref(n)))
+    return int(n.value)
+
+
+def qk_norm_rope_backward(ctx, gq, ld_gq, ld_gqh, gk, ld_gk, ld_gkh, q, ld_q, ld_qh, k, ld_k, ld_kh, tokens, q_heads,
+                          k_heads, head_dim, positions, rope, dq, ld_dq, ld_dqh, dk, ld_dk, ld_dkh, q_weight=None,
+                          k_weight=None, eps=1e-6, dq_weight=None, dk_weight=None, workspace=None, workspace_bytes=0,
+                          dtype=None, stream=None):
+    """sbt_qk_norm_rope_backward: gradients of q and k (and, fp32, of the weights) from those of q_out and k_out."""
+    code = _dtype_code(gk if gq is None else gq, dtype)
+    _check(load_library().sbt_qk_norm_rope_backward(
+        ctx.handle, code, _ptr(gq), ld_gq, ld_gqh, _ptr(gk), ld_gk, ld_gkh, _ptr(q), ld_q, ld_qh, _ptr(k), ld_k, ld_kh,
+        tokens, q_heads, k_heads, head_dim, _ptr(positions), _ref(rope), _ptr(q_weight), _ptr(k_weight), eps, _ptr(dq),
+        ld_dq, ld_dqh, _ptr(dk), ld_dk, ld_dkh, _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace), workspace_bytes,
+        _stream(stream)))
+
+
+def pages_workspace_size(ctx, n_seq, n_pages) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().sbt_pages_workspace_size(ctx.handle, n_seq, n_pages, ctypes.byref(n)))
+    return int(n.value)
+
+
+def pages_copy(ctx, pools, n_pages, src, dst, n, stream=None):
+    """sbt_pages_copy: page src[i] to page dst[i] in every plane of every pool."""
+    _check(load_library().sbt_pages_copy(ctx.handle, pools, len(pools), n_pages, _ptr(src), _ptr(dst), n,
+                                         _stream(stream)))
+
+
+def pages_reserve(ctx, map, pools, target, workspace, workspace_bytes, stream=None):
+    """sbt_pages_reserve: grow the sequences to target positions (map's lens show which did)."""
+    _check(load_library().sbt_pages_reserve(ctx.handle, _ref(map), pools, len(pools), _ptr(target), _ptr(workspace),
+                                            workspace_bytes, _stream(stream)))
+
+
+def pages_fork(ctx, map, pools, from_seq, to_seq, n, workspace, workspace_bytes, stream=None):
+    """sbt_pages_fork: sequence to_seq[i] becomes a copy of from_seq[i] that shares its full pages."""
+    _check(load_library().sbt_pages_fork(ctx.handle, _ref(map), pools, len(pools), _ptr(from_seq), _ptr(to_seq), n,
+                                         _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def pages_free(ctx, map, seqs, n, keep=None, stream=None):
+    """sbt_pages_free: cut sequence seqs[i] to keep[i] positions (to none without keep)."""
+    _check(load_library().sbt_pages_free(ctx.handle, _ref(map), _ptr(seqs), _ptr(keep), n, _stream(stream)))
+
+
+def pages_compact(ctx, map, pools, table_out, ld_out, refs_out, page_to, n_live, workspace, workspace_bytes,
+                  stream=None):
+    """sbt_pages_compact: pack the held pages to the front; page_to gets every page's new number or -1."""
+    _check(load_library().sbt_pages_compact(ctx.handle, _ref(map), pools, len(pools), _ptr(table_out), ld_out,
+                                            _ptr(refs_out), _ptr(page_to), _ptr(n_live), _ptr(workspace),
+                                            workspace_bytes, _stream(stream)))

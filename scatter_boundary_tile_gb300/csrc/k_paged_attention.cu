@@ -1,0 +1,309 @@
+// Paged attention, 16-bit caches: the tile math on the tensor cores.
+//
+// S^T = K Q^T and O^T += V^T P^T: positions (then head elements) are the
+// 16-row side of mma.m16n8k16 and the query heads of one key-value head its
+// 8-column side, so one to eight heads cost one column block.  The operation
+// reads every key and value once and does 2 x 8 multiply-adds with each, 54
+// TFLOP/s at the copy peak for one column block: memory bounds it, the mma.sync rate is
+// far above what it asks, and operands of 16 rows a warp let every warp run
+// its own softmax without waiting for a 128-row tile.
+//
+// The probabilities are rounded to 16 bits for the second product.  fp16 holds
+// them to 2^-11; bf16 would hold them to 2^-8 only, as much as the output's
+// own rounding, so there a probability is split in two bf16 numbers
+// (p = hi + lo to 2^-16) and multiplied twice.  l is summed from the fp32 values.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "k_paged_attention.cuh"
+
+namespace {
+
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t* r, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+template <bool BF>
+__device__ __forceinline__ void mma16(float* c, const uint32_t* a, const uint32_t* b) {
+    if (BF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+template <bool BF, int DP_, int NB>
+struct Mma16 {
+    typedef uint16_t T;
+    static constexpr int ES = 2, TOK = 16, DP = DP_, HEADS = 8 * NB, OWN = 2 * NB;
+    // rows of a multiple of 128 bytes swizzle their chunks, others are padded to an odd number of
+    // chunks: either way the eight rows of one 8 x 8 matrix lie in different banks
+    static constexpr bool SWIZZLE = DP % 64 == 0;
+    static constexpr int PITCH = SWIZZLE ? DP * 2 : DP * 2 + 16;
+    static constexpr int MERGE_HEADS = 4, SCRATCH_BYTES = 0;
+    static __device__ __forceinline__ int chunk16(int t, int c) { return SWIZZLE ? c ^ (t & 7) : c; }
+    static __device__ __forceinline__ uint16_t from_float(float x) {
+        return BF ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
+    }
+    static __device__ __forceinline__ float to_float(uint16_t x) {
+        return BF ? __bfloat162float(__ushort_as_bfloat16(x)) : __half2float(__ushort_as_half(x));
+    }
+
+    uint32_t qf[DP / 16][NB][2];
+    float o[DP / 16][NB][4];
+    float mx[NB][2], l[NB][2];
+
+    __device__ __forceinline__ void load_q(const AttnParams& p, const AttnRow& r, int32_t row, float*) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, q2 = (lane & 3) * 2;
+        const int32_t kvh = row / p.n_chunks, h0 = (row - kvh * p.n_chunks) * p.chunk;
+        const int32_t heads = p.group - h0 < p.chunk ? p.group - h0 : p.chunk;
+        const uint16_t* base = reinterpret_cast<const uint16_t*>(p.q) + r.b * p.ld_q + (kvh * p.group + h0) * p.ld_qh;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            const int h = n * 8 + g;
+            const uint16_t* x = base + h * p.ld_qh;
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int d = k * 16 + i * 8 + q2;
+                    uint32_t w = 0;
+                    if (h < heads && d < p.head_dim) {
+                        if (p.q_words) {
+                            w = __ldg(reinterpret_cast<const uint32_t*>(x + d));
+                        } else {
+                            w = __ldg(x + d);
+                            if (d + 1 < p.head_dim) w |= (uint32_t)__ldg(x + d + 1) << 16;
+                        }
+                    }
+                    qf[k][n][i] = w;
+                }
+            mx[n][0] = mx[n][1] = -CUDART_INF_F;
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[k][n][i] = 0.f;
+        }
+    }
+
+    __device__ __forceinline__ void tile(const AttnParams& p, const uint8_t*, uint32_t k_s, uint32_t v_s, uint32_t bits,
+                                         float*) {
+        const int lane = threadIdx.x & 31, g = lane >> 2;
+        float s[NB][4];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        const int kr = lane & 15, kc = lane >> 4;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+            uint32_t a[4];
+            ldsm4(a, k_s + kr * PITCH + chunk16(kr, 2 * k + kc) * 16);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) mma16<BF>(s[n], a, qf[k][n]);
+        }
+        const bool see0 = (bits >> g) & 1u, see1 = (bits >> (g + 8)) & 1u;
+        uint32_t hi[NB][2], lo[NB][2];
+        float alpha[NB][2];
+        bool grown = false;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            float pr[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float a = see0 ? s[n][j] * p.scale_log2 : -CUDART_INF_F;
+                const float b = see1 ? s[n][j + 2] * p.scale_log2 : -CUDART_INF_F;
+                float t = fmaxf(a, b);
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                t = fmaxf(t, mx[n][j]);
+                const float ts = t == -CUDART_INF_F ? 0.f : t;
+                alpha[n][j] = sbt_attn::exp2_fast(mx[n][j] - ts);
+                grown |= t != mx[n][j];
+                mx[n][j] = t;
+                pr[j] = sbt_attn::exp2_fast(a - ts);
+                pr[j + 2] = sbt_attn::exp2_fast(b - ts);
+                l[n][j] = l[n][j] * alpha[n][j] + pr[j] + pr[j + 2];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint16_t h0 = from_float(pr[2 * i]), h1 = from_float(pr[2 * i + 1]);
+                hi[n][i] = transpose8((uint32_t)h0 | (uint32_t)h1 << 16);
+                if (BF) {
+                    const uint16_t l0 = from_float(pr[2 * i] - to_float(h0)), l1 = from_float(pr[2 * i + 1] - to_float(h1));
+                    lo[n][i] = transpose8((uint32_t)l0 | (uint32_t)l1 << 16);
+                }
+            }
+        }
+        if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[k][n][i] *= alpha[n][i & 1];
+        }
+        const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+            uint32_t a[4];
+            ldsm4_t(a, v_s + vr * PITCH + chunk16(vr, 2 * k + vc) * 16);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                mma16<BF>(o[k][n], a, hi[n]);
+                if (BF) mma16<BF>(o[k][n], a, lo[n]);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void reduce() {
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 4);
+                l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 8);
+                l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 16);
+            }
+    }
+    __device__ __forceinline__ void put_ml(float* m, float* sum) const {
+        const int lane = threadIdx.x & 31;
+        if (lane < 4)
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    m[n * 8 + lane * 2 + j] = mx[n][j];
+                    sum[n * 8 + lane * 2 + j] = l[n][j];
+                }
+    }
+    __device__ __forceinline__ void heads_max(const float (*s_m)[HEADS], float* top) const {
+        const int q2 = (threadIdx.x & 3) * 2;
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            top[i] = -CUDART_INF_F;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) top[i] = fmaxf(top[i], s_m[w][(i >> 1) * 8 + q2 + (i & 1)]);
+        }
+    }
+    __device__ __forceinline__ void rescale_to(const float* top) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float a = sbt_attn::exp2_fast(mx[n][j] - top[2 * n + j]);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    o[k][n][j] *= a;
+                    o[k][n][j + 2] *= a;
+                }
+            }
+    }
+    // heads hb .. hb + 3 of this warp into dst[head - hb][element]
+    __device__ __forceinline__ void put_o(float* dst, int pitch, int hb) const {
+        const int lane = threadIdx.x & 31, g = lane >> 2, q2 = (lane & 3) * 2;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            if (n != hb / 8) continue;
+            const int h = n * 8 + q2 - hb;
+            if (h < 0 || h >= MERGE_HEADS) continue;
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+                dst[h * pitch + k * 16 + g] = o[k][n][0];
+                dst[(h + 1) * pitch + k * 16 + g] = o[k][n][1];
+                dst[h * pitch + k * 16 + g + 8] = o[k][n][2];
+                dst[(h + 1) * pitch + k * 16 + g + 8] = o[k][n][3];
+            }
+        }
+    }
+};
+
+template <bool BF, int DP, int STAGES>
+sbt_status by_heads(sbt_context* ctx, const AttnParams& p, cudaStream_t stream) {
+    const int heads = p.group < p.chunk ? p.group : p.chunk;
+    if (heads <= 8) return sbt_attention_enqueue<Mma16<BF, DP, 1>, STAGES>(ctx, p, stream);
+    return sbt_attention_enqueue<Mma16<BF, DP, 2>, STAGES>(ctx, p, stream);
+}
+
+template <bool BF>
+sbt_status by_dim(sbt_context* ctx, const AttnParams& p, cudaStream_t stream) {
+    if (p.head_dim <= 64) return by_heads<BF, 64, 6>(ctx, p, stream);
+    if (p.head_dim <= 128) return by_heads<BF, 128, 3>(ctx, p, stream);
+    return by_heads<BF, 256, 3>(ctx, p, stream);
+}
+
+}  // namespace
+
+namespace {
+
+// Query heads of one row: 16 of them (two column blocks) at most on the tensor
+// cores, 8 in fp32 multiply-adds; more are cut into rows of equal size.
+void cut_heads(int32_t group, int32_t most, int32_t* chunk, int32_t* n_chunks) {
+    *n_chunks = (int32_t)sbt_cdiv(group, most);
+    *chunk = (int32_t)sbt_cdiv(group, *n_chunks);
+}
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace
+
+// One size for every type: the states of two cut rows per block, for the
+// largest grid, and the descriptors of the rows that began in each block.
+size_t sbt_paged_attention_workspace_bytes(const sbt_context* ctx, int32_t q_heads, int32_t kv_heads,
+                                           int32_t head_dim) {
+    int32_t chunk, n;
+    cut_heads(q_heads / kv_heads, kAttnMaxHeads, &chunk, &n);
+    const size_t g = (size_t)ctx->sm_count * kAttnMaxPerSm;
+    const size_t heads = chunk <= 8 ? 8 : 16, dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
+    return round256(g * sizeof(AttnDesc)) + round256(2 * g * kAttnMaxHeads * sizeof(float2)) +
+           2 * g * heads * dp * sizeof(float);
+}
+
+sbt_status sbt_launch_paged_attention(sbt_context* ctx, sbt_dtype dtype, const SbtHeadRows& q, int32_t batch,
+                                      int32_t q_heads, const sbt_kv_cache* cache, const sbt_page_map* map,
+                                      const int32_t* seq, float scale, int32_t window, const SbtHeadRows& out,
+                                      float* lse, void* workspace, cudaStream_t stream) {
+    const int es = sbt_dtype_size(dtype);
+    AttnParams p = {};
+    p.q = (const char*)q.p, p.k = (const char*)cache->k, p.v = (const char*)cache->v;
+    p.out = (char*)const_cast<void*>(out.p), p.lse = lse;
+    p.table = map->page_table, p.lens = map->lens, p.seq = seq;
+    p.ld_q = q.ld, p.ld_qh = q.ldh, p.ld_out = out.ld, p.ld_oh = out.ldh;
+    p.ld_page = cache->ld_page, p.ld_slot = cache->ld_slot, p.ld_head = cache->ld_head;
+    p.ld_table = map->ld_table, p.n_pages = map->n_pages;
+    p.batch = batch, p.q_heads = q_heads, p.kv_heads = cache->heads, p.group = q_heads / cache->heads;
+    cut_heads(p.group, dtype == SBT_F32 ? 8 : kAttnMaxHeads, &p.chunk, &p.n_chunks);
+    p.n_seq = map->n_seq, p.head_dim = cache->head_dim, p.window = window;
+    const int64_t most = (int64_t)map->max_pages * map->page_size;
+    p.max_len = (int32_t)(most < 0x7ffffc00 ? most : 0x7ffffc00);  // tile positions stay below 2^31
+    p.page_size = sbt_make_fastdiv((uint32_t)map->page_size);
+    p.scale_log2 = scale * 1.4426950408889634f;
+    const int64_t bits = (reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) |
+                         ((int64_t)p.head_dim | p.ld_page | p.ld_slot | p.ld_head) * es;
+    p.copy_bytes = ctx->path == SBT_PATH_SCALAR ? es : bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : es;
+    p.q_words = (reinterpret_cast<uintptr_t>(p.q) | ((int64_t)p.head_dim | p.ld_q | p.ld_qh) * es) % 4 == 0;
+    const size_t g = (size_t)ctx->sm_count * kAttnMaxPerSm;
+    p.desc = (AttnDesc*)workspace;
+    p.part_ml = (float2*)((char*)workspace + round256(g * sizeof(AttnDesc)));
+    p.part_o = (float*)((char*)p.part_ml + round256(2 * g * kAttnMaxHeads * sizeof(float2)));
+    if (dtype == SBT_F32) return sbt_attention_f32(ctx, p, stream);
+    return dtype == SBT_BF16 ? by_dim<true>(ctx, p, stream) : by_dim<false>(ctx, p, stream);
+}

@@ -1,0 +1,160 @@
+// Paged attention, 32-bit caches: the tile math in fp32 multiply-adds, since a
+// tensor-core product would round the operands to fewer bits.
+//
+// A warp tile is eight positions.  Scores: four lanes share a position and take
+// every fourth 16-byte piece of its key; queries are read from shared memory
+// (one address per quarter of the warp).  Values: a lane owns DP / 32 elements
+// of the head and adds p v over the eight positions.
+#include "k_paged_attention.cuh"
+
+namespace {
+
+template <int DP_, int HT>
+struct Fma32 {
+    typedef float T;
+    static constexpr int ES = 4, TOK = 8, DP = DP_, HEADS = HT, OWN = HT;
+    static constexpr int PITCH = DP * 4 + 64;  // two rows of four 16-byte pieces fill the banks
+    static constexpr int MERGE_HEADS = HT < 4 ? HT : 4;
+    static constexpr int EL = DP / 32;         // head elements per lane
+    static constexpr int SCRATCH_BYTES = (HT * DP + kAttnWarps * TOK * HT) * 4;
+    static __device__ __forceinline__ int chunk16(int, int c) { return c; }
+    static __device__ __forceinline__ float from_float(float x) { return x; }
+
+    float o[HT][EL];
+    float mx[HT], l[HT];
+
+    __device__ __forceinline__ void load_q(const AttnParams& p, const AttnRow& r, int32_t row, float* s_q) {
+        const int32_t kvh = row / p.n_chunks, h0 = (row - kvh * p.n_chunks) * p.chunk;
+        const int32_t heads = p.group - h0 < p.chunk ? p.group - h0 : p.chunk;
+        const float* base = reinterpret_cast<const float*>(p.q) + r.b * p.ld_q + (kvh * p.group + h0) * p.ld_qh;
+        for (int i = threadIdx.x; i < HT * DP; i += kAttnThreads) {
+            const int h = i / DP, d = i - h * DP;
+            s_q[i] = h < heads && d < p.head_dim ? __ldg(base + h * p.ld_qh + d) : 0.f;
+        }
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+            mx[h] = -CUDART_INF_F;
+            l[h] = 0.f;
+#pragma unroll
+            for (int e = 0; e < EL; ++e) o[h][e] = 0.f;
+        }
+        __syncthreads();
+    }
+
+    __device__ __forceinline__ void tile(const AttnParams& p, const uint8_t* stage, uint32_t, uint32_t, uint32_t bits,
+                                         float* s_q) {
+        const int lane = threadIdx.x & 31, t = lane >> 2, part = lane & 3;
+        float* const s_p = s_q + HT * DP + (threadIdx.x >> 5) * TOK * HT;
+        const float* kr = reinterpret_cast<const float*>(stage + t * PITCH) + part * 4;
+        float s[HT];
+#pragma unroll
+        for (int h = 0; h < HT; ++h) s[h] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < DP / 16; ++i) {
+            const float4 k4 = *reinterpret_cast<const float4*>(kr + i * 16);
+#pragma unroll
+            for (int h = 0; h < HT; ++h) {
+                const float4 q4 = *reinterpret_cast<const float4*>(s_q + h * DP + i * 16 + part * 4);
+                s[h] = fmaf(k4.x, q4.x, fmaf(k4.y, q4.y, fmaf(k4.z, q4.z, fmaf(k4.w, q4.w, s[h]))));
+            }
+        }
+        const bool see = (bits >> t) & 1u;
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+            float x = s[h];
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            x = see ? x * p.scale_log2 : -CUDART_INF_F;
+            float top = x;
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            top = fmaxf(top, mx[h]);
+            const float ts = top == -CUDART_INF_F ? 0.f : top;
+            const float alpha = sbt_attn::exp2_fast(mx[h] - ts);
+            const float pr = sbt_attn::exp2_fast(x - ts);
+            mx[h] = top;
+            l[h] = l[h] * alpha + pr;  // the four lanes of a position hold the same sum
+            if (part == 0) s_p[t * HT + h] = pr;
+#pragma unroll
+            for (int e = 0; e < EL; ++e) o[h][e] *= alpha;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int tt = 0; tt < TOK; ++tt) {
+            const float* vr = reinterpret_cast<const float*>(stage + (TOK + tt) * PITCH) + lane * EL;
+            float v[EL], w[HT];
+            if (EL % 4 == 0) {
+#pragma unroll
+                for (int e = 0; e < EL; e += 4) *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(vr + e);
+            } else {
+                *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(vr);
+            }
+#pragma unroll
+            for (int h = 0; h < HT; ++h) w[h] = s_p[tt * HT + h];
+#pragma unroll
+            for (int h = 0; h < HT; ++h)
+#pragma unroll
+                for (int e = 0; e < EL; ++e) o[h][e] = fmaf(w[h], v[e], o[h][e]);
+        }
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ void reduce() {
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 4);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 8);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 16);
+        }
+    }
+    __device__ __forceinline__ void put_ml(float* m, float* sum) const {
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int h = 0; h < HT; ++h) {
+                m[h] = mx[h];
+                sum[h] = l[h];
+            }
+    }
+    __device__ __forceinline__ void heads_max(const float (*s_m)[HEADS], float* top) const {
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+            top[h] = -CUDART_INF_F;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) top[h] = fmaxf(top[h], s_m[w][h]);
+        }
+    }
+    __device__ __forceinline__ void rescale_to(const float* top) {
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+            const float a = sbt_attn::exp2_fast(mx[h] - top[h]);
+#pragma unroll
+            for (int e = 0; e < EL; ++e) o[h][e] *= a;
+        }
+    }
+    __device__ __forceinline__ void put_o(float* dst, int pitch, int hb) const {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int h = 0; h < HT; ++h)
+            if (h >= hb && h < hb + MERGE_HEADS)
+#pragma unroll
+                for (int e = 0; e < EL; ++e) dst[(h - hb) * pitch + lane * EL + e] = o[h][e];
+    }
+};
+
+template <int DP, int STAGES>
+sbt_status by_heads(sbt_context* ctx, const AttnParams& p, cudaStream_t stream) {
+    const int heads = p.group < p.chunk ? p.group : p.chunk;
+    if (heads <= 1) return sbt_attention_enqueue<Fma32<DP, 1>, STAGES>(ctx, p, stream);
+    if (heads <= 2) return sbt_attention_enqueue<Fma32<DP, 2>, STAGES>(ctx, p, stream);
+    if (heads <= 4) return sbt_attention_enqueue<Fma32<DP, 4>, STAGES>(ctx, p, stream);
+    return sbt_attention_enqueue<Fma32<DP, 8>, STAGES>(ctx, p, stream);
+}
+
+}  // namespace
+
+sbt_status sbt_attention_f32(sbt_context* ctx, const AttnParams& p, cudaStream_t stream) {
+    if (p.head_dim <= 64) return by_heads<64, 4>(ctx, p, stream);
+    if (p.head_dim <= 128) return by_heads<128, 2>(ctx, p, stream);
+    return by_heads<256, 2>(ctx, p, stream);
+}

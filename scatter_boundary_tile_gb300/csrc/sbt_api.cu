@@ -58,20 +58,6 @@ sbt_status sbt_after_launch(sbt_context* ctx, const char* what) {
     return SBT_OK;
 }
 
-#define SBT_REQUIRE(cond, msg)                                          \
-    do {                                                                \
-        if (!(cond)) return sbt_fail(SBT_ERR_INVALID_ARG, (msg));       \
-    } while (0)
-
-// Every array starts on a multiple of its element size (int32 indices and
-// cu_seqlens on 4 bytes): the kernels' element accesses are naturally aligned,
-// so a pointer that is not is refused here, before anything touches the device.
-#define SBT_REQUIRE_ALIGNED(ptr, bytes, msg)                                                    \
-    do {                                                                                        \
-        if ((reinterpret_cast<uintptr_t>(ptr) % (uintptr_t)(bytes)) != 0)                       \
-            return sbt_fail(SBT_ERR_ALIGNMENT, (msg));                                          \
-    } while (0)
-
 extern "C" {
 
 const char* sbt_last_error_message(void) { return t_last_error.c_str(); }

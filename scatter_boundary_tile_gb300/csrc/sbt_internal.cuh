@@ -37,6 +37,20 @@ sbt_status sbt_cuda_check(cudaError_t e, const char* what);
 // Makes ctx->device current.
 sbt_status sbt_use_device(sbt_context* ctx);
 
+#define SBT_REQUIRE(cond, msg)                                          \
+    do {                                                                \
+        if (!(cond)) return sbt_fail(SBT_ERR_INVALID_ARG, (msg));       \
+    } while (0)
+
+// Every array starts on a multiple of its element size (int32 indices and
+// cu_seqlens on 4 bytes): the kernels' element accesses are naturally aligned,
+// so a pointer that is not is refused here, before anything touches the device.
+#define SBT_REQUIRE_ALIGNED(ptr, bytes, msg)                                                    \
+    do {                                                                                        \
+        if ((reinterpret_cast<uintptr_t>(ptr) % (uintptr_t)(bytes)) != 0)                       \
+            return sbt_fail(SBT_ERR_ALIGNMENT, (msg));                                          \
+    } while (0)
+
 inline int sbt_dtype_size(sbt_dtype t) {
     switch (t) {
         case SBT_F32: return 4;
@@ -154,6 +168,47 @@ sbt_status sbt_launch_scatter_bulk(sbt_context* ctx, int es, void* dst, int64_t 
                                    const int32_t* idx, int64_t n_idx, int64_t row_offset, int64_t col_offset,
                                    const void* src, int64_t ld_src, int32_t tile_c, const uint8_t* mask,
                                    int64_t ld_mask, cudaStream_t stream);
+
+// Operators of the paged cache (k_paged_attention*.cu, k_norm_rope.cu, k_pages.cu).
+// Rows of heads: [tokens][heads][head_dim], element strides.
+struct SbtHeadRows {
+    const void* p;
+    int64_t ld, ldh;
+};
+sbt_status sbt_launch_paged_attention(sbt_context* ctx, sbt_dtype dtype, const SbtHeadRows& q, int32_t batch,
+                                      int32_t q_heads, const sbt_kv_cache* cache, const sbt_page_map* map,
+                                      const int32_t* seq, float scale, int32_t window, const SbtHeadRows& out,
+                                      float* lse, void* workspace, cudaStream_t stream);
+size_t sbt_paged_attention_workspace_bytes(const sbt_context* ctx, int32_t q_heads, int32_t kv_heads,
+                                           int32_t head_dim);
+sbt_status sbt_launch_norm_rope(sbt_context* ctx, sbt_dtype dtype, const SbtHeadRows& q, const SbtHeadRows& k,
+                                const SbtHeadRows& v, const SbtHeadRows& q_out, const SbtHeadRows& k_out,
+                                int64_t tokens, int32_t q_heads, int32_t k_heads, int32_t D, const int32_t* pos,
+                                const sbt_rope* rope, const void* wq, const void* wk, float eps,
+                                const sbt_kv_cache* cache, const sbt_page_map* map, const int32_t* seq,
+                                cudaStream_t stream);
+int sbt_norm_rope_bwd_blocks(const sbt_context* ctx);
+sbt_status sbt_launch_norm_rope_bwd(sbt_context* ctx, sbt_dtype dtype, const SbtHeadRows& gq, const SbtHeadRows& gk,
+                                    const SbtHeadRows& q, const SbtHeadRows& k, const SbtHeadRows& dq,
+                                    const SbtHeadRows& dk, int64_t tokens, int32_t q_heads, int32_t k_heads, int32_t D,
+                                    const int32_t* pos, const sbt_rope* rope, const void* wq, const void* wk,
+                                    float eps, float* dwq, float* dwk, void* workspace, cudaStream_t stream);
+sbt_status sbt_launch_rope_table(sbt_context* ctx, float* table, int64_t n_pos, int32_t rot, double base, int scaling,
+                                 double factor, int64_t orig, double low, double high, double amplitude,
+                                 cudaStream_t stream);
+size_t sbt_pages_workspace_bytes(int32_t n_seq, int64_t n_pages);
+sbt_status sbt_launch_pages_copy(sbt_context* ctx, const sbt_page_pool* pools, int32_t n_pools, int64_t n_pages,
+                                 const int32_t* src, const int32_t* dst, int64_t n, cudaStream_t stream);
+sbt_status sbt_launch_pages_free(sbt_context* ctx, const sbt_page_map* map, const int32_t* seqs, const int32_t* keep,
+                                 int32_t n, cudaStream_t stream);
+sbt_status sbt_launch_pages_reserve(sbt_context* ctx, const sbt_page_map* map, const sbt_page_pool* pools,
+                                    int32_t n_pools, const int32_t* target, void* workspace, cudaStream_t stream);
+sbt_status sbt_launch_pages_fork(sbt_context* ctx, const sbt_page_map* map, const sbt_page_pool* pools,
+                                 int32_t n_pools, const int32_t* from, const int32_t* to, int32_t n, void* workspace,
+                                 cudaStream_t stream);
+sbt_status sbt_launch_pages_compact(sbt_context* ctx, const sbt_page_map* map, const sbt_page_pool* pools,
+                                    int32_t n_pools, int32_t* table_out, int64_t ld_out, int32_t* refs_out,
+                                    int32_t* page_to, int32_t* n_live, void* workspace, cudaStream_t stream);
 
 // Checks the launch that was just enqueued and counts it.
 sbt_status sbt_after_launch(sbt_context* ctx, const char* what);
