@@ -85,6 +85,8 @@ _lock = threading.Lock()
 def load_library(path: str = LIB_PATH):
     """Load libsbt.so and declare its signatures (no CUDA call is made)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -162,7 +164,8 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current device's current stream, without building the Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

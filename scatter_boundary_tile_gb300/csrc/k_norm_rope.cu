@@ -19,6 +19,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "sbt_internal.cuh"
@@ -26,7 +27,13 @@
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+// Forward: heads per group, and blocks per SM the registers are held to.
+constexpr int kFwdHeads = 4, kFwdBlocks = 7;
+// Rows per SM and group of lanes from which a group takes several heads.
+constexpr int kManyRows = 16;
+// Gradient: heads per item, stages of the ring.
+constexpr int kBwdHeads = 2, kStages = 2;
 constexpr int kMaxScalarPairs = 8;  // pairs per lane of the element path: 512 elements
 
 enum Kind { kF32 = 0, kBF16 = 1, kF16 = 2 };
@@ -53,15 +60,17 @@ template <> struct Num<kF16> {
 
 template <int KIND>
 __device__ __forceinline__ void unpack(const uint4& v, float* x) {
-    if (Num<KIND>::V == 4) {
-        x[0] = Num<KIND>::get((typename Num<KIND>::T)v.x), x[1] = Num<KIND>::get((typename Num<KIND>::T)v.y);
-        x[2] = Num<KIND>::get((typename Num<KIND>::T)v.z), x[3] = Num<KIND>::get((typename Num<KIND>::T)v.w);
-    } else {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[(2 * i) % Num<KIND>::V] = Num<KIND>::get((typename Num<KIND>::T)(w[i] & 0xFFFFu));
-            x[(2 * i + 1) % Num<KIND>::V] = Num<KIND>::get((typename Num<KIND>::T)(w[i] >> 16));
+    for (int i = 0; i < 4; ++i) {
+        if (KIND == kF32) {
+            x[i] = __uint_as_float(w[i]);
+        } else if (KIND == kBF16) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            x[2 * i] = f.x, x[2 * i + 1] = f.y;
         }
     }
 }
@@ -70,10 +79,17 @@ template <int KIND>
 __device__ __forceinline__ uint4 pack(const float* x) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = Num<KIND>::V == 4 ? (uint32_t)Num<KIND>::put(x[i % Num<KIND>::V])
-                                 : (uint32_t)Num<KIND>::put(x[(2 * i) % Num<KIND>::V]) |
-                                       (uint32_t)Num<KIND>::put(x[(2 * i + 1) % Num<KIND>::V]) << 16;
+    for (int i = 0; i < 4; ++i) {
+        if (KIND == kF32) {
+            w[i] = __float_as_uint(x[i]);
+        } else if (KIND == kBF16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -115,48 +131,61 @@ __device__ __forceinline__ int64_t cache_slot(const FwdParams& p, int64_t t, int
     return page * p.ld_page + (int64_t)(pos - (int32_t)(j * p.page_size.d)) * p.ld_slot;
 }
 
-// The two vectors of lane j of a row: element offsets (-1: none) and the pair
-// the first of them starts with in the table (-1: not turned).
+// The two vectors of lane j of a row: element offsets (-1: none), and for the
+// first V / 2 and the last V / 2 of the lane's V pairs where they start in the
+// table (-1: not turned).  Neighbouring lanes hold neighbouring vectors: two
+// 16-byte halves of one 32-byte sector in different instructions would cost
+// twice the L2 traffic (measured on the fp16 interleaved append: 179 us so).
 struct Place {
-    int a, b, pair;
+    int a, b, pair[2];
 };
 template <int V, bool INTER>
-__device__ __forceinline__ Place place_of(int j, int D, int rot) {
+__device__ __forceinline__ Place place_of(int j, int lanes, int D, int rot) {
     Place q;
-    if (INTER) {
-        q.a = 2 * j * V < D ? 2 * j * V : -1;
-        q.b = (2 * j + 1) * V < D ? (2 * j + 1) * V : -1;
-        q.pair = q.a >= 0 && q.a < rot ? q.a / 2 : -1;
+    if (INTER) {  // vectors j and j + lanes, V / 2 pairs in each
+        q.a = j * V < D ? j * V : -1;
+        q.b = (lanes + j) * V < D ? (lanes + j) * V : -1;
+        q.pair[0] = q.a >= 0 && q.a < rot ? q.a / 2 : -1;
+        q.pair[1] = q.b >= 0 && q.b < rot ? q.b / 2 : -1;
         return q;
     }
     const int np = rot / (2 * V);
-    if (j < np) {
+    if (j < np) {  // pairs jV .. jV + V - 1, one element in each vector
         q.a = j * V;
         q.b = rot / 2 + j * V;
-        q.pair = j * V;
-    } else {
-        const int d = rot + 2 * (j - np) * V;
-        q.a = d < D ? d : -1;
-        q.b = d + V < D ? d + V : -1;
-        q.pair = -1;
+        q.pair[0] = j * V;
+        q.pair[1] = j * V + V / 2;
+    } else {       // what is not turned: its first half over the lanes left, then the second
+        const int left = (D - rot) / V, half = (left + 1) / 2, i = j - np;
+        q.a = i < half ? rot + i * V : -1;
+        q.b = i < half && half + i < left ? rot + (half + i) * V : -1;
+        q.pair[0] = q.pair[1] = -1;
     }
     return q;
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_l1(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // cos and sin of this lane's V pairs.
-template <int V, bool INTER>
-__device__ __forceinline__ void angles(const float2* row, const Place& q, int rot, float* cs, float* sn) {
+template <int V>
+__device__ __forceinline__ void angles(const float2* row, const Place& q, float* cs, float* sn) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) cs[i] = 1.f, sn[i] = 0.f;
-    if (q.pair < 0) return;
-    // interleaved: a vector holds V / 2 pairs, and the second vector may lie past rot_dim
-    const int n = INTER && (q.b < 0 || q.b >= rot) ? V / 2 : V;
-#pragma unroll
-    for (int i = 0; i < V; i += 2)
-        if (i < n) {
-            const float4 c = __ldg(reinterpret_cast<const float4*>(row + q.pair + i));
-            cs[i] = c.x, sn[i] = c.y, cs[i + 1] = c.z, sn[i + 1] = c.w;
-        }
+    for (int i = 0; i < V / 2; ++i) {
+        const int first = q.pair[i / (V / 4)];
+        float4 c = make_float4(1.f, 0.f, 1.f, 0.f);
+        if (first >= 0) c = __ldg(reinterpret_cast<const float4*>(row + first + 2 * (i % (V / 4))));
+        cs[2 * i] = c.x, sn[2 * i] = c.y, cs[2 * i + 1] = c.z, sn[2 * i + 1] = c.w;
+    }
 }
 
 // Turns the lane's 2 V elements (x[0..V) of vector a, x[V..2V) of vector b); sign -1: the transpose.
@@ -178,74 +207,74 @@ __device__ __forceinline__ float lanes_sum(float x) {
     return x;
 }
 
-// HB heads per group: grid (head blocks, token blocks).
+// HB heads of one kind of a token per group: grid (head blocks, token blocks).
 template <int KIND, bool INTER, int LPR, int HB>
-__global__ void __launch_bounds__(kThreads) k_norm_rope(const FwdParams p) {
+__global__ void __launch_bounds__(kThreads, HB == 1 ? 1 : kFwdBlocks) k_norm_rope(const FwdParams p) {
     constexpr int V = Num<KIND>::V, ES = 16 / V, GROUPS = kThreads / LPR;
     const int j = threadIdx.x % LPR, g = threadIdx.x / LPR;
-    const Place at = place_of<V, INTER>(j, p.D, p.rot);
-    const int total = p.heads[0] + p.heads[1] + p.heads[2];
-    const int h0 = blockIdx.x * HB;
+    const Place at = place_of<V, INTER>(j, LPR, p.D, p.rot);
+    const int hq = (p.heads[0] + HB - 1) / HB, hk = (p.heads[1] + HB - 1) / HB;
+    const int kind = (int)blockIdx.x < hq ? 0 : (int)blockIdx.x < hq + hk ? 1 : 2;
+    const int h0 = (blockIdx.x - (kind >= 1 ? hq : 0) - (kind == 2 ? hk : 0)) * HB;
+    const int rows = p.heads[kind] - h0;  // min(rows, HB) of them here
+    const Rows in = p.x[kind];
+    char* const cache = kind >= 1 ? p.cache[kind - 1] : nullptr;
+    const char* const wp = kind < 2 ? p.w[kind] : nullptr;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
     for (int64_t t0 = (int64_t)blockIdx.y * GROUPS; t0 < p.tokens; t0 += (int64_t)gridDim.y * GROUPS) {
         const int64_t t = t0 + g;
         const bool on = t < p.tokens;
+        const int32_t pos = on ? __ldg(p.pos + t) : -1;
+        const char* x = in.at(on ? t : 0, h0);
         uint4 va[HB], vb[HB];
-        int kind[HB], head[HB];
 #pragma unroll
         for (int i = 0; i < HB; ++i) {
-            int h = h0 + i;
-            kind[i] = h >= total ? -1 : h < p.heads[0] ? 0 : h < p.heads[0] + p.heads[1] ? 1 : 2;
-            head[i] = h - (kind[i] >= 1 ? p.heads[0] : 0) - (kind[i] == 2 ? p.heads[1] : 0);
-            va[i] = vb[i] = make_uint4(0, 0, 0, 0);
-            if (kind[i] >= 0 && on) {
-                const char* x = p.x[kind[i]].at(t, head[i]);
-                if (at.a >= 0) va[i] = *reinterpret_cast<const uint4*>(x + at.a * ES);
-                if (at.b >= 0) vb[i] = *reinterpret_cast<const uint4*>(x + at.b * ES);
-            }
+            va[i] = on && i < rows && at.a >= 0 ? *reinterpret_cast<const uint4*>(x + i * in.ldh + at.a * ES) : zero;
+            vb[i] = on && i < rows && at.b >= 0 ? *reinterpret_cast<const uint4*>(x + i * in.ldh + at.b * ES) : zero;
         }
-        const int32_t pos = on ? __ldg(p.pos + t) : -1;
         const bool real = pos >= 0 && (p.rot == 0 || pos < p.n_pos);
         int64_t slot = -1;
-        if (p.cache[0] && h0 + HB > p.heads[0] && real) slot = cache_slot(p, t, pos);
+        if (cache && real) slot = cache_slot(p, t, pos);
+        char* y = on && kind < 2 && p.y[kind].p ? const_cast<char*>(p.y[kind].at(t, h0)) : nullptr;
+        const int64_t ldy = kind < 2 ? p.y[kind].ldh : 0;
+        char* kept = slot >= 0 ? cache + slot + h0 * p.ld_head : nullptr;
         float cs[V], sn[V];
-        if (p.rot && real) {
-            angles<V, INTER>(p.table + (int64_t)pos * (p.rot / 2), at, p.rot, cs, sn);
-        } else {
+        if (kind < 2) {  // the same for the whole block
+            if (p.rot && real) {
+                angles<V>(p.table + (int64_t)pos * (p.rot / 2), at, cs, sn);
+            } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) cs[i] = 1.f, sn[i] = 0.f;
+                for (int i = 0; i < V; ++i) cs[i] = 1.f, sn[i] = 0.f;
+            }
         }
 #pragma unroll
         for (int i = 0; i < HB; ++i) {
-            if (kind[i] < 0) break;  // the same for the whole block
-            if (kind[i] < 2) {
-                float x[2 * V];
-                unpack<KIND>(va[i], x);
-                unpack<KIND>(vb[i], x + V);
-                if (p.w[kind[i]]) {
-                    float ss = 0.f;
+            uint4 a = va[i], b = vb[i];
+            if (kind < 2) {
+                float f[2 * V];
+                unpack<KIND>(a, f);
+                unpack<KIND>(b, f + V);
+                if (wp) {
+                    float ss = 0.f, w[2 * V];
 #pragma unroll
-                    for (int e = 0; e < 2 * V; ++e) ss += x[e] * x[e];
-                    const float r = 1.f / sqrtf(lanes_sum<LPR>(ss) / (float)p.D + p.eps);
-                    float w[2 * V];
-                    const uint4 one = make_uint4(0, 0, 0, 0);
-                    unpack<KIND>(at.a >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.w[kind[i]] + at.a * ES)) : one, w);
-                    unpack<KIND>(at.b >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.w[kind[i]] + at.b * ES)) : one, w + V);
+                    for (int e = 0; e < 2 * V; ++e) ss += f[e] * f[e];
+                    const float r = rsqrtf(lanes_sum<LPR>(ss) / (float)p.D + p.eps);
+                    unpack<KIND>(at.a >= 0 ? __ldg(reinterpret_cast<const uint4*>(wp + at.a * ES)) : zero, w);
+                    unpack<KIND>(at.b >= 0 ? __ldg(reinterpret_cast<const uint4*>(wp + at.b * ES)) : zero, w + V);
 #pragma unroll
-                    for (int e = 0; e < 2 * V; ++e) x[e] = x[e] * r * w[e];
+                    for (int e = 0; e < 2 * V; ++e) f[e] = f[e] * r * w[e];
                 }
-                turn<V, INTER>(x, cs, sn, 1.f);
-                va[i] = real ? pack<KIND>(x) : make_uint4(0, 0, 0, 0);
-                vb[i] = real ? pack<KIND>(x + V) : make_uint4(0, 0, 0, 0);
-                if (p.y[kind[i]].p && on) {
-                    char* y = const_cast<char*>(p.y[kind[i]].at(t, head[i]));
-                    if (at.a >= 0) *reinterpret_cast<uint4*>(y + at.a * ES) = va[i];
-                    if (at.b >= 0) *reinterpret_cast<uint4*>(y + at.b * ES) = vb[i];
-                }
+                turn<V, INTER>(f, cs, sn, 1.f);
+                a = real ? pack<KIND>(f) : zero;
+                b = real ? pack<KIND>(f + V) : zero;
             }
-            if (kind[i] >= 1 && slot >= 0) {
-                char* y = p.cache[kind[i] - 1] + slot + head[i] * p.ld_head;
-                if (at.a >= 0) *reinterpret_cast<uint4*>(y + at.a * ES) = va[i];
-                if (at.b >= 0) *reinterpret_cast<uint4*>(y + at.b * ES) = vb[i];
+            if (i < rows && y) {
+                if (at.a >= 0) *reinterpret_cast<uint4*>(y + i * ldy + at.a * ES) = a;
+                if (at.b >= 0) *reinterpret_cast<uint4*>(y + i * ldy + at.b * ES) = b;
+            }
+            if (i < rows && kept) {
+                if (at.a >= 0) *reinterpret_cast<uint4*>(kept + i * p.ld_head + at.a * ES) = a;
+                if (at.b >= 0) *reinterpret_cast<uint4*>(kept + i * p.ld_head + at.b * ES) = b;
             }
         }
     }
@@ -340,19 +369,45 @@ struct BwdParams {
     float* dw[2];
 };
 
+// Items of the vector kernel: HB heads of one token.  A group of
+// LPR lanes walks the items with a fixed stride, so that the place of the next
+// one follows by additions.
+struct Item {
+    int64_t t;
+    int32_t hb;
+};
+__device__ __forceinline__ Item item_at(int64_t i, int32_t hblocks) {
+    Item x;
+    x.t = i / hblocks;
+    x.hb = (int32_t)(i - x.t * hblocks);
+    return x;
+}
+__device__ __forceinline__ void advance(Item& x, const Item& step, int32_t hblocks) {
+    x.t += step.t;
+    x.hb += step.hb;
+    if (x.hb >= hblocks) {
+        x.hb -= hblocks;
+        ++x.t;
+    }
+}
+
 // One block takes head rows of the queries or of the keys only, so one set of
 // sums for dw stays in registers; the blocks' sums go to the workspace and are
 // added in block order by k_norm_rope_dw: no atomics, the same bits every run.
-template <int KIND, bool INTER, int LPR, int HB>
+template <int KIND, bool INTER, int LPR, int HB, int STAGES>
 __global__ void __launch_bounds__(kThreads) k_norm_rope_bwd(const BwdParams p) {
-    constexpr int V = Num<KIND>::V, ES = 16 / V, GROUPS = kThreads / LPR;
-    extern __shared__ float s_dw[];  // [GROUPS][LPR * 2 V]
+    constexpr int V = Num<KIND>::V, ES = 16 / V, GROUPS = kThreads / LPR, AV = V / 2;
+    constexpr int VECS = 4 * HB + AV;
+    extern __shared__ __align__(16) uint8_t smem[];  // [STAGES][VECS][kThreads] vectors, positions; then the sums
+    uint4* const ring = reinterpret_cast<uint4*>(smem) + threadIdx.x;
+    int32_t* const s_pos = reinterpret_cast<int32_t*>(smem + (size_t)STAGES * VECS * kThreads * 16) + threadIdx.x;
+    float* const s_dw = reinterpret_cast<float*>(smem);  // [GROUPS][LPR * 2 V], after the last item
+    const uint32_t ring_u32 = sbt_ptx::smem_u32(ring);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int j = threadIdx.x % LPR, g = threadIdx.x / LPR;
-    const Place at = place_of<V, INTER>(j, p.D, p.rot);
+    const Place at = place_of<V, INTER>(j, LPR, p.D, p.rot);
     const int kind = blockIdx.x >= p.blocks[0];
-    const int first = kind ? blockIdx.x - p.blocks[0] : blockIdx.x;
-    const int heads = p.heads[kind], hblocks = (heads + HB - 1) / HB;
+    const int32_t heads = p.heads[kind], hblocks = (heads + HB - 1) / HB;
     const char* const wp = p.w[kind];
     float w[2 * V], dw[2 * V];
 #pragma unroll
@@ -362,47 +417,76 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_bwd(const BwdParams p) {
         unpack<KIND>(at.a >= 0 ? __ldg(reinterpret_cast<const uint4*>(wp + at.a * ES)) : zero, w);
         unpack<KIND>(at.b >= 0 ? __ldg(reinterpret_cast<const uint4*>(wp + at.b * ES)) : zero, w + V);
     }
-    // items: (token, head block), tokens slowest
+    const float inv_d = 1.f / (float)p.D;
     const int64_t items = p.tokens * hblocks;
-    for (int64_t i0 = (int64_t)first * GROUPS; i0 < items; i0 += (int64_t)p.blocks[kind] * GROUPS) {
-        const int64_t it = i0 + g;
-        const bool on = it < items;
-        const int64_t t = on ? it / hblocks : 0;
-        const int h0 = on ? (int)(it - t * hblocks) * HB : 0;
-        uint4 ga[HB], gb[HB], xa[HB], xb[HB];
+    const int64_t first = (int64_t)(kind ? blockIdx.x - p.blocks[0] : blockIdx.x) * GROUPS;
+    const int64_t stride = (int64_t)p.blocks[kind] * GROUPS;
+    const int64_t steps = first < items ? (items - first - 1) / stride + 1 : 0;
+    const Item step = item_at(stride, hblocks);
+
+    Item in = item_at(first + g, hblocks);  // the next item to load
+    int32_t in_pos = in.t < p.tokens ? __ldg(p.pos + in.t) : -1;
+    auto load = [&](int stage) {
+        const uint32_t dst = ring_u32 + stage * VECS * kThreads * 16;
+        if (in.t < p.tokens) {
+            const int32_t h0 = in.hb * HB;
+            const char* gr = p.g[kind].at(in.t, h0);
+            const char* xr = p.x[kind].at(in.t, h0);
 #pragma unroll
-        for (int i = 0; i < HB; ++i) {
-            ga[i] = gb[i] = xa[i] = xb[i] = make_uint4(0, 0, 0, 0);
-            if (on && h0 + i < heads) {
-                const char* gr = p.g[kind].at(t, h0 + i);
-                if (at.a >= 0) ga[i] = *reinterpret_cast<const uint4*>(gr + at.a * ES);
-                if (at.b >= 0) gb[i] = *reinterpret_cast<const uint4*>(gr + at.b * ES);
-                if (wp) {
-                    const char* xr = p.x[kind].at(t, h0 + i);
-                    if (at.a >= 0) xa[i] = *reinterpret_cast<const uint4*>(xr + at.a * ES);
-                    if (at.b >= 0) xb[i] = *reinterpret_cast<const uint4*>(xr + at.b * ES);
+            for (int i = 0; i < HB; ++i)
+                if (h0 + i < heads) {
+                    const int64_t og = i * p.g[kind].ldh, ox = i * p.x[kind].ldh;
+                    if (at.a >= 0) copy16(dst + (4 * i) * kThreads * 16, gr + og + at.a * ES);
+                    if (at.b >= 0) copy16(dst + (4 * i + 1) * kThreads * 16, gr + og + at.b * ES);
+                    if (wp && at.a >= 0) copy16(dst + (4 * i + 2) * kThreads * 16, xr + ox + at.a * ES);
+                    if (wp && at.b >= 0) copy16(dst + (4 * i + 3) * kThreads * 16, xr + ox + at.b * ES);
+                }
+            if (in_pos >= 0 && in_pos < p.n_pos) {  // read only where something is turned
+                const float2* row = p.table + (int64_t)in_pos * (p.rot / 2);
+#pragma unroll
+                for (int i = 0; i < AV; ++i) {
+                    const int pair = at.pair[i / (AV / 2)];
+                    if (pair >= 0) copy16_l1(dst + (4 * HB + i) * kThreads * 16, row + pair + 2 * (i % (AV / 2)));
                 }
             }
         }
-        const int32_t pos = on ? __ldg(p.pos + t) : -1;
-        const bool real = pos >= 0 && (p.rot == 0 || pos < p.n_pos);
+        copy_commit();
+        s_pos[stage * kThreads] = in_pos;
+        advance(in, step, hblocks);
+        if (in.t < p.tokens) in_pos = __ldg(p.pos + in.t);
+    };
+#pragma unroll 1
+    for (int s = 0; s < STAGES - 1; ++s) load(s);
+
+    Item it = item_at(first + g, hblocks);
+    int stage = 0;
+#pragma unroll 1
+    for (int64_t n = 0; n < steps; ++n) {
+        copy_wait<STAGES - 2>();
+        load(stage == 0 ? STAGES - 1 : stage - 1);
+        const uint4* const v = ring + stage * VECS * kThreads;
+        const bool on = it.t < p.tokens;
+        const int32_t h0 = it.hb * HB, pos = s_pos[stage * kThreads];
+        const bool real = on && pos >= 0 && (p.rot == 0 || pos < p.n_pos);
+        const uint4 zero = make_uint4(0, 0, 0, 0), one = make_uint4(0x3F800000u, 0u, 0x3F800000u, 0u);
         float cs[V], sn[V];
-        if (p.rot && real) {
-            angles<V, INTER>(p.table + (int64_t)pos * (p.rot / 2), at, p.rot, cs, sn);
-        } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) cs[i] = 1.f, sn[i] = 0.f;
+        for (int i = 0; i < AV; ++i) {
+            const uint4 c = real && at.pair[i / (AV / 2)] >= 0 ? v[(4 * HB + i) * kThreads] : one;
+            cs[2 * i] = __uint_as_float(c.x), sn[2 * i] = __uint_as_float(c.y);
+            cs[2 * i + 1] = __uint_as_float(c.z), sn[2 * i + 1] = __uint_as_float(c.w);
         }
 #pragma unroll
         for (int i = 0; i < HB; ++i) {
+            const bool row = on && h0 + i < heads;
             float u[2 * V];
-            unpack<KIND>(ga[i], u);
-            unpack<KIND>(gb[i], u + V);
+            unpack<KIND>(row && real && at.a >= 0 ? v[(4 * i) * kThreads] : zero, u);
+            unpack<KIND>(row && real && at.b >= 0 ? v[(4 * i + 1) * kThreads] : zero, u + V);
             turn<V, INTER>(u, cs, sn, -1.f);
             if (wp) {
                 float x[2 * V], ss = 0.f, dot = 0.f;
-                unpack<KIND>(xa[i], x);
-                unpack<KIND>(xb[i], x + V);
+                unpack<KIND>(row && real && at.a >= 0 ? v[(4 * i + 2) * kThreads] : zero, x);
+                unpack<KIND>(row && real && at.b >= 0 ? v[(4 * i + 3) * kThreads] : zero, x + V);
 #pragma unroll
                 for (int e = 0; e < 2 * V; ++e) {
                     ss += x[e] * x[e];
@@ -410,28 +494,31 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_bwd(const BwdParams p) {
                 }
                 ss = lanes_sum<LPR>(ss);
                 dot = lanes_sum<LPR>(dot);
-                const float r = 1.f / sqrtf(ss / (float)p.D + p.eps);
-                const float c = dot / (float)p.D * r * r;
+                const float r = row && real ? rsqrtf(ss * inv_d + p.eps) : 0.f;
+                const float c = dot * inv_d * r * r;
 #pragma unroll
                 for (int e = 0; e < 2 * V; ++e) {
-                    if (real) dw[e] += u[e] * (x[e] * r);
+                    dw[e] += u[e] * (x[e] * r);  // nothing for rows of padding: u, x and r are zero
                     u[e] = r * (u[e] * w[e] - x[e] * c);
                 }
             }
-            if (on && h0 + i < heads) {
-                char* y = const_cast<char*>(p.dx[kind].at(t, h0 + i));
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-                if (at.a >= 0) *reinterpret_cast<uint4*>(y + at.a * ES) = real ? pack<KIND>(u) : zero;
-                if (at.b >= 0) *reinterpret_cast<uint4*>(y + at.b * ES) = real ? pack<KIND>(u + V) : zero;
+            if (row) {
+                char* y = const_cast<char*>(p.dx[kind].at(it.t, h0 + i));
+                if (at.a >= 0) *reinterpret_cast<uint4*>(y + at.a * ES) = pack<KIND>(u);
+                if (at.b >= 0) *reinterpret_cast<uint4*>(y + at.b * ES) = pack<KIND>(u + V);
             }
         }
+        advance(it, step, hblocks);
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
+    copy_wait<0>();
     if (!wp) return;
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < 2 * V; ++e) s_dw[(g * LPR + j) * 2 * V + e] = dw[e];
     __syncthreads();
     for (int c = threadIdx.x; c < LPR * 2 * V; c += kThreads) {
-        const Place q = place_of<V, INTER>(c / (2 * V), p.D, p.rot);
+        const Place q = place_of<V, INTER>(c / (2 * V), LPR, p.D, p.rot);
         const int e = c % (2 * V), d = e < V ? q.a : q.b;
         if (d < 0) continue;
         float sum = 0.f;
@@ -602,23 +689,42 @@ bool sizes_ok(int D, int rot, int V, bool inter) {
     return D % V == 0 && (inter ? rot % V == 0 : rot % (2 * V) == 0) && lanes_per_row(D, rot, V, inter) <= 32;
 }
 
-template <int KIND, bool INTER, int LPR>
-void fwd_launch(const FwdParams& p, int sms, cudaStream_t stream) {
-    constexpr int GROUPS = kThreads / LPR;
-    const int total = p.heads[0] + p.heads[1] + p.heads[2];
-    int64_t ty = sbt_cdiv(p.tokens, GROUPS);
-    if (ty > 65535) ty = 65535;
-    // Four heads per group once that leaves two blocks for every SM; one head per group below.
-    if (ty * sbt_cdiv(total, 4) >= 2 * sms)
-        k_norm_rope<KIND, INTER, LPR, 4><<<dim3((unsigned)sbt_cdiv(total, 4), (unsigned)ty), kThreads, 0, stream>>>(p);
-    else
-        k_norm_rope<KIND, INTER, LPR, 1><<<dim3((unsigned)total, (unsigned)ty), kThreads, 0, stream>>>(p);
+
+// Splits `most` blocks over the kinds in proportion to their rows, none without
+// work and none more than its items need.
+template <int N>
+void split_blocks(int64_t most, const int64_t (&need)[N], int32_t (&blocks)[N]) {
+    int64_t total = 0, left = most;
+    for (int i = 0; i < N; ++i) total += need[i];
+    for (int i = N - 1; i >= 0; --i) {
+        int64_t b = need[i];
+        if (total > most) b = i ? std::max<int64_t>(1, most * need[i] / total) : left;
+        blocks[i] = (int32_t)(need[i] ? std::min(b, need[i]) : 0);
+        left -= blocks[i];
+    }
 }
 
 template <int KIND, bool INTER, int LPR>
-void bwd_launch(const BwdParams& p, cudaStream_t stream) {
-    const size_t smem = (size_t)kThreads * 2 * Num<KIND>::V * sizeof(float);
-    k_norm_rope_bwd<KIND, INTER, LPR, 2><<<p.blocks[0] + p.blocks[1], kThreads, smem, stream>>>(p);
+void fwd_launch(const sbt_context* ctx, const FwdParams& p, cudaStream_t stream) {
+    constexpr int GROUPS = kThreads / LPR, HB = kFwdHeads;
+    const int64_t total = p.heads[0] + p.heads[1] + p.heads[2];
+    const unsigned ty = (unsigned)std::min<int64_t>(sbt_cdiv(p.tokens, GROUPS), 65535);
+    if (p.tokens * total >= (int64_t)ctx->sm_count * kManyRows * GROUPS) {
+        const int64_t hb = sbt_cdiv(p.heads[0], HB) + sbt_cdiv(p.heads[1], HB) + sbt_cdiv(p.heads[2], HB);
+        k_norm_rope<KIND, INTER, LPR, HB><<<dim3((unsigned)hb, ty), kThreads, 0, stream>>>(p);
+    } else {
+        k_norm_rope<KIND, INTER, LPR, 1><<<dim3((unsigned)total, ty), kThreads, 0, stream>>>(p);
+    }
+}
+
+template <int KIND, bool INTER, int LPR>
+void bwd_launch(const sbt_context* ctx, const BwdParams& p, cudaStream_t stream) {
+    constexpr int V = Num<KIND>::V;
+    const size_t smem = std::max((size_t)kStages * kThreads * ((4 * kBwdHeads + V / 2) * 16 + 4),
+                                 (size_t)kThreads * 2 * V * sizeof(float));
+    constexpr auto kern = k_norm_rope_bwd<KIND, INTER, LPR, kBwdHeads, kStages>;
+    sbt_resident_blocks<kern>(ctx, kThreads, smem);
+    kern<<<p.blocks[0] + p.blocks[1], kThreads, smem, stream>>>(p);
 }
 
 template <int KIND, bool INTER, class P, class F>
@@ -634,33 +740,33 @@ void by_lanes(int lpr, const P& p, F f) {
 }
 
 template <int KIND>
-void fwd(const FwdParams& p, bool vec, int sms, cudaStream_t stream) {
+void fwd(const sbt_context* ctx, const FwdParams& p, bool vec, cudaStream_t stream) {
     constexpr int V = Num<KIND>::V;
     if (!vec) {
         const int64_t rows = p.tokens * (p.heads[0] + p.heads[1] + p.heads[2]);
-        const int64_t blocks = std::min<int64_t>(sbt_cdiv(rows, kThreads / 32), (int64_t)sms * 16);
+        const int64_t blocks = std::min<int64_t>(sbt_cdiv(rows, kThreads / 32), (int64_t)ctx->sm_count * 16);
         k_norm_rope_elems<KIND><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
     } else if (p.interleaved) {
         by_lanes<KIND, true>(lanes_per_row(p.D, p.rot, V, true), p,
-                             [&](auto n) { fwd_launch<KIND, true, decltype(n)::value>(p, sms, stream); });
+                             [&](auto n) { fwd_launch<KIND, true, decltype(n)::value>(ctx, p, stream); });
     } else {
         by_lanes<KIND, false>(lanes_per_row(p.D, p.rot, V, false), p,
-                              [&](auto n) { fwd_launch<KIND, false, decltype(n)::value>(p, sms, stream); });
+                              [&](auto n) { fwd_launch<KIND, false, decltype(n)::value>(ctx, p, stream); });
     }
 }
 
 template <int KIND>
-void bwd(const BwdParams& p, bool vec, cudaStream_t stream) {
+void bwd(const sbt_context* ctx, const BwdParams& p, bool vec, cudaStream_t stream) {
     constexpr int V = Num<KIND>::V;
     if (!vec) {
         k_norm_rope_bwd_elems<KIND><<<p.blocks[0] + p.blocks[1], kThreads, (kThreads / 32) * p.D * sizeof(float),
                                       stream>>>(p);
     } else if (p.interleaved) {
         by_lanes<KIND, true>(lanes_per_row(p.D, p.rot, V, true), p,
-                             [&](auto n) { bwd_launch<KIND, true, decltype(n)::value>(p, stream); });
+                             [&](auto n) { bwd_launch<KIND, true, decltype(n)::value>(ctx, p, stream); });
     } else {
         by_lanes<KIND, false>(lanes_per_row(p.D, p.rot, V, false), p,
-                              [&](auto n) { bwd_launch<KIND, false, decltype(n)::value>(p, stream); });
+                              [&](auto n) { bwd_launch<KIND, false, decltype(n)::value>(ctx, p, stream); });
     }
 }
 
@@ -702,9 +808,9 @@ sbt_status sbt_launch_norm_rope(sbt_context* ctx, sbt_dtype dtype, const SbtHead
               sbt_mul16(cache->ld_slot, es) && sbt_mul16(cache->ld_head, es);
     }
     switch (kind_of(dtype)) {
-        case kF32: fwd<kF32>(p, vec, ctx->sm_count, stream); break;
-        case kBF16: fwd<kBF16>(p, vec, ctx->sm_count, stream); break;
-        default: fwd<kF16>(p, vec, ctx->sm_count, stream); break;
+        case kF32: fwd<kF32>(ctx, p, vec, stream); break;
+        case kBF16: fwd<kBF16>(ctx, p, vec, stream); break;
+        default: fwd<kF16>(ctx, p, vec, stream); break;
     }
     return sbt_after_launch(ctx, "qk_norm_rope");
 }
@@ -735,23 +841,16 @@ sbt_status sbt_launch_norm_rope_bwd(sbt_context* ctx, sbt_dtype dtype, const Sbt
                      sbt_aligned16(wq) && sbt_aligned16(wk) && sbt_aligned16(p.table) && (p.rot / 2) % 2 == 0;
     // blocks in proportion to the head rows, none without work
     const int lpr = vec ? lanes_per_row(D, p.rot, V, p.interleaved) : 32;
-    const int64_t groups = kThreads / lpr, hb = vec ? 2 : 1;
-    const int64_t need_q = sbt_cdiv(tokens * sbt_cdiv(q_heads, hb), groups);
-    const int64_t need_k = sbt_cdiv(tokens * sbt_cdiv(k_heads, hb), groups);
-    const int64_t most = sbt_norm_rope_bwd_blocks(ctx);
-    int64_t bq = need_q, bk = need_k;
-    if (bq + bk > most) {
-        bk = k_heads ? std::max<int64_t>(1, most * k_heads / (q_heads + k_heads)) : 0;
-        bk = std::min(bk, need_k);
-        bq = q_heads ? std::min(need_q, most - bk) : 0;
-    }
-    p.blocks[0] = (int32_t)bq, p.blocks[1] = (int32_t)bk;
+    const int64_t groups = kThreads / lpr, hb = vec ? kBwdHeads : 1;
+    const int64_t need[2] = {sbt_cdiv(tokens * sbt_cdiv(q_heads, hb), groups),
+                             sbt_cdiv(tokens * sbt_cdiv(k_heads, hb), groups)};
+    split_blocks(sbt_norm_rope_bwd_blocks(ctx), need, p.blocks);
     sbt_status st = SBT_OK;
-    if (bq + bk > 0) {  // no rows: only the weights' gradients, which are zero
+    if (p.blocks[0] + p.blocks[1] > 0) {  // no rows: only the weights' gradients, which are zero
         switch (kind_of(dtype)) {
-            case kF32: bwd<kF32>(p, vec, stream); break;
-            case kBF16: bwd<kBF16>(p, vec, stream); break;
-            default: bwd<kF16>(p, vec, stream); break;
+            case kF32: bwd<kF32>(ctx, p, vec, stream); break;
+            case kBF16: bwd<kBF16>(ctx, p, vec, stream); break;
+            default: bwd<kF16>(ctx, p, vec, stream); break;
         }
         st = sbt_after_launch(ctx, "qk_norm_rope_backward");
     }

@@ -180,12 +180,14 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention(const AttnPara
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- units of all rows, and this block's range
-    int64_t total = 0;
-    for (int32_t b0 = 0; b0 < p.batch; b0 += kAttnThreads) {
-        const int32_t b = b0 + threadIdx.x;
-        total += b < p.batch ? row_of<UNIT>(p, b).units : 0;
-    }
-    {
+    const bool one_scan = p.batch <= kAttnThreads;  // every thread holds its own entry's units
+    int64_t total = 0, at = 0;
+    int32_t mine = 0;
+    if (one_scan) {
+        if ((int32_t)threadIdx.x < p.batch) mine = row_of<UNIT>(p, threadIdx.x).units;
+        at = block_scan(mine, &total, s_warp);
+    } else {
+        for (int32_t b = threadIdx.x; b < p.batch; b += kAttnThreads) total += row_of<UNIT>(p, b).units;
         int64_t sum;
         block_scan(total, &sum, s_warp);
         total = sum;
@@ -194,38 +196,47 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention(const AttnPara
     const int64_t G = U < gridDim.x ? U : gridDim.x;
     if (threadIdx.x == 0) p.desc[blockIdx.x].valid = 0;
 
-    // ---- empty rows: zeros, and a log-sum-exp of minus infinity
-    for (int32_t b = blockIdx.x; b < p.batch; b += gridDim.x) {
-        if (row_of<UNIT>(p, b).units != 0) continue;
-        for (int32_t i = threadIdx.x; i < p.q_heads * p.head_dim; i += kAttnThreads) {
-            const int32_t h = i / p.head_dim, d = i - h * p.head_dim;
-            reinterpret_cast<typename M::T*>(p.out)[b * p.ld_out + h * p.ld_oh + d] = M::from_float(0.f);
+    // rows that see nothing: zeros, and a log-sum-exp of minus infinity
+    auto empty_rows = [&]() {
+        for (int32_t b = blockIdx.x; b < p.batch; b += gridDim.x) {
+            if (row_of<UNIT>(p, b).units != 0) continue;
+            for (int32_t i = threadIdx.x; i < p.q_heads * p.head_dim; i += kAttnThreads) {
+                const int32_t h = i / p.head_dim, d = i - h * p.head_dim;
+                reinterpret_cast<typename M::T*>(p.out)[b * p.ld_out + h * p.ld_oh + d] = M::from_float(0.f);
+            }
+            if (p.lse)
+                for (int32_t h = threadIdx.x; h < p.q_heads; h += kAttnThreads)
+                    p.lse[(int64_t)b * p.q_heads + h] = -CUDART_INF_F;
         }
-        if (p.lse)
-            for (int32_t h = threadIdx.x; h < p.q_heads; h += kAttnThreads)
-                p.lse[(int64_t)b * p.q_heads + h] = -CUDART_INF_F;
+    };
+    if (blockIdx.x >= G) {
+        empty_rows();
+        return;
     }
-    if (blockIdx.x >= G) return;
 
     const int64_t u0 = range_start(blockIdx.x, U, G), u1 = range_start(blockIdx.x + 1, U, G);
 
     // ---- the sequence that holds unit u0
-    {
-        int64_t before = 0;
-        for (int32_t b0 = 0; b0 < p.batch; b0 += kAttnThreads) {
-            const int32_t b = b0 + threadIdx.x;
-            const int64_t mine = b < p.batch ? row_of<UNIT>(p, b).units : 0;
-            int64_t sum;
-            const int64_t at = before + block_scan(mine, &sum, s_warp);
-            if (mine > 0 && at * rows_per_seq <= u0 && u0 < (at + mine) * rows_per_seq) {
-                s_start[0] = at * rows_per_seq;
-                s_start[1] = b;
-            }
-            before += sum;
-            if (before * rows_per_seq > u0) break;
+    auto claim = [&](int32_t b) {
+        if (mine > 0 && at * rows_per_seq <= u0 && u0 < (at + mine) * rows_per_seq) {
+            s_start[0] = at * rows_per_seq;
+            s_start[1] = b;
         }
-        __syncthreads();
+    };
+    if (one_scan) {
+        claim(threadIdx.x);
+    } else {
+        int64_t before = 0;
+        for (int32_t b0 = 0; b0 < p.batch && before * rows_per_seq <= u0; b0 += kAttnThreads) {
+            const int32_t b = b0 + threadIdx.x;
+            mine = b < p.batch ? row_of<UNIT>(p, b).units : 0;
+            int64_t sum;
+            at = before + block_scan(mine, &sum, s_warp);
+            claim(b);
+            before += sum;
+        }
     }
+    __syncthreads();
 
     // ---- loader state: runs up to STAGES units ahead of the math
     AttnRow lr = row_of<UNIT>(p, (int32_t)s_start[1]);
@@ -320,6 +331,15 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention(const AttnPara
         __syncwarp();
     }
 
+    // the query of a row the loader has reached, towards L2: the math reads it a few units later
+    auto prefetch_q = [&](const AttnRow& r, int32_t head) {
+        const int32_t kvh = head / p.n_chunks, h0 = (head - kvh * p.n_chunks) * p.chunk;
+        const int32_t heads = p.group - h0 < p.chunk ? p.group - h0 : p.chunk;
+        if (lane >= heads) return;
+        const char* x = p.q + (r.b * p.ld_q + (int64_t)(kvh * p.group + h0 + lane) * p.ld_qh) * ES;
+        for (int i = 0; i < p.head_dim * ES; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + i));
+    };
+
     int64_t l_u = u0;
     int32_t slot_next, page_next = page_index(slot_next);
     auto load_step = [&](int stage) {  // issue the loader's unit, then look up the next one's pages
@@ -328,6 +348,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention(const AttnPara
             if (++l_u < u1) {
                 next(lr, l_head, l_tile);
                 page_next = page_index(slot_next);
+                if (l_tile == 0 && warp == 0) prefetch_q(lr, l_head);
             }
         }
         cp_commit();
@@ -427,82 +448,90 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention(const AttnPara
             ++c_tile;
         }
     }
+    empty_rows();
 }
 
-// Joins the parts of the rows that block borders cut.  Block (c, h) handles
-// query head h of the row that began in block c, if one did.  Eight groups of
-// 32 lanes take the parts in turn, four elements a lane, and meet in shared memory.
+// Joins the parts of the rows that block borders cut, in block order.  Block
+// (c, y) looks at the row that began in block c, if one did.  Up to
+// kJoinFew parts (rows are many): blocks with y % 8 == 0 give a warp to each of
+// eight heads.  More parts (rows are few): block y takes head y, its
+// eight warps the parts in turn, and the warps meet in shared memory.
+constexpr int kJoinFew = 64;
+
 template <class T, T (*FROM)(float), int HEADS, int DP>
 __global__ void __launch_bounds__(256) k_attention_join(const AttnParams p) {
     using namespace sbt_attn;
+    constexpr int NV = (DP + 127) / 128;  // float4s of a head per lane
+    __shared__ float s_l[8];
+    __shared__ float4 s_o[8][NV][32];
     sbt_ptx::griddep_wait();
     const AttnDesc e = p.desc[blockIdx.x];
     if (!e.valid) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n = e.last - e.first + 1;
+    const bool few = n <= kJoinFew;
+    if (few && (blockIdx.y & 7)) return;
     const int32_t h0 = e.chunk * p.chunk;
     const int32_t heads = p.group - h0 < p.chunk ? p.group - h0 : p.chunk;
-    const int head = blockIdx.y;
-    if (head >= heads) return;
-    const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-    const int n = e.last - e.first + 1;
-    __shared__ float s_red[8];
-    __shared__ float4 s_o[8][32];
+    const int head = few ? blockIdx.y + warp : blockIdx.y;
+    const int i0 = few ? 0 : warp, di = few ? 1 : 8;
+    if (head >= heads) return;  // the whole block, unless each warp is by itself
     auto slot = [&](int i) -> int64_t { return 2 * (int64_t)(e.first + i) + (i == 0 ? e.first_slot : 0); };
 
     float mm = -CUDART_INF_F;
-    for (int i = threadIdx.x; i < n; i += 256) {
-        const float x = p.part_ml[slot(i) * kAttnMaxHeads + head].x;
-        mm = fmaxf(mm, x);
-    }
+    for (int i = lane; i < n; i += 32) mm = fmaxf(mm, p.part_ml[slot(i) * kAttnMaxHeads + head].x);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        const float x = __shfl_xor_sync(0xffffffffu, mm, d);
-        mm = fmaxf(mm, x);
-    }
-    if (lane == 0) s_red[g] = mm;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 8; ++w) mm = fmaxf(mm, s_red[w]);
+    for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
     const float ms = mm == -CUDART_INF_F ? 0.f : mm;
-    __syncthreads();
 
-    for (int d0 = 0; d0 < DP; d0 += 128) {
-        const int d = d0 + lane * 4;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
+    float4 o[NV];
+    float l = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int i = g; i < n; i += 8) {
-            const int64_t s = slot(i);
-            const float2 ml = p.part_ml[s * kAttnMaxHeads + head];
-            const float w = exp2_fast(ml.x - ms);
-            l += ml.y * w;
+    for (int i = i0; i < n; i += di) {
+        const int64_t s = slot(i);
+        const float2 ml = p.part_ml[s * kAttnMaxHeads + head];
+        const float w = exp2_fast(ml.x - ms);
+        l += ml.y * w;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int d = v * 128 + lane * 4;
             if (d < DP) {
                 const float4 x = *reinterpret_cast<const float4*>(p.part_o + (s * HEADS + head) * DP + d);
-                o.x += x.x * w, o.y += x.y * w, o.z += x.z * w, o.w += x.w * w;
+                o[v].x += x.x * w, o[v].y += x.y * w, o[v].z += x.z * w, o[v].w += x.w * w;
             }
         }
-        s_o[g][lane] = o;
-        if (lane == 0) s_red[g] = l;
-        __syncthreads();
-        if (g == 0) {
-#pragma unroll
-            for (int w = 1; w < 8; ++w) {
-                const float4 x = s_o[w][lane];
-                o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
-                l += s_red[w];
-            }
-            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-            const int32_t qh = e.kvh * p.group + h0 + head;
-            T* dst = reinterpret_cast<T*>(p.out) + e.b * p.ld_out + qh * p.ld_oh + d;
-            if (d + 0 < p.head_dim) dst[0] = FROM(o.x * inv);
-            if (d + 1 < p.head_dim) dst[1] = FROM(o.y * inv);
-            if (d + 2 < p.head_dim) dst[2] = FROM(o.z * inv);
-            if (d + 3 < p.head_dim) dst[3] = FROM(o.w * inv);
-            if (d == 0 && p.lse)
-                p.lse[(int64_t)e.b * p.q_heads + qh] =
-                    l == 0.f ? -CUDART_INF_F : (mm + log2f(l)) * 0.6931471805599453f;
-        }
-        __syncthreads();
     }
+    if (!few) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) s_o[warp][v][lane] = o[v];
+        if (lane == 0) s_l[warp] = l;
+        __syncthreads();
+        if (warp != 0) return;
+#pragma unroll
+        for (int w = 1; w < 8; ++w) {
+            l += s_l[w];
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const float4 x = s_o[w][v][lane];
+                o[v].x += x.x, o[v].y += x.y, o[v].z += x.z, o[v].w += x.w;
+            }
+        }
+    }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const int32_t qh = e.kvh * p.group + h0 + head;
+    T* const dst = reinterpret_cast<T*>(p.out) + e.b * p.ld_out + qh * p.ld_oh;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int d = v * 128 + lane * 4;
+        if (d + 0 < p.head_dim) dst[d + 0] = FROM(o[v].x * inv);
+        if (d + 1 < p.head_dim) dst[d + 1] = FROM(o[v].y * inv);
+        if (d + 2 < p.head_dim) dst[d + 2] = FROM(o[v].z * inv);
+        if (d + 3 < p.head_dim) dst[d + 3] = FROM(o[v].w * inv);
+    }
+    if (lane == 0 && p.lse)
+        p.lse[(int64_t)e.b * p.q_heads + qh] = l == 0.f ? -CUDART_INF_F : (mm + log2f(l)) * 0.6931471805599453f;
 }
 
 // Enqueues the kernel and the join for one instantiation.
@@ -511,12 +540,8 @@ sbt_status sbt_attention_enqueue(sbt_context* ctx, const AttnParams& p, cudaStre
     constexpr int HB = M::MERGE_HEADS;
     constexpr size_t smem = (size_t)kAttnWarps * STAGES * 2 * M::TOK * M::PITCH +
                             (size_t)kAttnWarps * HB * (M::DP + 4) * sizeof(float) + M::SCRATCH_BYTES;
-    const void* kern = (const void*)k_paged_attention<M, STAGES>;
     sbt_status st;
-    if ((st = sbt_cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
-                             "paged_attention shared memory")))
-        return st;
-    int grid = sbt_persistent_grid(ctx, kern, kAttnThreads, smem, INT64_MAX);
+    int grid = sbt_resident_blocks<k_paged_attention<M, STAGES>>(ctx, kAttnThreads, smem);
     if (grid > ctx->sm_count * kAttnMaxPerSm) grid = ctx->sm_count * kAttnMaxPerSm;
     k_paged_attention<M, STAGES><<<grid, kAttnThreads, smem, stream>>>(p);
     if ((st = sbt_after_launch(ctx, "paged_attention"))) return st;

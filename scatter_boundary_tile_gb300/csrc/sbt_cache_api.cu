@@ -4,33 +4,35 @@
 
 namespace {
 
+// Messages are put together only where a check fails.
+std::string say(const char* what, const char* text) { return std::string(what) + text; }
+
 sbt_status check_dtype(sbt_dtype dtype, const char* what) {
     const int es = sbt_dtype_size(dtype);
-    if (es != 2 && es != 4) return sbt_fail(SBT_ERR_UNSUPPORTED, std::string(what) + ": unsupported dtype");
+    if (es != 2 && es != 4) return sbt_fail(SBT_ERR_UNSUPPORTED, say(what, ": unsupported dtype"));
     return SBT_OK;
 }
 
 sbt_status check_workspace(const void* ws, size_t bytes, size_t need, const char* what) {
     if (!ws || bytes < need)
-        return sbt_fail(SBT_ERR_ALIGNMENT, std::string(what) + ": workspace smaller than its size query");
+        return sbt_fail(SBT_ERR_ALIGNMENT, say(what, ": workspace smaller than its size query"));
     if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
-        return sbt_fail(SBT_ERR_ALIGNMENT, std::string(what) + ": workspace must be 256-byte aligned");
+        return sbt_fail(SBT_ERR_ALIGNMENT, say(what, ": workspace must be 256-byte aligned"));
     return SBT_OK;
 }
 
 sbt_status check_map(const sbt_page_map* m, bool lens, bool refs, const char* what) {
-    const std::string w = what;
-    SBT_REQUIRE(m, w + ": map is NULL");
-    SBT_REQUIRE(m->n_seq >= 0 && m->max_pages >= 0 && m->n_pages >= 0, w + ": negative extent in the page map");
-    SBT_REQUIRE(m->n_pages < (1ll << 31), w + ": n_pages must be below 2^31");
-    SBT_REQUIRE(m->page_size >= 1, w + ": page_size must be at least 1");
-    SBT_REQUIRE(m->ld_table >= m->max_pages, w + ": ld_table < max_pages");
-    SBT_REQUIRE(m->n_seq == 0 || m->max_pages == 0 || m->page_table, w + ": page_table is NULL");
-    SBT_REQUIRE(!lens || m->n_seq == 0 || m->lens, w + ": lens is NULL");
-    SBT_REQUIRE(!refs || m->n_pages == 0 || m->refs, w + ": refs is NULL");
-    SBT_REQUIRE_ALIGNED(m->page_table, 4, w + ": page_table is not 4-byte aligned");
-    if (lens) SBT_REQUIRE_ALIGNED(m->lens, 4, w + ": lens is not 4-byte aligned");
-    if (refs) SBT_REQUIRE_ALIGNED(m->refs, 4, w + ": refs is not 4-byte aligned");
+    SBT_REQUIRE(m, say(what, ": map is NULL"));
+    SBT_REQUIRE(m->n_seq >= 0 && m->max_pages >= 0 && m->n_pages >= 0, say(what, ": negative extent in the page map"));
+    SBT_REQUIRE(m->n_pages < (1ll << 31), say(what, ": n_pages must be below 2^31"));
+    SBT_REQUIRE(m->page_size >= 1, say(what, ": page_size must be at least 1"));
+    SBT_REQUIRE(m->ld_table >= m->max_pages, say(what, ": ld_table < max_pages"));
+    SBT_REQUIRE(m->n_seq == 0 || m->max_pages == 0 || m->page_table, say(what, ": page_table is NULL"));
+    SBT_REQUIRE(!lens || m->n_seq == 0 || m->lens, say(what, ": lens is NULL"));
+    SBT_REQUIRE(!refs || m->n_pages == 0 || m->refs, say(what, ": refs is NULL"));
+    SBT_REQUIRE_ALIGNED(m->page_table, 4, say(what, ": page_table is not 4-byte aligned"));
+    if (lens) SBT_REQUIRE_ALIGNED(m->lens, 4, say(what, ": lens is not 4-byte aligned"));
+    if (refs) SBT_REQUIRE_ALIGNED(m->refs, 4, say(what, ": refs is not 4-byte aligned"));
     return SBT_OK;
 }
 
@@ -38,54 +40,51 @@ sbt_status check_map(const sbt_page_map* m, bool lens, bool refs, const char* wh
 bool apart(int64_t n, int64_t ld, int32_t dim) { return n <= 1 || ld >= dim; }
 
 sbt_status check_cache(const sbt_kv_cache* c, const sbt_page_map* m, int es, const char* what) {
-    const std::string w = what;
-    SBT_REQUIRE(c, w + ": cache is NULL");
-    SBT_REQUIRE(c->heads >= 1 && c->head_dim >= 1, w + ": cache heads and head_dim must be positive");
-    SBT_REQUIRE(m->n_pages == 0 || (c->k && c->v), w + ": cache k or v is NULL");
+    SBT_REQUIRE(c, say(what, ": cache is NULL"));
+    SBT_REQUIRE(c->heads >= 1 && c->head_dim >= 1, say(what, ": cache heads and head_dim must be positive"));
+    SBT_REQUIRE(m->n_pages == 0 || (c->k && c->v), say(what, ": cache k or v is NULL"));
     SBT_REQUIRE(apart(m->n_pages, c->ld_page, c->head_dim) && apart(m->page_size, c->ld_slot, c->head_dim) &&
                     apart(c->heads, c->ld_head, c->head_dim) && c->ld_page >= 0 && c->ld_slot >= 0 && c->ld_head >= 0,
-                w + ": cache stride smaller than head_dim");
-    SBT_REQUIRE_ALIGNED(c->k, es, w + ": cache k is not aligned to its element size");
-    SBT_REQUIRE_ALIGNED(c->v, es, w + ": cache v is not aligned to its element size");
+                say(what, ": cache stride smaller than head_dim"));
+    SBT_REQUIRE_ALIGNED(c->k, es, say(what, ": cache k is not aligned to its element size"));
+    SBT_REQUIRE_ALIGNED(c->v, es, say(what, ": cache v is not aligned to its element size"));
     return SBT_OK;
 }
 
 // A set of head rows that is read (or, with `write`, written).
 sbt_status check_rows(const SbtHeadRows& r, int64_t tokens, int32_t heads, int32_t dim, int es, bool write,
                       const char* name, const char* what) {
-    const std::string w = std::string(what) + ": " + name;
+    auto row = [&](const char* text) { return say(what, ": ") + name + text; };
     if (heads == 0) return SBT_OK;
-    SBT_REQUIRE(r.p, w + " is NULL");
-    SBT_REQUIRE(r.ld >= 0 && r.ldh >= 0, w + " has a negative stride");
-    SBT_REQUIRE(!write || (apart(tokens, r.ld, dim) && apart(heads, r.ldh, dim)), w + " stride smaller than head_dim");
-    SBT_REQUIRE_ALIGNED(r.p, es, w + " is not aligned to its element size");
+    SBT_REQUIRE(r.p, row(" is NULL"));
+    SBT_REQUIRE(r.ld >= 0 && r.ldh >= 0, row(" has a negative stride"));
+    SBT_REQUIRE(!write || (apart(tokens, r.ld, dim) && apart(heads, r.ldh, dim)), row(" stride smaller than head_dim"));
+    SBT_REQUIRE_ALIGNED(r.p, es, row(" is not aligned to its element size"));
     return SBT_OK;
 }
 
 sbt_status check_rope(const sbt_rope* r, int32_t head_dim, const char* what) {
-    const std::string w = what;
     if (!r || r->rot_dim == 0) return SBT_OK;
     SBT_REQUIRE(r->rot_dim > 0 && r->rot_dim % 2 == 0 && r->rot_dim <= head_dim,
-                w + ": rot_dim must be even and at most head_dim");
+                say(what, ": rot_dim must be even and at most head_dim"));
     if (r->layout != SBT_ROPE_HALF && r->layout != SBT_ROPE_INTERLEAVED)
-        return sbt_fail(SBT_ERR_UNSUPPORTED, w + ": unknown rotation layout");
-    SBT_REQUIRE(r->n_pos >= 0 && (r->n_pos == 0 || r->table), w + ": rotation table is NULL");
-    SBT_REQUIRE_ALIGNED(r->table, 8, w + ": rotation table is not 8-byte aligned");
+        return sbt_fail(SBT_ERR_UNSUPPORTED, say(what, ": unknown rotation layout"));
+    SBT_REQUIRE(r->n_pos >= 0 && (r->n_pos == 0 || r->table), say(what, ": rotation table is NULL"));
+    SBT_REQUIRE_ALIGNED(r->table, 8, say(what, ": rotation table is not 8-byte aligned"));
     return SBT_OK;
 }
 
 sbt_status check_pools(const sbt_page_pool* pools, int32_t n, int64_t n_pages, const char* what) {
-    const std::string w = what;
-    SBT_REQUIRE(n >= 1 && n <= SBT_MAX_PAGE_POOLS && pools, w + ": between 1 and SBT_MAX_PAGE_POOLS pools");
+    SBT_REQUIRE(n >= 1 && n <= SBT_MAX_PAGE_POOLS && pools, say(what, ": between 1 and SBT_MAX_PAGE_POOLS pools"));
     for (int32_t i = 0; i < n; ++i) {
         const sbt_page_pool& q = pools[i];
         SBT_REQUIRE(q.n_planes >= 1 && q.n_planes < (1ll << 31) && q.page_bytes >= 1,
-                    w + ": pool planes and page_bytes must be positive");
-        SBT_REQUIRE(q.page_bytes < (1ll << 40), w + ": page_bytes too large");
+                    say(what, ": pool planes and page_bytes must be positive"));
+        SBT_REQUIRE(q.page_bytes < (1ll << 40), say(what, ": page_bytes too large"));
         SBT_REQUIRE((n_pages <= 1 || q.page_stride >= q.page_bytes) &&
                         (q.n_planes == 1 || q.plane_stride >= q.page_bytes),
-                    w + ": pool stride smaller than page_bytes");
-        SBT_REQUIRE(n_pages == 0 || q.base, w + ": pool base is NULL");
+                    say(what, ": pool stride smaller than page_bytes"));
+        SBT_REQUIRE(n_pages == 0 || q.base, say(what, ": pool base is NULL"));
     }
     return SBT_OK;
 }

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 
 #include "../../include/sbt.h"
@@ -209,6 +210,23 @@ sbt_status sbt_launch_pages_fork(sbt_context* ctx, const sbt_page_map* map, cons
 sbt_status sbt_launch_pages_compact(sbt_context* ctx, const sbt_page_map* map, const sbt_page_pool* pools,
                                     int32_t n_pools, int32_t* table_out, int64_t ld_out, int32_t* refs_out,
                                     int32_t* page_to, int32_t* n_live, void* workspace, cudaStream_t stream);
+
+// Blocks of a kernel with dynamic shared memory that the device holds at once.
+// Asked of the runtime on a kernel's first use on a device, remembered after.
+template <auto KERN>
+int sbt_resident_blocks(const sbt_context* ctx, int threads, size_t smem) {
+    static std::atomic<int> known[64];
+    std::atomic<int>& n = known[ctx->device & 63];
+    int v = n.load(std::memory_order_relaxed);
+    if (v == 0) {
+        if (cudaFuncSetAttribute((const void*)KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+            cudaSuccess)
+            return ctx->sm_count;  // the launch will fail and say why
+        v = sbt_persistent_grid(ctx, (const void*)KERN, threads, smem, INT64_MAX);
+        n.store(v, std::memory_order_relaxed);
+    }
+    return v;
+}
 
 // Checks the launch that was just enqueued and counts it.
 sbt_status sbt_after_launch(sbt_context* ctx, const char* what);
