@@ -50,21 +50,30 @@ __device__ __forceinline__ void mma16(float* c, const uint32_t* a, const uint32_
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-template <bool BF, int DP_, int NB>
+template <bool BF, int DP_, int NB, int MT>
 struct Mma16 {
     typedef uint16_t T;
-    static constexpr int ES = 2, TOK = 16, DP = DP_, HEADS = 8 * NB, OWN = 2 * NB;
-    // rows of a multiple of 128 bytes swizzle their chunks, others are padded to an odd number of
-    // chunks: either way the eight rows of one 8 x 8 matrix lie in different banks
-    static constexpr bool SWIZZLE = DP % 64 == 0;
-    static constexpr int PITCH = SWIZZLE ? DP * 2 : DP * 2 + 16;
-    static constexpr int MERGE_HEADS = 4, SCRATCH_BYTES = 0;
-    static __device__ __forceinline__ int chunk16(int t, int c) { return SWIZZLE ? c ^ (t & 7) : c; }
+    static constexpr int ES = 2, TOK = 16 * MT, DP = DP_, HEADS = 8 * NB, SCRATCH = 0;
+    static constexpr int PITCH = DP * 2;
+    // the eight rows of one 8 x 8 matrix lie in different banks: rows of 128 n bytes differ in the
+    // XOR of all three chunk bits, rows of 192 in their start's and two
+    static constexpr bool WIDE = PITCH % 128 == 0;
+    static __device__ __forceinline__ int swizzle(int t) { return WIDE ? t & 7 : (t >> 1) & 3; }
+    // byte of chunk 2 k + x (x = 0, 1) in a row, where s = x ^ swizzle(row)
+    static __device__ __forceinline__ uint32_t chunk_at(int k, uint32_t s) {
+        return WIDE ? (k >> 2) * 128 + ((s ^ (2 * (k & 3))) << 4) : (k >> 1) * 64 + ((s ^ (2 * (k & 1))) << 4);
+    }
     static __device__ __forceinline__ uint16_t from_float(float x) {
         return BF ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
     }
-    static __device__ __forceinline__ float to_float(uint16_t x) {
-        return BF ? __bfloat162float(__ushort_as_bfloat16(x)) : __half2float(__ushort_as_half(x));
+    // two values rounded to 16 bits, the first in the low half
+    static __device__ __forceinline__ uint32_t pack2(float x, float y) {
+        if (BF) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+            return *reinterpret_cast<const uint32_t*>(&h);
+        }
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
     }
 
     uint32_t qf[DP / 16][NB][2];
@@ -108,29 +117,48 @@ struct Mma16 {
     __device__ __forceinline__ void tile(const AttnParams& p, const uint8_t*, uint32_t k_s, uint32_t v_s, uint32_t bits,
                                          float*) {
         const int lane = threadIdx.x & 31, g = lane >> 2;
-        float s[NB][4];
+        float s[MT][NB][4];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-        const int kr = lane & 15, kc = lane >> 4;
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-            uint32_t a[4];
-            ldsm4(a, k_s + kr * PITCH + chunk16(kr, 2 * k + kc) * 16);
+            for (int n = 0; n < NB; ++n) s[m][n][0] = s[m][n][1] = s[m][n][2] = s[m][n][3] = 0.f;
+        const uint32_t k_row = k_s + (lane & 15) * PITCH;
+        const uint32_t k_x = (lane >> 4) ^ swizzle(lane & 15);
 #pragma unroll
-            for (int n = 0; n < NB; ++n) mma16<BF>(s[n], a, qf[k][n]);
+        for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                uint32_t a[4];
+                ldsm4(a, k_row + m * 16 * PITCH + chunk_at(k, k_x));
+#pragma unroll
+                for (int n = 0; n < NB; ++n) mma16<BF>(s[m][n], a, qf[k][n]);
+            }
+        constexpr uint32_t ALL = MT == 2 ? 0xffffffffu : 0xffffu;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[m][n][i] *= p.scale_log2;
+        if (bits != ALL) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!((bits >> (m * 16 + g + (i >> 1) * 8)) & 1u)) s[m][n][i] = -CUDART_INF_F;
         }
-        const bool see0 = (bits >> g) & 1u, see1 = (bits >> (g + 8)) & 1u;
-        uint32_t hi[NB][2], lo[NB][2];
+        uint32_t hi[MT][NB][2], lo[MT][NB][2];
         float alpha[NB][2];
         bool grown = false;
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-            float pr[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float a = see0 ? s[n][j] * p.scale_log2 : -CUDART_INF_F;
-                const float b = see1 ? s[n][j + 2] * p.scale_log2 : -CUDART_INF_F;
-                float t = fmaxf(a, b);
+                float t = fmaxf(s[0][n][j], s[0][n][j + 2]);
+#pragma unroll
+                for (int m = 1; m < MT; ++m) t = fmaxf(t, fmaxf(s[m][n][j], s[m][n][j + 2]));
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
@@ -139,19 +167,24 @@ struct Mma16 {
                 alpha[n][j] = sbt_attn::exp2_fast(mx[n][j] - ts);
                 grown |= t != mx[n][j];
                 mx[n][j] = t;
-                pr[j] = sbt_attn::exp2_fast(a - ts);
-                pr[j + 2] = sbt_attn::exp2_fast(b - ts);
-                l[n][j] = l[n][j] * alpha[n][j] + pr[j] + pr[j + 2];
-            }
+                l[n][j] *= alpha[n][j];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint16_t h0 = from_float(pr[2 * i]), h1 = from_float(pr[2 * i + 1]);
-                hi[n][i] = transpose8((uint32_t)h0 | (uint32_t)h1 << 16);
-                if (BF) {
-                    const uint16_t l0 = from_float(pr[2 * i] - to_float(h0)), l1 = from_float(pr[2 * i + 1] - to_float(h1));
-                    lo[n][i] = transpose8((uint32_t)l0 | (uint32_t)l1 << 16);
+                for (int m = 0; m < MT; ++m) {
+                    s[m][n][j] = sbt_attn::exp2_fast(s[m][n][j] - ts);
+                    s[m][n][j + 2] = sbt_attn::exp2_fast(s[m][n][j + 2] - ts);
+                    l[n][j] += s[m][n][j] + s[m][n][j + 2];
                 }
             }
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float p0 = s[m][n][2 * i], p1 = s[m][n][2 * i + 1];
+                    const uint32_t h = pack2(p0, p1);
+                    hi[m][n][i] = transpose8(h);
+                    if (BF)
+                        lo[m][n][i] = transpose8(pack2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xFFFF0000u)));
+                }
         }
         if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
@@ -161,20 +194,24 @@ struct Mma16 {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[k][n][i] *= alpha[n][i & 1];
         }
-        const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
+        const int v_t = (lane & 7) + ((lane >> 4) << 3);
+        const uint32_t v_row = v_s + v_t * PITCH, v_x = ((lane >> 3) & 1) ^ swizzle(v_t);
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-            uint32_t a[4];
-            ldsm4_t(a, v_s + vr * PITCH + chunk16(vr, 2 * k + vc) * 16);
+        for (int k = 0; k < DP / 16; ++k)
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                mma16<BF>(o[k][n], a, hi[n]);
-                if (BF) mma16<BF>(o[k][n], a, lo[n]);
+            for (int m = 0; m < MT; ++m) {
+                uint32_t a[4];
+                ldsm4_t(a, v_row + m * 16 * PITCH + chunk_at(k, v_x));
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    mma16<BF>(o[k][n], a, hi[m][n]);
+                    if (BF) mma16<BF>(o[k][n], a, lo[m][n]);
+                }
             }
-        }
     }
 
-    __device__ __forceinline__ void reduce() {
+    // l over the lanes that hold different positions of the same heads
+    __device__ __forceinline__ void finish() {
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -184,70 +221,73 @@ struct Mma16 {
                 l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 16);
             }
     }
-    __device__ __forceinline__ void put_ml(float* m, float* sum) const {
-        const int lane = threadIdx.x & 31;
-        if (lane < 4)
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    m[n * 8 + lane * 2 + j] = mx[n][j];
-                    sum[n * 8 + lane * 2 + j] = l[n][j];
-                }
-    }
-    __device__ __forceinline__ void heads_max(const float (*s_m)[HEADS], float* top) const {
-        const int q2 = (threadIdx.x & 3) * 2;
-#pragma unroll
-        for (int i = 0; i < OWN; ++i) {
-            top[i] = -CUDART_INF_F;
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) top[i] = fmaxf(top[i], s_m[w][(i >> 1) * 8 + q2 + (i & 1)]);
-        }
-    }
-    __device__ __forceinline__ void rescale_to(const float* top) {
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float a = sbt_attn::exp2_fast(mx[n][j] - top[2 * n + j]);
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
-                    o[k][n][j] *= a;
-                    o[k][n][j + 2] *= a;
-                }
-            }
-    }
-    // heads hb .. hb + 3 of this warp into dst[head - hb][element]
-    __device__ __forceinline__ void put_o(float* dst, int pitch, int hb) const {
+
+    // Lane (g, q) holds elements 16 k + g and 16 k + g + 8 of heads 2 q, 2 q + 1; transposed in
+    // 16 bits it holds element pairs 16 k + 2 q and 16 k + 8 + 2 q of head g: four lanes write 16 bytes.
+    __device__ __forceinline__ void put_row(const AttnParams& p, int32_t b, int32_t qh, int32_t heads) {
+        finish();
         const int lane = threadIdx.x & 31, g = lane >> 2, q2 = (lane & 3) * 2;
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-            if (n != hb / 8) continue;
-            const int h = n * 8 + q2 - hb;
-            if (h < 0 || h >= MERGE_HEADS) continue;
+            if (n * 8 >= heads) break;
+            const float inv0 = sbt_attn::inverse(l[n][0]), inv1 = sbt_attn::inverse(l[n][1]);
+            const int h = n * 8 + g;
+            uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + b * p.ld_out + (int64_t)(qh + h) * p.ld_oh;
 #pragma unroll
-            for (int k = 0; k < DP / 16; ++k) {
-                dst[h * pitch + k * 16 + g] = o[k][n][0];
-                dst[(h + 1) * pitch + k * 16 + g] = o[k][n][1];
-                dst[h * pitch + k * 16 + g + 8] = o[k][n][2];
-                dst[(h + 1) * pitch + k * 16 + g + 8] = o[k][n][3];
-            }
+            for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t w = transpose8(pack2(o[k][n][2 * i] * inv0, o[k][n][2 * i + 1] * inv1));
+                    const int d = k * 16 + i * 8 + q2;
+                    if (h >= heads || d >= p.head_dim) continue;
+                    if (p.out_words) {
+                        *reinterpret_cast<uint32_t*>(dst + d) = w;
+                    } else {
+                        dst[d] = (uint16_t)w;
+                        if (d + 1 < p.head_dim) dst[d + 1] = (uint16_t)(w >> 16);
+                    }
+                }
+            if (p.lse && g == 0)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (n * 8 + q2 + j < heads)
+                        p.lse[(int64_t)b * p.q_heads + qh + n * 8 + q2 + j] = sbt_attn::log_sum(mx[n][j], l[n][j]);
+        }
+    }
+
+    // the state to dst [DP][HEADS] and ml [HEADS]
+    __device__ __forceinline__ void put_part(float* dst, float2* ml) {
+        finish();
+        const int lane = threadIdx.x & 31, g = lane >> 2, q2 = (lane & 3) * 2;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<float2*>(dst + (k * 16 + i * 8 + g) * HEADS + n * 8 + q2) =
+                        make_float2(o[k][n][2 * i], o[k][n][2 * i + 1]);
+            if (g == 0)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) ml[n * 8 + q2 + j] = make_float2(mx[n][j], l[n][j]);
         }
     }
 };
 
-template <bool BF, int DP, int STAGES>
+template <bool BF, int DP, int MT, int STAGES, int WARPS, int BLOCKS>
 sbt_status by_heads(sbt_context* ctx, const AttnParams& p, cudaStream_t stream) {
-    const int heads = p.group < p.chunk ? p.group : p.chunk;
-    if (heads <= 8) return sbt_attention_enqueue<Mma16<BF, DP, 1>, STAGES>(ctx, p, stream);
-    return sbt_attention_enqueue<Mma16<BF, DP, 2>, STAGES>(ctx, p, stream);
+    if (p.chunk <= 8) return sbt_attention_enqueue<Mma16<BF, DP, 1, MT>, STAGES, WARPS, BLOCKS>(ctx, p, stream);
+    return sbt_attention_enqueue<Mma16<BF, DP, 2, MT>, STAGES, WARPS, BLOCKS>(ctx, p, stream);
 }
 
+// Warps per block and blocks per SM: as many as two stages each leave room for.
 template <bool BF>
 sbt_status by_dim(sbt_context* ctx, const AttnParams& p, cudaStream_t stream) {
-    if (p.head_dim <= 64) return by_heads<BF, 64, 6>(ctx, p, stream);
-    if (p.head_dim <= 128) return by_heads<BF, 128, 3>(ctx, p, stream);
-    return by_heads<BF, 256, 3>(ctx, p, stream);
+    if (p.head_dim <= 64) return by_heads<BF, 64, 2, 2, 4, 3>(ctx, p, stream);
+    if (p.head_dim <= 96) return by_heads<BF, 96, 1, 3, 4, 3>(ctx, p, stream);
+    if (p.head_dim <= 128) return by_heads<BF, 128, 1, 2, 4, 3>(ctx, p, stream);
+    if (p.head_dim <= 192) return by_heads<BF, 192, 1, 2, 4, 2>(ctx, p, stream);
+    return by_heads<BF, 256, 1, 2, 6, 1>(ctx, p, stream);
 }
 
 }  // namespace
@@ -265,13 +305,13 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
 
-// One size for every type: the states of two cut rows per block, for the
-// largest grid, and the descriptors of the rows that began in each block.
+// One size for every type: the states of two cut rows per warp, for the
+// largest grid, and the descriptors of cut rows.
 size_t sbt_paged_attention_workspace_bytes(const sbt_context* ctx, int32_t q_heads, int32_t kv_heads,
                                            int32_t head_dim) {
     int32_t chunk, n;
     cut_heads(q_heads / kv_heads, kAttnMaxHeads, &chunk, &n);
-    const size_t g = (size_t)ctx->sm_count * kAttnMaxPerSm;
+    const size_t g = (size_t)ctx->sm_count * kAttnMaxWarps;
     const size_t heads = chunk <= 8 ? 8 : 16, dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
     return round256(g * sizeof(AttnDesc)) + round256(2 * g * kAttnMaxHeads * sizeof(float2)) +
            2 * g * heads * dp * sizeof(float);
@@ -300,7 +340,8 @@ sbt_status sbt_launch_paged_attention(sbt_context* ctx, sbt_dtype dtype, const S
                          ((int64_t)p.head_dim | p.ld_page | p.ld_slot | p.ld_head) * es;
     p.copy_bytes = ctx->path == SBT_PATH_SCALAR ? es : bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : es;
     p.q_words = (reinterpret_cast<uintptr_t>(p.q) | ((int64_t)p.head_dim | p.ld_q | p.ld_qh) * es) % 4 == 0;
-    const size_t g = (size_t)ctx->sm_count * kAttnMaxPerSm;
+    p.out_words = (reinterpret_cast<uintptr_t>(p.out) | ((int64_t)p.head_dim | p.ld_out | p.ld_oh) * es) % 4 == 0;
+    const size_t g = (size_t)ctx->sm_count * kAttnMaxWarps;
     p.desc = (AttnDesc*)workspace;
     p.part_ml = (float2*)((char*)workspace + round256(g * sizeof(AttnDesc)));
     p.part_o = (float*)((char*)p.part_ml + round256(2 * g * kAttnMaxHeads * sizeof(float2)));

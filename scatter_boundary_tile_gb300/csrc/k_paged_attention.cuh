@@ -6,34 +6,49 @@
 // m, the sum l = sum_j 2^(s'_j - m) and the vector o = sum_j 2^(s'_j - m) v_j
 // (s' = s * log2 e), rescaling l and o by 2^(m_old - m_new) when m grows; all
 // three are fp32.  Two such states over disjoint positions join by the same
-// rule, which is what lets one row be split over warps and over blocks.
+// rule, which is what lets one row be split.
 //
-// Split.  A row is one (sequence, key-value head, chunk of its query heads).
-// Rows are cut into units of 4 warp tiles; all units of all rows lie on one
-// line, and block c of G takes the units [c U / G, (c + 1) U / G).  Every block
-// so reads the same amount to within one unit whatever the lengths are, and
-// the lengths are read on the device.  A row wholly inside one block is
-// written by it; of a row cut by block borders each block writes its state to
-// the workspace and k_attention_join adds them in block order (the result
-// does not depend on which block finished first).
+// Split.  A row is one (sequence, key-value head, chunk of its query heads),
+// cut into tiles of TOK positions.  All tiles of all rows lie on one line, and
+// warp c of G takes U / G of the U tiles, in order: every warp reads the same
+// amount to within one tile, whatever the lengths are, and the lengths are read
+// on the device.  A row wholly inside one warp's range is written by that
+// warp; of a row cut by range borders each warp writes its state to the
+// workspace and k_attention_join adds them in the order of the line (the result
+// does not depend on which warp finished first).
 //
-// Each warp owns one tile of every unit and a private ring of shared-memory
-// stages filled by cp.async, so the main loop has no block-wide barrier; the
-// ring runs ahead across row borders, and the warps meet only where a row ends.
+// After the first prefix sum no warp waits for another: each has a private ring
+// of shared-memory stages filled by cp.async, which runs ahead of the math and
+// across row ends.  Ranges per block with a join of its warps at each row end
+// were measured first: 103 us against 90 on 64 ragged sequences, 142 against 61
+// on 1024 short ones (bf16, 32 query and 8 key-value heads of 128).  Rows
+// fetched by the bulk-copy engine, one 256-byte row a lane, took 136 us there:
+// the engine starts about one row per 15 cycles.
+//
 // Positions that are masked (past the length, outside the window, on an
-// unmapped page) are zero-filled in shared memory and never read from the
-// cache, so stale or NaN contents there cannot reach a sum.
+// unmapped page) are never read from the cache and are zero in shared memory,
+// so stale or NaN contents there cannot reach a sum.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <math_constants.h>
 
 #include "sbt_internal.cuh"
 #include "tc_ptx.cuh"
 
-constexpr int kAttnWarps = 4;
-constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kAttnMaxPerSm = 4;    // blocks per SM the workspace is sized for
+constexpr int kAttnMaxWarps = 16;   // warps per SM the workspace is sized for
+constexpr int kClusterMost = 8, kClusterTiles = 16;
 constexpr int kAttnMaxHeads = 16;   // query heads of one key-value head that one row carries
+
+// A cut row: the warps first .. last hold its parts, in slot 2 first +
+// first_slot and in slots 2 c of the others -- except that a block which lies
+// wholly inside the row has joined its warps' parts in its first warp's slot.
+// That holds for all blocks between the first's and the last's, and for those
+// two as the flags say.
+struct AttnDesc {
+    int32_t valid, b, kvh, chunk;
+    int32_t first, last, first_slot, joined;  // joined: bit 0 the first's block, bit 1 the last's
+};
 
 struct AttnParams {
     const char* q;
@@ -53,55 +68,56 @@ struct AttnParams {
     int32_t max_len;                         // max_pages * page_size, capped to int32
     sbt_fastdiv page_size;
     float scale_log2;                        // scale * log2(e)
-    int32_t q_words;                         // query rows are read in 4-byte words
+    int32_t q_words, out_words;              // rows of q / out start on 4 bytes and head_dim fills whole words
+    int32_t tile_in_page;                    // pages hold whole tiles
     int32_t copy_bytes;                      // 16, 4 or the element size: width of one copy into shared memory
+    int32_t cluster;                         // blocks per row of the cluster form
+    int32_t desc_by_row;                     // descriptors by row (there are no more rows than warps), else by warp
     // workspace
-    struct AttnDesc* desc;
-    float2* part_ml;                         // [2 G][kAttnMaxHeads] (m, l)
-    float* part_o;                           // [2 G][heads][DP]
+    AttnDesc* desc;
+    float2* part_ml;                         // [2 G][HEADS] (m, l)
+    float* part_o;                           // [2 G][DP][HEADS]
 };
 
-// Row whose first units lie in the block that wrote this and whose last ones
-// do not: the parts are slot `first_slot` of block `first` and slot 0 of the
-// blocks first + 1 .. last.
-struct AttnDesc {
-    int32_t valid, b, kvh, chunk;
-    int32_t first, last, first_slot, pad;
-};
-
-// Visible positions of batch entry b: [lo, hi), and its units.
+// Visible positions of batch entry b: [lo, hi), and its tiles from `base` on.
 struct AttnRow {
-    int32_t b, seq, lo, hi, base, units;
+    int32_t b, seq, lo, hi, base, tiles;
 };
 
 namespace sbt_attn {
 
-template <int UNIT>
+template <int TOK>
 __device__ __forceinline__ AttnRow row_of(const AttnParams& p, int32_t b) {
     AttnRow r;
     r.b = b;
     r.seq = p.seq ? __ldg(p.seq + b) : b;
-    r.lo = r.hi = r.base = r.units = 0;
+    r.lo = r.hi = r.base = r.tiles = 0;
     if (r.seq >= 0 && r.seq < p.n_seq) {
         int32_t n = __ldg(p.lens + r.seq);
         n = n < 0 ? 0 : n > p.max_len ? p.max_len : n;
         r.hi = n;
         r.lo = (p.window > 0 && n > p.window) ? n - p.window : 0;
-        r.base = r.lo & ~(UNIT - 1);
-        r.units = (int32_t)(((int64_t)r.hi - r.base + UNIT - 1) / UNIT);
+        r.base = r.lo & ~(TOK - 1);
+        r.tiles = (r.hi - r.base + TOK - 1) / TOK;
     }
     return r;
 }
 
-__device__ __forceinline__ int64_t range_start(int64_t c, int64_t U, int64_t G) { return c * U / G; }
-
-// Block whose range holds unit u (1 <= G <= U).
-__device__ __forceinline__ int32_t block_of(int64_t u, int64_t U, int64_t G) {
-    int64_t c = u * G / U;
-    while (c + 1 < G && range_start(c + 1, U, G) <= u) ++c;
-    while (c > 0 && range_start(c, U, G) > u) --c;
-    return (int32_t)c;
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {  // a >= 0, b > 0
+    return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
+
+// U tiles over G warps (1 <= G <= U): the first `more` warps take size + 1, the others size.
+struct Line {
+    int64_t size, more;
+    __device__ __forceinline__ Line(int64_t U, int64_t G) : size(divide(U, G)) { more = U - size * G; }
+    __device__ __forceinline__ int64_t start(int64_t c) const { return c * size + (c < more ? c : more); }
+    // warp whose range holds tile u
+    __device__ __forceinline__ int32_t warp_of(int64_t u) const {
+        const int64_t big = more * (size + 1);
+        return (int32_t)(u < big ? divide(u, size + 1) : more + divide(u - big, size));
+    }
+};
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int src_bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
@@ -121,7 +137,14 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// Sum over the block of one int64 per thread, and its exclusive prefix.
+// 1 / l, or 0 for a row that saw nothing (l = 0); NaN stays NaN.
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float log_sum(float m, float l) {
+    return l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// Exclusive prefix over the block of one int64 per thread, and the sum.
+template <int WARPS>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* total, int64_t* s_warp) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t x = v;
@@ -135,7 +158,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* total, int64_t
     __syncthreads();
     int64_t before = 0, sum = 0;
 #pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += s_warp[w];
         sum += s_warp[w];
     }
@@ -147,409 +170,556 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* total, int64_t
 
 // M is the math of one warp:
 //   T, ES         raw element type and its size
-//   TOK           positions of one warp tile (a power of two, at most 32)
+//   TOK           positions of one tile (a power of two, at most 32)
 //   DP            head size padded to what the tile math needs (padding columns are zero)
-//   HEADS         query heads a row carries at most
-//   PITCH, chunk16(t, c)   bytes between tile rows, place of 16-byte chunk c of row t
-//   MERGE_HEADS   heads joined per pass through the merge buffer
-//   load_q        query of a row into registers or scratch, state reset (all warps together)
+//   HEADS         query heads a row carries at most (a power of two)
+//   PITCH         bytes between tile rows
+//   swizzle(t)    what the 16-byte chunk numbers of row t are XORed with.  Rows start on 64 bytes
+//                 or more: a copy whose global lines straddle shared-memory lines asks L2 twice
+//                 (rows padded by 16 bytes: 39 % of the sectors, 105 us against 98 on 64 ragged
+//                 sequences); the XOR keeps the math's reads free of bank conflicts
+//   SCRATCH       floats of shared memory per warp
+//   load_q        query of a row into registers or scratch, state reset
 //   tile          one tile; bit t of the mask: position t is visible
-//   reduce, put_ml, heads_max, rescale_to, put_o    the state, for the join of the warps
+//   put_row       the finished row to out and lse
+//   put_part      the state to memory
+
+// One warp's tiles on their way into its ring: the loads run STAGES - 1 tiles
+// ahead of the math and cross row ends by themselves.
 template <class M, int STAGES>
-__global__ void __launch_bounds__(kAttnThreads) k_paged_attention(const AttnParams p) {
-    using namespace sbt_attn;
-    using namespace sbt_ptx;
-    constexpr int TOK = M::TOK, DP = M::DP, ES = M::ES, HEADS = M::HEADS, PITCH = M::PITCH;
-    constexpr int UNIT = TOK * kAttnWarps;
-    constexpr int STAGE_BYTES = 2 * TOK * PITCH;
-    constexpr int MERGE_PITCH = DP + 4;  // floats between heads in the merge buffer
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_warp[kAttnWarps];
-    __shared__ int64_t s_start[2];       // first unit of the found row's sequence, its batch entry
-    __shared__ float s_m[kAttnWarps][HEADS], s_l[kAttnWarps][HEADS];
-    __shared__ uint32_t s_mask[kAttnWarps][STAGES];
-    float* const s_merge = reinterpret_cast<float*>(smem + (size_t)kAttnWarps * STAGES * STAGE_BYTES);
-    float* const s_scratch = s_merge + kAttnWarps * M::MERGE_HEADS * MERGE_PITCH;
+struct AttnLoader {
+    static constexpr int TOK = M::TOK, DP = M::DP, ES = M::ES, PITCH = M::PITCH;
+    static constexpr int STAGE_BYTES = 2 * TOK * PITCH;
+    static constexpr uint32_t ALL = TOK == 32 ? 0xffffffffu : (1u << (TOK & 31)) - 1u;
+    // 16-byte copies: LPR lanes on one row, RPI rows at a time
+    static constexpr int VECS = DP * ES / 16, LPR = VECS > 16 ? 32 : VECS > 8 ? 16 : 8, RPI = 32 / LPR;
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int32_t rows_per_seq = p.kv_heads * p.n_chunks;
-    uint8_t* const ring = smem + (size_t)warp * STAGES * STAGE_BYTES;
-    const uint32_t ring_u32 = smem_u32(ring);
+    const AttnParams& p;
+    uint8_t* const ring;
+    uint32_t* const mask;   // [STAGES] visible positions of each stage's tile
+    const uint32_t ring_u32;
+    const int lane, c0, r0, vecs;
+    const int32_t rows_per_seq;
+    const int64_t v_minus_k;
+    AttnRow row;
+    int32_t head, tile, left;
+    int32_t page, slot;     // this lane's position in the next tile: its page (-1: masked) and slot
 
-    // the join's blocks may take their places as soon as this grid's are all running
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    // ---- units of all rows, and this block's range
-    const bool one_scan = p.batch <= kAttnThreads;  // every thread holds its own entry's units
-    int64_t total = 0, at = 0;
-    int32_t mine = 0;
-    if (one_scan) {
-        if ((int32_t)threadIdx.x < p.batch) mine = row_of<UNIT>(p, threadIdx.x).units;
-        at = block_scan(mine, &total, s_warp);
-    } else {
-        for (int32_t b = threadIdx.x; b < p.batch; b += kAttnThreads) total += row_of<UNIT>(p, b).units;
-        int64_t sum;
-        block_scan(total, &sum, s_warp);
-        total = sum;
-    }
-    const int64_t U = total * rows_per_seq;
-    const int64_t G = U < gridDim.x ? U : gridDim.x;
-    if (threadIdx.x == 0) p.desc[blockIdx.x].valid = 0;
-
-    // rows that see nothing: zeros, and a log-sum-exp of minus infinity
-    auto empty_rows = [&]() {
-        for (int32_t b = blockIdx.x; b < p.batch; b += gridDim.x) {
-            if (row_of<UNIT>(p, b).units != 0) continue;
-            for (int32_t i = threadIdx.x; i < p.q_heads * p.head_dim; i += kAttnThreads) {
-                const int32_t h = i / p.head_dim, d = i - h * p.head_dim;
-                reinterpret_cast<typename M::T*>(p.out)[b * p.ld_out + h * p.ld_oh + d] = M::from_float(0.f);
-            }
-            if (p.lse)
-                for (int32_t h = threadIdx.x; h < p.q_heads; h += kAttnThreads)
-                    p.lse[(int64_t)b * p.q_heads + h] = -CUDART_INF_F;
+    // `left` tiles from tile `tile` of row (row, head) on
+    __device__ __forceinline__ AttnLoader(const AttnParams& p_, uint8_t* ring_, uint32_t* mask_, const AttnRow& row_,
+                                          int32_t head_, int32_t tile_, int32_t left_)
+        : p(p_), ring(ring_), mask(mask_), ring_u32(sbt_ptx::smem_u32(ring_)), lane(threadIdx.x & 31),
+          c0((threadIdx.x & 31) % LPR), r0((threadIdx.x & 31) / LPR), vecs(p_.head_dim * ES / 16),
+          rows_per_seq(p_.kv_heads * p_.n_chunks), v_minus_k(p_.v - p_.k), row(row_), head(head_), tile(tile_),
+          left(left_) {
+        // columns past the head size stay zero for the whole call
+        if (p.head_dim < DP) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(ring);
+            for (int i = lane; i < STAGES * STAGE_BYTES / 4; i += 32) w[i] = 0;
+            __syncwarp();
         }
-    };
-    if (blockIdx.x >= G) {
-        empty_rows();
-        return;
+        look_up();
+#pragma unroll 1
+        for (int s = 0; s < STAGES - 1; ++s) step(s);
     }
 
-    const int64_t u0 = range_start(blockIdx.x, U, G), u1 = range_start(blockIdx.x + 1, U, G);
-
-    // ---- the sequence that holds unit u0
-    auto claim = [&](int32_t b) {
-        if (mine > 0 && at * rows_per_seq <= u0 && u0 < (at + mine) * rows_per_seq) {
-            s_start[0] = at * rows_per_seq;
-            s_start[1] = b;
-        }
-    };
-    if (one_scan) {
-        claim(threadIdx.x);
-    } else {
-        int64_t before = 0;
-        for (int32_t b0 = 0; b0 < p.batch && before * rows_per_seq <= u0; b0 += kAttnThreads) {
-            const int32_t b = b0 + threadIdx.x;
-            mine = b < p.batch ? row_of<UNIT>(p, b).units : 0;
-            int64_t sum;
-            at = before + block_scan(mine, &sum, s_warp);
-            claim(b);
-            before += sum;
-        }
-    }
-    __syncthreads();
-
-    // ---- loader state: runs up to STAGES units ahead of the math
-    AttnRow lr = row_of<UNIT>(p, (int32_t)s_start[1]);
-    int32_t l_head, l_tile;
-    {
-        const int64_t in = u0 - s_start[0];
-        l_head = (int32_t)(in / lr.units);
-        l_tile = (int32_t)(in - (int64_t)l_head * lr.units);
-    }
-    AttnRow cr = lr;  // math state
-    int32_t c_head = l_head, c_tile = l_tile;
-
-    auto next = [&](AttnRow& r, int32_t& head, int32_t& tile) {
-        if (++tile < r.units) return;
-        tile = 0;
-        if (++head < rows_per_seq) return;
-        head = 0;
+    // The tile after (r, h, t) on the line.
+    __device__ __forceinline__ void next(AttnRow& r, int32_t& h, int32_t& t) const {
+        if (++t < r.tiles) return;
+        t = 0;
+        if (++h < rows_per_seq) return;
+        h = 0;
         int32_t b = r.b + 1;
         while (b < p.batch) {
-            r = row_of<UNIT>(p, b);
-            if (r.units) break;
+            r = sbt_attn::row_of<TOK>(p, b);
+            if (r.tiles) break;
             ++b;
         }
-    };
-    // page of this lane's position in the loader's tile (-1: masked), and the position
-    auto page_index = [&](int32_t& slot) -> int32_t {
-        const int32_t pos = lr.base + l_tile * UNIT + warp * TOK + (lane & (TOK - 1));
-        slot = 0;
-        if (pos < lr.lo || pos >= lr.hi) return -1;
+    }
+
+    __device__ __forceinline__ void look_up() {
+        const int32_t pos = row.base + tile * TOK + (lane & (TOK - 1));
+        slot = 0, page = -1;
+        if (left <= 0 || pos < row.lo || pos >= row.hi) return;
         const uint32_t pg = sbt_div(p.page_size, (uint32_t)pos);
         slot = pos - (int32_t)(pg * p.page_size.d);
-        return __ldg(p.table + (int64_t)lr.seq * p.ld_table + pg);
-    };
-    auto issue = [&](int stage, int32_t page, int32_t slot, int32_t head) {
+        page = __ldg(p.table + (int64_t)row.seq * p.ld_table + pg);
+    }
+
+    // The query of a row, towards L2: the math reads it a tile or two later.
+    __device__ __forceinline__ void prefetch_q() const {
+        const int32_t kvh = head / p.n_chunks, h0 = (head - kvh * p.n_chunks) * p.chunk;
+        const int32_t heads = p.group - h0 < p.chunk ? p.group - h0 : p.chunk;
+        if (lane >= heads) return;
+        const char* x = p.q + (row.b * p.ld_q + (int64_t)(kvh * p.group + h0 + lane) * p.ld_qh) * ES;
+        for (int i = 0; i < p.head_dim * ES; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + i));
+    }
+
+    // Starts the next tile's copies into `stage`, then looks up the pages of the one after.
+    __device__ __forceinline__ void step(int stage) {
+        if (left > 0) {
+            issue(stage);
+            if (--left > 0) {
+                next(row, head, tile);
+                if (tile == 0) prefetch_q();
+            }
+            look_up();
+        }
+        sbt_attn::cp_commit();
+    }
+
+    __device__ __forceinline__ void issue(int stage) {
+        using namespace sbt_attn;
         const bool ok = page >= 0 && page < p.n_pages;
-        const int32_t kvh = head / p.n_chunks;
+        const int32_t kvh = p.n_chunks == 1 ? head : head / p.n_chunks;
         const int64_t off = ok ? (page * p.ld_page + slot * p.ld_slot + kvh * p.ld_head) * ES : -1;
-        const uint32_t bits = __ballot_sync(0xffffffffu, ok) & (TOK == 32 ? 0xffffffffu : (1u << (TOK & 31)) - 1u);
-        if (lane == 0) s_mask[warp][stage] = bits;
+        const uint32_t bits = __ballot_sync(0xffffffffu, ok) & ALL;
+        if (lane == 0) mask[stage] = bits;
         const uint32_t dst = ring_u32 + stage * STAGE_BYTES;
         if (bits == 0) return;  // the tile is skipped: nothing reads this stage
         if (p.copy_bytes == 16) {
-            const int vecs = p.head_dim * ES / 16;   // vectors of one row
-            constexpr int LPR = DP * ES / 16 < 32 ? DP * ES / 16 : 32;  // lanes on one row
-            constexpr int RPI = 32 / LPR;
-            const int c0 = lane % LPR, r0 = lane / LPR;
-#pragma unroll
-            for (int i = 0; i < TOK / RPI; ++i) {
+            // place of row i RPI + r0, vector v + c0, relative to the stage
+            auto place = [&](int i, int v) -> uint32_t {
                 const int t = i * RPI + r0;
-                const int64_t o = __shfl_sync(0xffffffffu, off, t);
+                return t * PITCH + (((v + c0) ^ M::swizzle(t)) << 4);
+            };
+            if (p.tile_in_page && bits == ALL) {
+                // every row of the tile follows the first at the slots' stride
+                const char* k = p.k + __shfl_sync(0xffffffffu, off, 0) + r0 * (p.ld_slot * ES) + c0 * 16;
+                const int64_t step = RPI * p.ld_slot * ES;
 #pragma unroll
-                for (int c = c0; c < DP * ES / 16; c += LPR) {
-                    if (c < vecs) {
-                        const int64_t a = o < 0 ? 0 : o + c * 16;
-                        const uint32_t at = t * PITCH + M::chunk16(t, c) * 16;
-                        cp_async16(dst + at, p.k + a, o < 0 ? 0 : 16);
-                        cp_async16(dst + TOK * PITCH + at, p.v + a, o < 0 ? 0 : 16);
-                    }
+                for (int i = 0; i < TOK / RPI; ++i) {
+#pragma unroll
+                    for (int v = 0; v < VECS; v += LPR)
+                        if (c0 + v < vecs) {
+                            cp_async16(dst + place(i, v), k + v * 16, 16);
+                            cp_async16(dst + TOK * PITCH + place(i, v), k + v_minus_k + v * 16, 16);
+                        }
+                    k += step;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < TOK / RPI; ++i) {
+                    const int64_t o = __shfl_sync(0xffffffffu, off, i * RPI + r0);
+                    const char* k = p.k + (o < 0 ? 0 : o) + c0 * 16;
+                    const int n = o < 0 ? 0 : 16;  // no byte is read of a masked row: zeros
+#pragma unroll
+                    for (int v = 0; v < VECS; v += LPR)
+                        if (c0 + v < vecs) {
+                            cp_async16(dst + place(i, v), k + v * 16, n);
+                            cp_async16(dst + TOK * PITCH + place(i, v), k + v_minus_k + v * 16, n);
+                        }
                 }
             }
         } else if (p.copy_bytes == 4) {
             const int words = p.head_dim * ES / 4;
             for (int t = 0; t < TOK; ++t) {
                 const int64_t o = __shfl_sync(0xffffffffu, off, t);
-                for (int c = lane; c < words; c += 32) {
-                    const int64_t a = o < 0 ? 0 : o + c * 4;
-                    const uint32_t at = t * PITCH + M::chunk16(t, c / 4) * 16 + (c & 3) * 4;
-                    cp_async4(dst + at, p.k + a, o < 0 ? 0 : 4);
-                    cp_async4(dst + TOK * PITCH + at, p.v + a, o < 0 ? 0 : 4);
+                for (int w = lane; w < words; w += 32) {
+                    const int64_t a = o < 0 ? 0 : o + w * 4;
+                    const uint32_t s = t * PITCH + (((w >> 2) ^ M::swizzle(t)) << 4) + (w & 3) * 4;
+                    cp_async4(dst + s, p.k + a, o < 0 ? 0 : 4);
+                    cp_async4(dst + TOK * PITCH + s, p.v + a, o < 0 ? 0 : 4);
                 }
             }
         } else if (ES == 2) {
             typedef typename M::T T;
             uint8_t* const st = ring + stage * STAGE_BYTES;
-            constexpr int V = 16 / ES;
             for (int t = 0; t < TOK; ++t) {
                 const int64_t o = __shfl_sync(0xffffffffu, off, t);
-                for (int c = lane; c < p.head_dim; c += 32) {
-                    const int at = t * PITCH + M::chunk16(t, c / V) * 16 + (c % V) * ES;
-                    *reinterpret_cast<T*>(st + at) = o < 0 ? T(0) : __ldg(reinterpret_cast<const T*>(p.k + o) + c);
-                    *reinterpret_cast<T*>(st + TOK * PITCH + at) =
-                        o < 0 ? T(0) : __ldg(reinterpret_cast<const T*>(p.v + o) + c);
+                for (int e = lane; e < p.head_dim; e += 32) {
+                    const int a = t * PITCH + (((e >> 3) ^ M::swizzle(t)) << 4) + (e & 7) * ES;
+                    *reinterpret_cast<T*>(st + a) = o < 0 ? T(0) : __ldg(reinterpret_cast<const T*>(p.k + o) + e);
+                    *reinterpret_cast<T*>(st + TOK * PITCH + a) =
+                        o < 0 ? T(0) : __ldg(reinterpret_cast<const T*>(p.v + o) + e);
                 }
             }
         }
-    };
-
-    // columns past the head size stay zero for the whole call
-    if (p.head_dim < DP) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(ring);
-        for (int i = lane; i < STAGES * STAGE_BYTES / 4; i += 32) w[i] = 0;
-        __syncwarp();
     }
 
-    // the query of a row the loader has reached, towards L2: the math reads it a few units later
-    auto prefetch_q = [&](const AttnRow& r, int32_t head) {
-        const int32_t kvh = head / p.n_chunks, h0 = (head - kvh * p.n_chunks) * p.chunk;
-        const int32_t heads = p.group - h0 < p.chunk ? p.group - h0 : p.chunk;
-        if (lane >= heads) return;
-        const char* x = p.q + (r.b * p.ld_q + (int64_t)(kvh * p.group + h0 + lane) * p.ld_qh) * ES;
-        for (int i = 0; i < p.head_dim * ES; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + i));
-    };
-
-    int64_t l_u = u0;
-    int32_t slot_next, page_next = page_index(slot_next);
-    auto load_step = [&](int stage) {  // issue the loader's unit, then look up the next one's pages
-        if (l_u < u1) {
-            issue(stage, page_next, slot_next, l_head);
-            if (++l_u < u1) {
-                next(lr, l_head, l_tile);
-                page_next = page_index(slot_next);
-                if (l_tile == 0 && warp == 0) prefetch_q(lr, l_head);
-            }
-        }
-        cp_commit();
-    };
-#pragma unroll 1
-    for (int s = 0; s < STAGES - 1; ++s) load_step(s);
-
-    M m;
-    m.load_q(p, cr, c_head, s_scratch);
-    int stage = 0;
-    int64_t row_u0 = u0 - c_tile;  // first unit of the current row on the line
-    bool row_cut = c_tile != 0;    // the row began in an earlier block
-    for (int64_t u = u0; u < u1; ++u) {
-        cp_wait<STAGES - 2>();
+    // Waits for the tile in `stage`, refills the stage the last step read, and does the math.
+    __device__ __forceinline__ void do_tile(M& m, int& stage, float* scratch) {
+        sbt_attn::cp_wait<STAGES - 2>();
         __syncwarp();
-        // the stage read in the last step is free: refill it before this step's math
-        load_step(stage == 0 ? STAGES - 1 : stage - 1);
-        const uint32_t bits = s_mask[warp][stage];
+        step(stage == 0 ? STAGES - 1 : stage - 1);
+        const uint32_t bits = mask[stage];
         if (bits) {
             const uint32_t k_s = ring_u32 + stage * STAGE_BYTES;
-            m.tile(p, ring + stage * STAGE_BYTES, k_s, k_s + TOK * PITCH, bits, s_scratch);
+            m.tile(p, ring + stage * STAGE_BYTES, k_s, k_s + TOK * PITCH, bits, scratch);
         }
         stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+};
 
-        const bool row_end = c_tile + 1 == cr.units;
-        if (row_end || u + 1 == u1) {
-            // ---- join the four warps
-            m.reduce();
-            m.put_ml(s_m[warp], s_l[warp]);
+// (m, l) of head h over `n` states, and each state's weight for element i of o.
+template <class M>
+__device__ __forceinline__ float attn_join(const float* o, const float2* ml, int64_t o_step, int ml_step, int n, int i,
+                                           float* top_out, float* l_out) {
+    const int h = i % M::HEADS;
+    float top = -CUDART_INF_F, l = 0.f, x = 0.f;
+    for (int w = 0; w < n; ++w) top = fmaxf(top, ml[w * ml_step + h].x);
+    const float ts = top == -CUDART_INF_F ? 0.f : top;
+    for (int w = 0; w < n; ++w) {
+        const float2 v = ml[w * ml_step + h];
+        const float a = sbt_attn::exp2_fast(v.x - ts);
+        l += v.y * a;
+        x += o[w * o_step + i] * a;
+    }
+    *top_out = top, *l_out = l;
+    return x;
+}
+
+template <class M, int STAGES, int WARPS, int BLOCKS>
+__global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention(const AttnParams p) {
+    using namespace sbt_attn;
+    typedef AttnLoader<M, STAGES> Loader;
+    constexpr int TOK = M::TOK, DP = M::DP, THREADS = 32 * WARPS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t s_warp[WARPS];
+    __shared__ int64_t s_first[THREADS];  // first tile of each batch entry of a scan step
+    __shared__ uint32_t s_mask[WARPS][STAGES];
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t rows_per_seq = p.kv_heads * p.n_chunks;
+    float* const scratch =
+        reinterpret_cast<float*>(smem + (size_t)WARPS * STAGES * Loader::STAGE_BYTES) + (size_t)warp * M::SCRATCH;
+    sbt_ptx::griddep_wait();
+
+    // ---- the line: tiles of all rows
+    const bool one_step = p.batch <= THREADS;  // every thread holds its own entry's tiles
+    int64_t total = 0, at = 0;
+    int32_t mine = 0;
+    if (one_step) {
+        if ((int32_t)threadIdx.x < p.batch) mine = row_of<TOK>(p, threadIdx.x).tiles;
+        at = block_scan<WARPS>(mine, &total, s_warp);
+    } else {
+        for (int32_t b = threadIdx.x; b < p.batch; b += THREADS) total += row_of<TOK>(p, b).tiles;
+        int64_t sum;
+        block_scan<WARPS>(total, &sum, s_warp);
+        total = sum;
+    }
+    const int64_t U = total * rows_per_seq;
+    const int64_t all_warps = (int64_t)gridDim.x * WARPS, G = U < all_warps ? U : all_warps;
+    const int64_t c = (int64_t)blockIdx.x * WARPS + warp;
+    const bool idle = c >= G;
+    const Line line(U, G > 0 ? G : 1);
+    const int64_t u0 = idle ? U : line.start(c), u1 = idle ? U : line.start(c + 1);
+
+    // ---- the batch entry that holds tile u0, and its first tile
+    int32_t b_first = 0;
+    int64_t u_first = 0;
+    {
+        int64_t before = 0;
+        for (int32_t b0 = 0; b0 < p.batch; b0 += THREADS) {
+            int64_t sum = total;
+            if (!one_step) {
+                const int32_t b = b0 + threadIdx.x;
+                mine = b < p.batch ? row_of<TOK>(p, b).tiles : 0;
+                at = before + block_scan<WARPS>(mine, &sum, s_warp);
+            }
+            s_first[threadIdx.x] = at * rows_per_seq;
             __syncthreads();
-            float top[M::OWN], own[M::OWN];
-            m.heads_max(s_m, top);
-#pragma unroll
-            for (int i = 0; i < M::OWN; ++i) own[i] = top[i] == -CUDART_INF_F ? 0.f : top[i];
-            m.rescale_to(own);
-            const int32_t kvh = c_head / p.n_chunks, chunk = c_head - kvh * p.n_chunks;
-            const bool whole = row_end && !row_cut;
-            const int part_slot = row_cut || row_u0 == u0 ? 0 : 1;
-            const int32_t h0 = chunk * p.chunk;
-            const int32_t heads = p.group - h0 < p.chunk ? p.group - h0 : p.chunk;
-            constexpr int HB = M::MERGE_HEADS;  // heads per pass through the merge buffer
-#pragma unroll
-            for (int hb = 0; hb < HEADS; hb += HB) {
-                if (hb >= heads) break;
-                m.put_o(s_merge + (size_t)warp * HB * MERGE_PITCH, MERGE_PITCH, hb);
-                __syncthreads();
-                for (int i = threadIdx.x; i < HB * (DP / 4); i += kAttnThreads) {
-                    const int h = i / (DP / 4), d = (i - h * (DP / 4)) * 4, head = hb + h;
-                    if (head >= heads) break;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float mm = -CUDART_INF_F, ll = 0.f;
-#pragma unroll
-                    for (int w = 0; w < kAttnWarps; ++w) mm = fmaxf(mm, s_m[w][head]);
-                    const float ms = mm == -CUDART_INF_F ? 0.f : mm;
-#pragma unroll
-                    for (int w = 0; w < kAttnWarps; ++w) {
-                        const float4 x = *reinterpret_cast<const float4*>(s_merge + ((size_t)w * HB + h) * MERGE_PITCH + d);
-                        o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
-                        ll += s_l[w][head] * exp2_fast(s_m[w][head] - ms);
-                    }
-                    const int32_t qh = kvh * p.group + h0 + head;
-                    if (whole) {
-                        const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
-                        typename M::T* dst =
-                            reinterpret_cast<typename M::T*>(p.out) + cr.b * p.ld_out + qh * p.ld_oh + d;
-                        if (d + 0 < p.head_dim) dst[0] = M::from_float(o.x * inv);
-                        if (d + 1 < p.head_dim) dst[1] = M::from_float(o.y * inv);
-                        if (d + 2 < p.head_dim) dst[2] = M::from_float(o.z * inv);
-                        if (d + 3 < p.head_dim) dst[3] = M::from_float(o.w * inv);
-                        if (d == 0 && p.lse)
-                            p.lse[(int64_t)cr.b * p.q_heads + qh] =
-                                ll == 0.f ? -CUDART_INF_F : (mm + log2f(ll)) * 0.6931471805599453f;
-                    } else {
-                        const int64_t s = 2 * (int64_t)blockIdx.x + part_slot;
-                        *reinterpret_cast<float4*>(p.part_o + (s * HEADS + head) * DP + d) = o;
-                        if (d == 0) p.part_ml[s * kAttnMaxHeads + head] = make_float2(mm, ll);
+            if (!idle && before * rows_per_seq <= u0 && u0 < (before + sum) * rows_per_seq) {
+                for (int i = lane; i < THREADS; i += 32) {
+                    const int64_t end = i + 1 < THREADS ? s_first[i + 1] : (before + sum) * rows_per_seq;
+                    const uint32_t hit = __ballot_sync(0xffffffffu, s_first[i] <= u0 && u0 < end);
+                    if (hit) {
+                        b_first = b0 + (i & ~31) + __ffs(hit) - 1;
+                        u_first = s_first[(i & ~31) + __ffs(hit) - 1];
                     }
                 }
-                __syncthreads();
             }
-            if (!whole && !row_cut && threadIdx.x == 0) {
-                AttnDesc e;
-                e.valid = 1, e.b = cr.b, e.kvh = kvh, e.chunk = chunk;
-                e.first = blockIdx.x;
-                e.last = block_of(row_u0 + cr.units - 1, U, G);
-                e.first_slot = part_slot;
-                e.pad = 0;
-                p.desc[blockIdx.x] = e;
+            __syncthreads();
+            before += sum;
+        }
+    }
+
+    // ---- rows that see nothing: zeros, and a log-sum-exp of minus infinity
+    auto empty_rows = [&]() {
+        for (int64_t b = c; b < p.batch; b += all_warps) {
+            if (row_of<TOK>(p, (int32_t)b).tiles != 0) continue;
+            for (int32_t i = lane; i < p.q_heads * p.head_dim; i += 32) {
+                const int32_t h = i / p.head_dim, d = i - h * p.head_dim;
+                reinterpret_cast<typename M::T*>(p.out)[b * p.ld_out + h * p.ld_oh + d] = typename M::T(0);
             }
-            if (u + 1 < u1) {
-                row_u0 = u + 1;
-                row_cut = false;
-                next(cr, c_head, c_tile);
-                m.load_q(p, cr, c_head, s_scratch);
-            }
-        } else {
+            if (p.lse)
+                for (int32_t h = lane; h < p.q_heads; h += 32) p.lse[b * p.q_heads + h] = -CUDART_INF_F;
+            if (p.desc_by_row)
+                for (int32_t h = lane; h < rows_per_seq; h += 32) p.desc[b * rows_per_seq + h].valid = 0;
+        }
+    };
+    if (!p.desc_by_row && lane == 0) p.desc[c].valid = 0;
+    if (idle) {
+        empty_rows();
+        return;
+    }
+
+    // ---- this warp's tiles
+    AttnRow cr = row_of<TOK>(p, b_first);
+    int32_t c_head = (int32_t)divide(u0 - u_first, cr.tiles);
+    int32_t c_tile = (int32_t)((u0 - u_first) - (int64_t)c_head * cr.tiles);
+    int32_t to_do = (int32_t)(u1 - u0);
+    Loader loader(p, smem + (size_t)warp * STAGES * Loader::STAGE_BYTES, s_mask[warp], cr, c_head, c_tile, to_do);
+
+    // block B lies wholly inside a row that covers the tiles [a, e) of the line
+    auto inside = [&](int64_t B, int64_t a, int64_t e) {
+        return (B + 1) * WARPS <= G && a <= line.start(B * WARPS) && e >= line.start((B + 1) * WARPS);
+    };
+
+    M m;
+    m.load_q(p, cr, c_head, scratch);
+    int stage = 0;
+    bool first = true;           // the current row is the range's first
+    bool cut = c_tile != 0;      // it began in an earlier range
+    bool join_block = false;     // this block's warps join their parts
+#pragma unroll 1
+    while (to_do-- > 0) {
+        loader.do_tile(m, stage, scratch);
+        const bool row_end = c_tile + 1 == cr.tiles;
+        if (!row_end && to_do > 0) {
             ++c_tile;
+            continue;
+        }
+        const int32_t kvh = c_head / p.n_chunks, chunk = c_head - kvh * p.n_chunks, h0 = chunk * p.chunk;
+        const int32_t heads = p.group - h0 < p.chunk ? p.group - h0 : p.chunk, qh = kvh * p.group + h0;
+        AttnDesc e;
+        e.valid = 0;
+        if (row_end && !cut) {
+            m.put_row(p, cr.b, qh, heads);
+        } else {
+            const int slot = first ? 0 : 1;
+            const int64_t row_a = u1 - 1 - to_do - c_tile, row_e = row_a + cr.tiles;  // the row on the line
+            join_block = first && to_do == 0 && inside(blockIdx.x, row_a, row_e);
+            if (!join_block)
+                m.put_part(p.part_o + (2 * c + slot) * M::HEADS * DP, p.part_ml + (2 * c + slot) * M::HEADS);
+            if (!cut) {
+                e.valid = 1, e.b = cr.b, e.kvh = kvh, e.chunk = chunk;
+                e.first = (int32_t)c, e.first_slot = slot;
+                e.last = line.warp_of(row_e - 1);
+                e.joined = (inside(blockIdx.x, row_a, row_e) ? 1 : 0) | (inside(e.last / WARPS, row_a, row_e) ? 2 : 0);
+            }
+        }
+        if (!cut && lane == 0) {
+            if (p.desc_by_row)
+                p.desc[(int64_t)cr.b * rows_per_seq + c_head] = e;
+            else if (e.valid)
+                p.desc[c] = e;
+        }
+        if (to_do > 0) {
+            first = cut = false;
+            loader.next(cr, c_head, c_tile);
+            m.load_q(p, cr, c_head, scratch);
+        }
+    }
+    if (join_block) {  // the same for all warps of the block; the ring is free
+        constexpr int N = M::HEADS * DP;
+        float* const s_o = reinterpret_cast<float*>(smem);
+        float2* const s_ml = reinterpret_cast<float2*>(s_o + WARPS * N);
+        cp_wait<0>();
+        __syncthreads();
+        m.put_part(s_o + warp * N, s_ml + warp * M::HEADS);
+        __syncthreads();
+        const int64_t slot = 2 * (int64_t)blockIdx.x * WARPS;
+        for (int i = threadIdx.x; i < N; i += THREADS) {
+            float top, l;
+            p.part_o[slot * N + i] = attn_join<M>(s_o, s_ml, N, M::HEADS, WARPS, i, &top, &l);
+            if (i < M::HEADS) p.part_ml[slot * M::HEADS + i] = make_float2(top, l);
         }
     }
     empty_rows();
 }
 
-// Joins the parts of the rows that block borders cut, in block order.  Block
-// (c, y) looks at the row that began in block c, if one did.  Up to
-// kJoinFew parts (rows are many): blocks with y % 8 == 0 give a warp to each of
-// eight heads.  More parts (rows are few): block y takes head y, its
-// eight warps the parts in turn, and the warps meet in shared memory.
-constexpr int kJoinFew = 64;
-
-template <class T, T (*FROM)(float), int HEADS, int DP>
-__global__ void __launch_bounds__(256) k_attention_join(const AttnParams p) {
+// Few rows that are not long: a cluster of p.cluster blocks per row, whose warps
+// take its tiles evenly and join their states through distributed shared
+// memory.  One launch, no workspace and no prefix sum; but a long row has only
+// one cluster's warps.
+template <class M, int STAGES, int WARPS, int BLOCKS>
+__global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention_cluster(const AttnParams p) {
     using namespace sbt_attn;
-    constexpr int NV = (DP + 127) / 128;  // float4s of a head per lane
-    __shared__ float s_l[8];
-    __shared__ float4 s_o[8][NV][32];
+    namespace cg = cooperative_groups;
+    typedef AttnLoader<M, STAGES> Loader;
+    constexpr int N = M::HEADS * M::DP, THREADS = 32 * WARPS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint32_t s_mask[WARPS][STAGES];
+    const int warp = threadIdx.x >> 5;
+    const int32_t rows_per_seq = p.kv_heads * p.n_chunks, ranks = p.cluster, rank = blockIdx.x % ranks;
+    const int32_t b = (int32_t)(blockIdx.x / ranks) / rows_per_seq;
+    const int32_t head = (int32_t)(blockIdx.x / ranks) - b * rows_per_seq;
+    float* const scratch =
+        reinterpret_cast<float*>(smem + (size_t)WARPS * STAGES * Loader::STAGE_BYTES) + (size_t)warp * M::SCRATCH;
     sbt_ptx::griddep_wait();
-    const AttnDesc e = p.desc[blockIdx.x];
-    if (!e.valid) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n = e.last - e.first + 1;
-    const bool few = n <= kJoinFew;
-    if (few && (blockIdx.y & 7)) return;
-    const int32_t h0 = e.chunk * p.chunk;
+    const AttnRow row = row_of<M::TOK>(p, b);
+    const int32_t w = WARPS * ranks, me = rank * WARPS + warp, size = row.tiles / w, more = row.tiles - size * w;
+    const int32_t mine = size + (me < more);
+    Loader loader(p, smem + (size_t)warp * STAGES * Loader::STAGE_BYTES, s_mask[warp], row, head,
+                  me * size + min(me, more), mine);
+    M m;
+    m.load_q(p, row, head, scratch);
+    int stage = 0;
+#pragma unroll 1
+    for (int32_t i = 0; i < mine; ++i) loader.do_tile(m, stage, scratch);
+
+    // the block's warps, then the cluster's blocks: each block finishes a share of the elements
+    float* const s_o = reinterpret_cast<float*>(smem);            // [WARPS][N], then [N] of the block
+    float2* const s_ml = reinterpret_cast<float2*>(s_o + (WARPS + 1) * N);
+    float* const b_o = s_o + WARPS * N;
+    float2* const b_ml = s_ml + WARPS * M::HEADS;
+    cp_wait<0>();
+    __syncthreads();
+    m.put_part(s_o + warp * N, s_ml + warp * M::HEADS);
+    __syncthreads();
+    for (int i = threadIdx.x; i < N; i += THREADS) {
+        float top, l;
+        b_o[i] = attn_join<M>(s_o, s_ml, N, M::HEADS, WARPS, i, &top, &l);
+        if (i < M::HEADS) b_ml[i] = make_float2(top, l);
+    }
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    const int32_t kvh = head / p.n_chunks, h0 = (head - kvh * p.n_chunks) * p.chunk;
     const int32_t heads = p.group - h0 < p.chunk ? p.group - h0 : p.chunk;
-    const int head = few ? blockIdx.y + warp : blockIdx.y;
-    const int i0 = few ? 0 : warp, di = few ? 1 : 8;
-    if (head >= heads) return;  // the whole block, unless each warp is by itself
-    auto slot = [&](int i) -> int64_t { return 2 * (int64_t)(e.first + i) + (i == 0 ? e.first_slot : 0); };
-
-    float mm = -CUDART_INF_F;
-    for (int i = lane; i < n; i += 32) mm = fmaxf(mm, p.part_ml[slot(i) * kAttnMaxHeads + head].x);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-    const float ms = mm == -CUDART_INF_F ? 0.f : mm;
-
-    float4 o[NV];
-    float l = 0.f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = i0; i < n; i += di) {
-        const int64_t s = slot(i);
-        const float2 ml = p.part_ml[s * kAttnMaxHeads + head];
-        const float w = exp2_fast(ml.x - ms);
-        l += ml.y * w;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int d = v * 128 + lane * 4;
-            if (d < DP) {
-                const float4 x = *reinterpret_cast<const float4*>(p.part_o + (s * HEADS + head) * DP + d);
-                o[v].x += x.x * w, o[v].y += x.y * w, o[v].z += x.z * w, o[v].w += x.w * w;
-            }
+    for (int i = rank * THREADS + threadIdx.x; i < N; i += ranks * THREADS) {
+        const int h = i % M::HEADS, d = i / M::HEADS;
+        if (h >= heads || d >= p.head_dim) continue;
+        float top = -CUDART_INF_F, l = 0.f, x = 0.f;
+        for (int r = 0; r < ranks; ++r) {
+            const float2 ml = *cluster.map_shared_rank(b_ml + h, r);
+            const float o = *cluster.map_shared_rank(b_o + i, r);
+            const float t = fmaxf(top, ml.x), ts = t == -CUDART_INF_F ? 0.f : t;
+            const float a = exp2_fast(top - ts), c = exp2_fast(ml.x - ts);
+            top = t;
+            l = l * a + ml.y * c;
+            x = x * a + o * c;
         }
+        const int32_t qh = kvh * p.group + h0 + h;
+        reinterpret_cast<typename M::T*>(p.out)[b * p.ld_out + qh * p.ld_oh + d] = M::from_float(x * inverse(l));
+        if (d == 0 && p.lse) p.lse[(int64_t)b * p.q_heads + qh] = log_sum(top, l);
     }
-    if (!few) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) s_o[warp][v][lane] = o[v];
-        if (lane == 0) s_l[warp] = l;
-        __syncthreads();
-        if (warp != 0) return;
-#pragma unroll
-        for (int w = 1; w < 8; ++w) {
-            l += s_l[w];
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const float4 x = s_o[w][v][lane];
-                o[v].x += x.x, o[v].y += x.y, o[v].z += x.z, o[v].w += x.w;
-            }
-        }
-    }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    const int32_t qh = e.kvh * p.group + h0 + head;
-    T* const dst = reinterpret_cast<T*>(p.out) + e.b * p.ld_out + qh * p.ld_oh;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int d = v * 128 + lane * 4;
-        if (d + 0 < p.head_dim) dst[d + 0] = FROM(o[v].x * inv);
-        if (d + 1 < p.head_dim) dst[d + 1] = FROM(o[v].y * inv);
-        if (d + 2 < p.head_dim) dst[d + 2] = FROM(o[v].z * inv);
-        if (d + 3 < p.head_dim) dst[d + 3] = FROM(o[v].w * inv);
-    }
-    if (lane == 0 && p.lse)
-        p.lse[(int64_t)e.b * p.q_heads + qh] = l == 0.f ? -CUDART_INF_F : (mm + log2f(l)) * 0.6931471805599453f;
+    cluster.sync();  // no block leaves while another reads its shared memory
 }
 
-// Enqueues the kernel and the join for one instantiation.
-template <class M, int STAGES>
-sbt_status sbt_attention_enqueue(sbt_context* ctx, const AttnParams& p, cudaStream_t stream) {
-    constexpr int HB = M::MERGE_HEADS;
-    constexpr size_t smem = (size_t)kAttnWarps * STAGES * 2 * M::TOK * M::PITCH +
-                            (size_t)kAttnWarps * HB * (M::DP + 4) * sizeof(float) + M::SCRATCH_BYTES;
-    sbt_status st;
-    int grid = sbt_resident_blocks<k_paged_attention<M, STAGES>>(ctx, kAttnThreads, smem);
-    if (grid > ctx->sm_count * kAttnMaxPerSm) grid = ctx->sm_count * kAttnMaxPerSm;
-    k_paged_attention<M, STAGES><<<grid, kAttnThreads, smem, stream>>>(p);
-    if ((st = sbt_after_launch(ctx, "paged_attention"))) return st;
-    const int heads = p.group < p.chunk ? p.group : p.chunk;
-    if ((st = sbt_cuda_check(sbt_launch_dependent(k_attention_join<typename M::T, M::from_float, M::HEADS, M::DP>,
-                                                  dim3(grid, heads), dim3(256), 0, stream, p),
-                             "paged_attention join launch")))
-        return st;
+// Joins the parts of one cut row, in the order of the line.  Block (i, y) takes
+// the i-th descriptor.  Up to kJoinFew parts (the rule among many rows): a
+// float4 of the [DP][HEADS] state per thread, the blocks y = 0, 1, .. that this
+// takes.  More parts: 64 float4s per block, and GROUPS groups of 64 threads go
+// through the parts side by side, each with its running maximum, and meet in
+// shared memory.
+constexpr int kJoinFew = 8;
+
+template <class M, int WARPS, int GROUPS>
+__global__ void __launch_bounds__(64 * GROUPS) k_attention_join(const AttnParams p) {
+    using namespace sbt_attn;
+    constexpr int HEADS = M::HEADS, DP = M::DP, MH = HEADS < 4 ? HEADS : 4;  // MH: different heads in one float4
+    __shared__ float s_m[GROUPS][64][MH], s_l[GROUPS][64][MH];
+    __shared__ float4 s_o[GROUPS][64];
+    sbt_ptx::griddep_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const AttnDesc e = p.desc[blockIdx.x];
+    if (!e.valid) return;
+    // parts of the first's block, of the blocks between, of the last's
+    const int bf = e.first / WARPS, bl = e.last / WARPS;
+    const int nf = (e.joined & 1) ? 1 : min(e.last, bf * WARPS + WARPS - 1) - e.first + 1;
+    const int nb = bl > bf ? bl - bf - 1 : 0;
+    const int nl = bl == bf ? 0 : (e.joined & 2) ? 1 : e.last - bl * WARPS + 1;
+    const int n = nf + nb + nl;
+    const bool few = n <= kJoinFew;
+    const int t = few ? threadIdx.x : threadIdx.x & 63, g = few ? 0 : threadIdx.x >> 6, dg = few ? 1 : GROUPS;
+    const int at = (blockIdx.y * (few ? 64 * GROUPS : 64) + t) * 4, head = at % HEADS;  // of the float4's first element
+    const bool in = at < DP * HEADS;
+    if (few && !in) return;
+    auto slot = [&](int i) -> int64_t {
+        if (i < nf) return (e.joined & 1) ? 2ll * bf * WARPS : 2ll * (e.first + i) + (i == 0 ? e.first_slot : 0);
+        i -= nf;
+        return i < nb ? 2ll * (bf + 1 + i) * WARPS : 2ll * (bl * WARPS + i - nb);
+    };
+    float m[MH], l[MH];
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < MH; ++k) m[k] = -CUDART_INF_F, l[k] = 0.f;
+    auto add = [&](const float* pm, const float* pl, const float4& x) {
+        const float px[4] = {x.x, x.y, x.z, x.w};
+        float a[MH], b[MH];
+#pragma unroll
+        for (int k = 0; k < MH; ++k) {
+            const float top = fmaxf(m[k], pm[k]), ts = top == -CUDART_INF_F ? 0.f : top;
+            a[k] = exp2_fast(m[k] - ts), b[k] = exp2_fast(pm[k] - ts);
+            m[k] = top;
+            l[k] = l[k] * a[k] + pl[k] * b[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = o[k] * a[k % MH] + px[k] * b[k % MH];
+    };
+    if (in)
+#pragma unroll 4
+        for (int i = g; i < n; i += dg) {
+            const int64_t s = slot(i);
+            float pm[MH], pl[MH];
+#pragma unroll
+            for (int k = 0; k < MH; ++k) {
+                const float2 ml = p.part_ml[s * HEADS + head + k];
+                pm[k] = ml.x, pl[k] = ml.y;
+            }
+            add(pm, pl, *reinterpret_cast<const float4*>(p.part_o + s * HEADS * DP + at));
+        }
+    if (!few) {
+#pragma unroll
+        for (int k = 0; k < MH; ++k) s_m[g][t][k] = m[k], s_l[g][t][k] = l[k];
+        s_o[g][t] = make_float4(o[0], o[1], o[2], o[3]);
+        __syncthreads();
+    }
+    if (g != 0 || !in) return;
+    if (!few)
+        for (int w = 1; w < GROUPS; ++w) add(s_m[w][t], s_l[w][t], s_o[w][t]);
+    const int32_t h0 = e.chunk * p.chunk, heads = p.group - h0 < p.chunk ? p.group - h0 : p.chunk;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int h = (at + k) % HEADS, d = (at + k) / HEADS;
+        if (h >= heads || d >= p.head_dim) continue;
+        const int32_t qh = e.kvh * p.group + h0 + h;
+        reinterpret_cast<typename M::T*>(p.out)[e.b * p.ld_out + qh * p.ld_oh + d] =
+            M::from_float(o[k] * inverse(l[k % MH]));
+        if (d == 0 && p.lse) p.lse[(int64_t)e.b * p.q_heads + qh] = log_sum(m[k % MH], l[k % MH]);
+    }
+}
+
+// Enqueues the kernel and the join, or the cluster form, for one instantiation.
+template <class M, int STAGES, int WARPS, int BLOCKS>
+sbt_status sbt_attention_enqueue(sbt_context* ctx, AttnParams p, cudaStream_t stream) {
+    constexpr size_t ring = (size_t)WARPS * (STAGES * 2 * M::TOK * M::PITCH + M::SCRATCH * sizeof(float));
+    constexpr size_t states = (size_t)(WARPS + 1) * M::HEADS * (M::DP * sizeof(float) + sizeof(float2));
+    constexpr size_t smem = ring > states ? ring : states;
+    p.tile_in_page = p.page_size.d % M::TOK == 0;
+    const int resident = sbt_resident_blocks<k_paged_attention<M, STAGES, WARPS, BLOCKS>>(ctx, 32 * WARPS, smem);
+    const int64_t rows = (int64_t)p.batch * p.kv_heads * p.n_chunks;
+    // The longest row there can be, in tiles.
+    const int64_t longest = sbt_cdiv(p.window > 0 && p.window < p.max_len ? (int64_t)p.window + M::TOK : p.max_len, M::TOK);
+    // A cluster per row where all clusters fit at once and a warp gets kClusterTiles tiles at most: below
+    // that the second launch and the way through memory cost more than uneven work.
+    int ranks = kClusterMost;
+    while (ranks > 1 && rows * ranks > resident) ranks >>= 1;
+    while (ranks > 1 && (ranks >> 1) * WARPS >= longest) ranks >>= 1;
+    if (rows * ranks <= resident && longest <= (int64_t)ranks * WARPS * kClusterTiles) {
+        p.cluster = ranks;
+        sbt_resident_blocks<k_paged_attention_cluster<M, STAGES, WARPS, BLOCKS>>(ctx, 32 * WARPS, smem);
+        if (sbt_status st = sbt_cuda_check(
+                sbt_launch_dependent_cluster(k_paged_attention_cluster<M, STAGES, WARPS, BLOCKS>,
+                                             dim3((unsigned)(rows * ranks)), dim3(32 * WARPS), (unsigned)ranks, smem,
+                                             stream, p),
+                "paged_attention launch"))
+            return st;
+        return sbt_after_launch(ctx, "paged_attention");
+    }
+    const int most = ctx->sm_count * kAttnMaxWarps / WARPS, grid = resident < most ? resident : most;
+    p.desc_by_row = rows <= (int64_t)grid * WARPS;
+    sbt_status st = sbt_cuda_check(sbt_launch_dependent(k_paged_attention<M, STAGES, WARPS, BLOCKS>, dim3(grid),
+                                                        dim3(32 * WARPS), smem, stream, p),
+                                   "paged_attention launch");
+    if (st || (st = sbt_after_launch(ctx, "paged_attention"))) return st;
+    // few rows may have many parts each: more groups
+    const dim3 join((unsigned)(p.desc_by_row ? rows : (int64_t)grid * WARPS), (M::DP * M::HEADS + 255) / 256);
+    const cudaError_t err =
+        rows <= 64 ? sbt_launch_dependent(k_attention_join<M, WARPS, 16>, join, dim3(1024), 0, stream, p)
+                   : sbt_launch_dependent(k_attention_join<M, WARPS, 4>, join, dim3(256), 0, stream, p);
+    if ((st = sbt_cuda_check(err, "paged_attention join launch"))) return st;
     return sbt_after_launch(ctx, "paged_attention join");
 }
 

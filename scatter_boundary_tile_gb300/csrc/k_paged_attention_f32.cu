@@ -12,12 +12,12 @@ namespace {
 template <int DP_, int HT>
 struct Fma32 {
     typedef float T;
-    static constexpr int ES = 4, TOK = 8, DP = DP_, HEADS = HT, OWN = HT;
-    static constexpr int PITCH = DP * 4 + 64;  // two rows of four 16-byte pieces fill the banks
-    static constexpr int MERGE_HEADS = HT < 4 ? HT : 4;
+    static constexpr int ES = 4, TOK = 8, DP = DP_, HEADS = HT;
+    static constexpr int PITCH = DP * 4;
+    // scores read four 16-byte pieces of two rows at once: of odd rows the other half of the banks
+    static __device__ __forceinline__ int swizzle(int t) { return (t & 1) << 2; }
     static constexpr int EL = DP / 32;         // head elements per lane
-    static constexpr int SCRATCH_BYTES = (HT * DP + kAttnWarps * TOK * HT) * 4;
-    static __device__ __forceinline__ int chunk16(int, int c) { return c; }
+    static constexpr int SCRATCH = HT * DP + TOK * HT;  // the query, and a tile's probabilities
     static __device__ __forceinline__ float from_float(float x) { return x; }
 
     float o[HT][EL];
@@ -27,7 +27,8 @@ struct Fma32 {
         const int32_t kvh = row / p.n_chunks, h0 = (row - kvh * p.n_chunks) * p.chunk;
         const int32_t heads = p.group - h0 < p.chunk ? p.group - h0 : p.chunk;
         const float* base = reinterpret_cast<const float*>(p.q) + r.b * p.ld_q + (kvh * p.group + h0) * p.ld_qh;
-        for (int i = threadIdx.x; i < HT * DP; i += kAttnThreads) {
+        __syncwarp();  // the last tile's reads
+        for (int i = threadIdx.x & 31; i < HT * DP; i += 32) {
             const int h = i / DP, d = i - h * DP;
             s_q[i] = h < heads && d < p.head_dim ? __ldg(base + h * p.ld_qh + d) : 0.f;
         }
@@ -38,20 +39,21 @@ struct Fma32 {
 #pragma unroll
             for (int e = 0; e < EL; ++e) o[h][e] = 0.f;
         }
-        __syncthreads();
+        __syncwarp();
     }
 
     __device__ __forceinline__ void tile(const AttnParams& p, const uint8_t* stage, uint32_t, uint32_t, uint32_t bits,
                                          float* s_q) {
         const int lane = threadIdx.x & 31, t = lane >> 2, part = lane & 3;
-        float* const s_p = s_q + HT * DP + (threadIdx.x >> 5) * TOK * HT;
-        const float* kr = reinterpret_cast<const float*>(stage + t * PITCH) + part * 4;
+        float* const s_p = s_q + HT * DP;
+        const uint8_t* const kr = stage + t * PITCH;
+        const int k_x = part ^ swizzle(t);
         float s[HT];
 #pragma unroll
         for (int h = 0; h < HT; ++h) s[h] = 0.f;
 #pragma unroll 4
         for (int i = 0; i < DP / 16; ++i) {
-            const float4 k4 = *reinterpret_cast<const float4*>(kr + i * 16);
+            const float4 k4 = *reinterpret_cast<const float4*>(kr + ((i * 4) ^ k_x) * 16);
 #pragma unroll
             for (int h = 0; h < HT; ++h) {
                 const float4 q4 = *reinterpret_cast<const float4*>(s_q + h * DP + i * 16 + part * 4);
@@ -82,13 +84,19 @@ struct Fma32 {
         __syncwarp();
 #pragma unroll
         for (int tt = 0; tt < TOK; ++tt) {
-            const float* vr = reinterpret_cast<const float*>(stage + (TOK + tt) * PITCH) + lane * EL;
+            const uint8_t* const vr = stage + (TOK + tt) * PITCH;
             float v[EL], w[HT];
-            if (EL % 4 == 0) {
+            constexpr int N = EL % 4 == 0 ? 4 : EL % 2 == 0 ? 2 : 1;  // elements per read
 #pragma unroll
-                for (int e = 0; e < EL; e += 4) *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(vr + e);
-            } else {
-                *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(vr);
+            for (int e = 0; e < EL; e += N) {
+                const int at = lane * EL + e;
+                const uint8_t* x = vr + (((at >> 2) ^ swizzle(tt)) << 4) + (at & 3) * 4;
+                if (N == 4)
+                    *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(x);
+                else if (N == 2)
+                    *reinterpret_cast<float2*>(v + e) = *reinterpret_cast<const float2*>(x);
+                else
+                    v[e] = *reinterpret_cast<const float*>(x);
             }
 #pragma unroll
             for (int h = 0; h < HT; ++h) w[h] = s_p[tt * HT + h];
@@ -100,7 +108,7 @@ struct Fma32 {
         __syncwarp();
     }
 
-    __device__ __forceinline__ void reduce() {
+    __device__ __forceinline__ void finish() {
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 4);
@@ -108,53 +116,50 @@ struct Fma32 {
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 16);
         }
     }
-    __device__ __forceinline__ void put_ml(float* m, float* sum) const {
-        if ((threadIdx.x & 31) == 0)
-#pragma unroll
-            for (int h = 0; h < HT; ++h) {
-                m[h] = mx[h];
-                sum[h] = l[h];
-            }
-    }
-    __device__ __forceinline__ void heads_max(const float (*s_m)[HEADS], float* top) const {
-#pragma unroll
-        for (int h = 0; h < HT; ++h) {
-            top[h] = -CUDART_INF_F;
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) top[h] = fmaxf(top[h], s_m[w][h]);
-        }
-    }
-    __device__ __forceinline__ void rescale_to(const float* top) {
-#pragma unroll
-        for (int h = 0; h < HT; ++h) {
-            const float a = sbt_attn::exp2_fast(mx[h] - top[h]);
-#pragma unroll
-            for (int e = 0; e < EL; ++e) o[h][e] *= a;
-        }
-    }
-    __device__ __forceinline__ void put_o(float* dst, int pitch, int hb) const {
+
+    __device__ __forceinline__ void put_row(const AttnParams& p, int32_t b, int32_t qh, int32_t heads) {
+        finish();
         const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int h = 0; h < HT; ++h)
-            if (h >= hb && h < hb + MERGE_HEADS)
+        for (int h = 0; h < HT; ++h) {
+            if (h >= heads) break;
+            const float inv = sbt_attn::inverse(l[h]);
+            float* dst = reinterpret_cast<float*>(p.out) + b * p.ld_out + (int64_t)(qh + h) * p.ld_oh;
 #pragma unroll
-                for (int e = 0; e < EL; ++e) dst[(h - hb) * pitch + lane * EL + e] = o[h][e];
+            for (int e = 0; e < EL; ++e)
+                if (lane * EL + e < p.head_dim) dst[lane * EL + e] = o[h][e] * inv;
+            if (p.lse && lane == 0) p.lse[(int64_t)b * p.q_heads + qh + h] = sbt_attn::log_sum(mx[h], l[h]);
+        }
+    }
+
+    // the state to dst [DP][HEADS] and ml [HEADS]
+    __device__ __forceinline__ void put_part(float* dst, float2* ml) {
+        finish();
+        const int lane = threadIdx.x & 31;
+        dst += lane * EL * HT;
+#pragma unroll
+        for (int e = 0; e < EL; ++e)
+#pragma unroll
+            for (int h = 0; h < HT; ++h) dst[e * HT + h] = o[h][e];
+        if (lane == 0)
+#pragma unroll
+            for (int h = 0; h < HT; ++h) ml[h] = make_float2(mx[h], l[h]);
     }
 };
 
-template <int DP, int STAGES>
+template <int DP, int STAGES, int WARPS, int BLOCKS>
 sbt_status by_heads(sbt_context* ctx, const AttnParams& p, cudaStream_t stream) {
-    const int heads = p.group < p.chunk ? p.group : p.chunk;
-    if (heads <= 1) return sbt_attention_enqueue<Fma32<DP, 1>, STAGES>(ctx, p, stream);
-    if (heads <= 2) return sbt_attention_enqueue<Fma32<DP, 2>, STAGES>(ctx, p, stream);
-    if (heads <= 4) return sbt_attention_enqueue<Fma32<DP, 4>, STAGES>(ctx, p, stream);
-    return sbt_attention_enqueue<Fma32<DP, 8>, STAGES>(ctx, p, stream);
+    if (p.chunk <= 1) return sbt_attention_enqueue<Fma32<DP, 1>, STAGES, WARPS, BLOCKS>(ctx, p, stream);
+    if (p.chunk <= 2) return sbt_attention_enqueue<Fma32<DP, 2>, STAGES, WARPS, BLOCKS>(ctx, p, stream);
+    if (p.chunk <= 4) return sbt_attention_enqueue<Fma32<DP, 4>, STAGES, WARPS, BLOCKS>(ctx, p, stream);
+    return sbt_attention_enqueue<Fma32<DP, 8>, STAGES, WARPS, BLOCKS>(ctx, p, stream);
 }
 
 }  // namespace
 
 sbt_status sbt_attention_f32(sbt_context* ctx, const AttnParams& p, cudaStream_t stream) {
-    if (p.head_dim <= 64) return by_heads<64, 4>(ctx, p, stream);
-    if (p.head_dim <= 128) return by_heads<128, 2>(ctx, p, stream);
-    return by_heads<256, 2>(ctx, p, stream);
+    if (p.head_dim <= 64) return by_heads<64, 2, 4, 3>(ctx, p, stream);
+    if (p.head_dim <= 96) return by_heads<96, 2, 4, 3>(ctx, p, stream);
+    if (p.head_dim <= 128) return by_heads<128, 2, 4, 2>(ctx, p, stream);
+    return by_heads<256, 2, 4, 1>(ctx, p, stream);
 }

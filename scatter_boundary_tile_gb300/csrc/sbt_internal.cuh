@@ -251,6 +251,26 @@ cudaError_t sbt_launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, 
     return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
 }
 
+// The same with clusters of `ranks` blocks.
+template <typename... KArgs, typename... Args>
+cudaError_t sbt_launch_dependent_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, unsigned ranks, size_t smem,
+                                         cudaStream_t stream, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
+}
+
 // ----------------------------------------------------------------------------
 // Device side: raw element types and 16-byte vector accesses
 // ----------------------------------------------------------------------------

@@ -273,3 +273,4 @@ def test_refusals(ctx):
             call(**kw)
         assert e.value.status == status, kw
     assert ctx.launch_count == before
+
