@@ -154,18 +154,27 @@ def _check(status: int):
 
 
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
 
+_torch = None  # the torch module, its raw-stream query and its dtypes' codes, once a call needs them
+
+
+def _load_torch():
+    global _torch, _raw_stream, _device_index, _CODES
+    import torch
+    _raw_stream, _device_index = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+    _CODES = {torch.float32: SBT_F32, torch.bfloat16: SBT_BF16, torch.float16: SBT_F16}
+    _torch = torch
+
+
 def _stream(stream) -> int | None:
-    if stream is None:
-        import torch
-        # the current device's current stream, without building the Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:  # the current device's current stream, without building a Stream object
+        if _torch is None:
+            _load_torch()
+        return _raw_stream(_device_index())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -174,10 +183,10 @@ def _stream(stream) -> int | None:
 def _dtype_code(t, dtype):
     if dtype is not None:
         return {"f32": SBT_F32, "bf16": SBT_BF16, "f16": SBT_F16}[dtype] if isinstance(dtype, str) else int(dtype)
-    import torch
-    if t.dtype == torch.float16:
-        return SBT_F16
-    return {4: SBT_F32, 2: SBT_BF16}[t.element_size()]
+    if _torch is None:
+        _load_torch()
+    code = _CODES.get(t.dtype)
+    return {4: SBT_F32, 2: SBT_BF16}[t.element_size()] if code is None else code
 
 
 def _pad_bytes(pad, code):

@@ -210,6 +210,7 @@ __device__ __forceinline__ float lanes_sum(float x) {
 // HB heads of one kind of a token per group: grid (head blocks, token blocks).
 template <int KIND, bool INTER, int LPR, int HB>
 __global__ void __launch_bounds__(kThreads, HB == 1 ? 1 : kFwdBlocks) k_norm_rope(const FwdParams p) {
+    sbt_ptx::griddep_wait();
     constexpr int V = Num<KIND>::V, ES = 16 / V, GROUPS = kThreads / LPR;
     const int j = threadIdx.x % LPR, g = threadIdx.x / LPR;
     const Place at = place_of<V, INTER>(j, LPR, p.D, p.rot);
@@ -296,6 +297,7 @@ __device__ __forceinline__ void pair_at(int i, int D, int rot, bool inter, int* 
 template <int KIND>
 __global__ void __launch_bounds__(kThreads) k_norm_rope_elems(const FwdParams p) {
     typedef typename Num<KIND>::T T;
+    sbt_ptx::griddep_wait();
     const int lane = threadIdx.x & 31;
     const int total = p.heads[0] + p.heads[1] + p.heads[2];
     const int64_t rows = p.tokens * total;
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_bwd(const BwdParams p) {
     int32_t* const s_pos = reinterpret_cast<int32_t*>(smem + (size_t)STAGES * VECS * kThreads * 16) + threadIdx.x;
     float* const s_dw = reinterpret_cast<float*>(smem);  // [GROUPS][LPR * 2 V], after the last item
     const uint32_t ring_u32 = sbt_ptx::smem_u32(ring);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    sbt_ptx::griddep_wait();
     const int j = threadIdx.x % LPR, g = threadIdx.x / LPR;
     const Place at = place_of<V, INTER>(j, LPR, p.D, p.rot);
     const int kind = blockIdx.x >= p.blocks[0];
@@ -531,7 +533,7 @@ template <int KIND>
 __global__ void __launch_bounds__(kThreads) k_norm_rope_bwd_elems(const BwdParams p) {
     typedef typename Num<KIND>::T T;
     extern __shared__ float s_dw[];  // [warps][D]
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    sbt_ptx::griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int kind = blockIdx.x >= p.blocks[0];
     const int first = kind ? blockIdx.x - p.blocks[0] : blockIdx.x;
@@ -652,6 +654,7 @@ struct TableParams {
 // Angles are formed and reduced in 64 bits: at position 10^6 an fp32 product
 // would already be off by 0.06.
 __global__ void __launch_bounds__(kThreads) k_rope_table(const TableParams p) {
+    sbt_ptx::griddep_wait();
     const int half = p.rot / 2;
     const int64_t n = p.n_pos * half;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
@@ -711,9 +714,9 @@ void fwd_launch(const sbt_context* ctx, const FwdParams& p, cudaStream_t stream)
     const unsigned ty = (unsigned)std::min<int64_t>(sbt_cdiv(p.tokens, GROUPS), 65535);
     if (p.tokens * total >= (int64_t)ctx->sm_count * kManyRows * GROUPS) {
         const int64_t hb = sbt_cdiv(p.heads[0], HB) + sbt_cdiv(p.heads[1], HB) + sbt_cdiv(p.heads[2], HB);
-        k_norm_rope<KIND, INTER, LPR, HB><<<dim3((unsigned)hb, ty), kThreads, 0, stream>>>(p);
+        sbt_launch_dependent(k_norm_rope<KIND, INTER, LPR, HB>, dim3((unsigned)hb, ty), dim3(kThreads), 0, stream, p);
     } else {
-        k_norm_rope<KIND, INTER, LPR, 1><<<dim3((unsigned)total, ty), kThreads, 0, stream>>>(p);
+        sbt_launch_dependent(k_norm_rope<KIND, INTER, LPR, 1>, dim3((unsigned)total, ty), dim3(kThreads), 0, stream, p);
     }
 }
 
@@ -724,7 +727,7 @@ void bwd_launch(const sbt_context* ctx, const BwdParams& p, cudaStream_t stream)
                                  (size_t)kThreads * 2 * V * sizeof(float));
     constexpr auto kern = k_norm_rope_bwd<KIND, INTER, LPR, kBwdHeads, kStages>;
     sbt_resident_blocks<kern>(ctx, kThreads, smem);
-    kern<<<p.blocks[0] + p.blocks[1], kThreads, smem, stream>>>(p);
+    sbt_launch_dependent(kern, dim3(p.blocks[0] + p.blocks[1]), dim3(kThreads), smem, stream, p);
 }
 
 template <int KIND, bool INTER, class P, class F>
@@ -745,7 +748,7 @@ void fwd(const sbt_context* ctx, const FwdParams& p, bool vec, cudaStream_t stre
     if (!vec) {
         const int64_t rows = p.tokens * (p.heads[0] + p.heads[1] + p.heads[2]);
         const int64_t blocks = std::min<int64_t>(sbt_cdiv(rows, kThreads / 32), (int64_t)ctx->sm_count * 16);
-        k_norm_rope_elems<KIND><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+        sbt_launch_dependent(k_norm_rope_elems<KIND>, dim3((unsigned)blocks), dim3(kThreads), 0, stream, p);
     } else if (p.interleaved) {
         by_lanes<KIND, true>(lanes_per_row(p.D, p.rot, V, true), p,
                              [&](auto n) { fwd_launch<KIND, true, decltype(n)::value>(ctx, p, stream); });
@@ -759,8 +762,8 @@ template <int KIND>
 void bwd(const sbt_context* ctx, const BwdParams& p, bool vec, cudaStream_t stream) {
     constexpr int V = Num<KIND>::V;
     if (!vec) {
-        k_norm_rope_bwd_elems<KIND><<<p.blocks[0] + p.blocks[1], kThreads, (kThreads / 32) * p.D * sizeof(float),
-                                      stream>>>(p);
+        sbt_launch_dependent(k_norm_rope_bwd_elems<KIND>, dim3(p.blocks[0] + p.blocks[1]), dim3(kThreads),
+                             (kThreads / 32) * p.D * sizeof(float), stream, p);
     } else if (p.interleaved) {
         by_lanes<KIND, true>(lanes_per_row(p.D, p.rot, V, true), p,
                              [&](auto n) { bwd_launch<KIND, true, decltype(n)::value>(ctx, p, stream); });
@@ -866,6 +869,6 @@ sbt_status sbt_launch_rope_table(sbt_context* ctx, float* table, int64_t n_pos, 
                                  cudaStream_t stream) {
     TableParams p = {(float2*)table, n_pos, rot, scaling, base, factor, low, high, (double)orig, amplitude};
     const int64_t blocks = std::min<int64_t>(sbt_cdiv(n_pos * (rot / 2), kThreads), (int64_t)ctx->sm_count * 16);
-    k_rope_table<<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+    sbt_launch_dependent(k_rope_table, dim3((unsigned)blocks), dim3(kThreads), 0, stream, p);
     return sbt_after_launch(ctx, "rope_table");
 }

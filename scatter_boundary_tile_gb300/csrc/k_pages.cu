@@ -10,8 +10,7 @@
 // Deciding is a few prefix sums over the sequences and the pages; one block of
 // 1024 threads does it (a pass over 65,536 counts is 256 KB) and leaves a plan
 // in the workspace.  Moving the pages' bytes is memory-bound; the second
-// kernel, launched as a programmatic dependent so that its blocks are in place
-// when the plan is ready, spreads the plan's rows and pages over the GPU.
+// kernel spreads the plan's rows and pages over the GPU.
 #include <algorithm>
 
 #include "sbt_internal.cuh"
@@ -24,6 +23,7 @@ using sbt_ptx::griddep_wait;
 constexpr int kPlanThreads = 1024;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveVecs = 4;                                    // 16-byte vectors per thread and chunk
+constexpr int kMoveBlocks = 32;                                 // blocks per SM at most (8: 173 us, 32: 159 us for 1 GB each way)
 constexpr int kChunkBytes = kMoveThreads * kMoveVecs * 16;
 
 struct Pool {
@@ -169,6 +169,7 @@ __device__ __forceinline__ void move_pages(const Pools& q, const int32_t* src, c
 
 __global__ void __launch_bounds__(kMoveThreads) k_pages_copy(const __grid_constant__ Pools q, const int32_t* src,
                                                              const int32_t* dst, int64_t n, int32_t n_pages) {
+    griddep_wait();
     move_pages(q, src, dst, n, n_pages);
 }
 
@@ -182,6 +183,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_pages_moves(const __grid_const
 // ------------------------------------------------------------------------------------ free
 
 __global__ void __launch_bounds__(kMoveThreads) k_pages_free(const Map m, const int32_t* seqs, const int32_t* keep) {
+    griddep_wait();
     const int32_t s = __ldg(seqs + blockIdx.x);
     if (s < 0 || s >= m.n_seq) return;
     int32_t k = keep ? __ldg(keep + blockIdx.x) : 0;
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_pages_free(const Map m, const 
 // --------------------------------------------------------------------------------- reserve
 
 __global__ void __launch_bounds__(kPlanThreads) k_pages_reserve(const Map m, const Plan w, const int32_t* target) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    griddep_wait();
     __shared__ int32_t s_warp[32];
     __shared__ int32_t s_moves;
     if (threadIdx.x == 0) s_moves = 0;
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_reserve(const Map m, con
 
 __global__ void __launch_bounds__(kPlanThreads) k_pages_fork(const Map m, const Plan w, const int32_t* from,
                                                              const int32_t* to, int32_t n) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    griddep_wait();
     __shared__ int32_t s_warp[32];
     auto ok = [&](int32_t i, int32_t& a, int32_t& c) {
         a = __ldg(from + i), c = __ldg(to + i);
@@ -350,7 +352,7 @@ struct Packed {
 // holes below L: the fewest moves that pack the pool, and no page is both read
 // and written.
 __global__ void __launch_bounds__(kPlanThreads) k_pages_compact(const Map m, const Plan w, const Packed o) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    griddep_wait();
     __shared__ int32_t s_warp[32];
     int32_t mine = 0, live;
     for (int32_t p = threadIdx.x; p < m.n_pages; p += kPlanThreads) mine += m.refs[p] > 0;
@@ -428,8 +430,14 @@ Pools pools_of(const sbt_page_pool* pools, int32_t n) {
     return q;
 }
 
+// Every launch is a programmatic dependent: the kernels wait for the one ahead before they touch memory.
+sbt_status launched(sbt_context* ctx, const char* what, cudaError_t e) {
+    const sbt_status st = sbt_cuda_check(e, what);
+    return st ? st : sbt_after_launch(ctx, what);
+}
+
 int move_grid(const sbt_context* ctx, int64_t jobs) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(jobs, (int64_t)ctx->sm_count * 8));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(jobs, (int64_t)ctx->sm_count * kMoveBlocks));
 }
 
 }  // namespace
@@ -439,14 +447,15 @@ size_t sbt_pages_workspace_bytes(int32_t n_seq, int64_t n_pages) { return plan_b
 sbt_status sbt_launch_pages_copy(sbt_context* ctx, const sbt_page_pool* pools, int32_t n_pools, int64_t n_pages,
                                  const int32_t* src, const int32_t* dst, int64_t n, cudaStream_t stream) {
     const Pools q = pools_of(pools, n_pools);
-    k_pages_copy<<<move_grid(ctx, n * q.chunks), kMoveThreads, 0, stream>>>(q, src, dst, n, (int32_t)n_pages);
-    return sbt_after_launch(ctx, "pages_copy");
+    return launched(ctx, "pages_copy",
+                    sbt_launch_dependent(k_pages_copy, dim3(move_grid(ctx, n * q.chunks)), dim3(kMoveThreads), 0,
+                                         stream, q, src, dst, n, (int32_t)n_pages));
 }
 
 sbt_status sbt_launch_pages_free(sbt_context* ctx, const sbt_page_map* map, const int32_t* seqs, const int32_t* keep,
                                  int32_t n, cudaStream_t stream) {
-    k_pages_free<<<n, kMoveThreads, 0, stream>>>(map_of(map), seqs, keep);
-    return sbt_after_launch(ctx, "pages_free");
+    return launched(ctx, "pages_free",
+                    sbt_launch_dependent(k_pages_free, dim3(n), dim3(kMoveThreads), 0, stream, map_of(map), seqs, keep));
 }
 
 sbt_status sbt_launch_pages_reserve(sbt_context* ctx, const sbt_page_map* map, const sbt_page_pool* pools,
@@ -454,14 +463,12 @@ sbt_status sbt_launch_pages_reserve(sbt_context* ctx, const sbt_page_map* map, c
     const Map m = map_of(map);
     const Plan w = plan_of(workspace, map->n_seq, map->n_pages);
     const Pools q = pools_of(pools, n_pools);
-    k_pages_reserve<<<1, kPlanThreads, 0, stream>>>(m, w, target);
-    sbt_status st = sbt_after_launch(ctx, "pages_reserve");
+    const sbt_status st = launched(ctx, "pages_reserve", sbt_launch_dependent(k_pages_reserve, dim3(1), dim3(kPlanThreads),
+                                                                              0, stream, m, w, target));
     if (st) return st;
-    if ((st = sbt_cuda_check(sbt_launch_dependent(k_pages_moves, dim3(move_grid(ctx, map->n_seq * q.chunks)),
-                                                  dim3(kMoveThreads), 0, stream, q, w, m.n_pages),
-                             "pages_reserve moves launch")))
-        return st;
-    return sbt_after_launch(ctx, "pages_reserve moves");
+    return launched(ctx, "pages_reserve moves",
+                    sbt_launch_dependent(k_pages_moves, dim3(move_grid(ctx, map->n_seq * q.chunks)),
+                                         dim3(kMoveThreads), 0, stream, q, w, m.n_pages));
 }
 
 sbt_status sbt_launch_pages_fork(sbt_context* ctx, const sbt_page_map* map, const sbt_page_pool* pools,
@@ -470,14 +477,12 @@ sbt_status sbt_launch_pages_fork(sbt_context* ctx, const sbt_page_map* map, cons
     const Map m = map_of(map);
     const Plan w = plan_of(workspace, map->n_seq, map->n_pages);
     const Pools q = pools_of(pools, n_pools);
-    k_pages_fork<<<1, kPlanThreads, 0, stream>>>(m, w, from, to, n);
-    sbt_status st = sbt_after_launch(ctx, "pages_fork");
+    const sbt_status st = launched(ctx, "pages_fork", sbt_launch_dependent(k_pages_fork, dim3(1), dim3(kPlanThreads), 0,
+                                                                           stream, m, w, from, to, n));
     if (st) return st;
-    if ((st = sbt_cuda_check(sbt_launch_dependent(k_pages_fork_rows, dim3(move_grid(ctx, n * q.chunks)),
-                                                  dim3(kMoveThreads), 0, stream, q, m, w, from, to, n),
-                             "pages_fork rows launch")))
-        return st;
-    return sbt_after_launch(ctx, "pages_fork rows");
+    return launched(ctx, "pages_fork rows",
+                    sbt_launch_dependent(k_pages_fork_rows, dim3(move_grid(ctx, n * q.chunks)), dim3(kMoveThreads), 0,
+                                         stream, q, m, w, from, to, n));
 }
 
 sbt_status sbt_launch_pages_compact(sbt_context* ctx, const sbt_page_map* map, const sbt_page_pool* pools,
@@ -487,13 +492,11 @@ sbt_status sbt_launch_pages_compact(sbt_context* ctx, const sbt_page_map* map, c
     const Plan w = plan_of(workspace, map->n_seq, map->n_pages);
     const Pools q = pools_of(pools, n_pools);
     const Packed o = {table_out, ld_out, refs_out, page_to, n_live};
-    k_pages_compact<<<1, kPlanThreads, 0, stream>>>(m, w, o);
-    sbt_status st = sbt_after_launch(ctx, "pages_compact");
+    const sbt_status st = launched(ctx, "pages_compact", sbt_launch_dependent(k_pages_compact, dim3(1), dim3(kPlanThreads),
+                                                                              0, stream, m, w, o));
     if (st) return st;
     const int64_t jobs = std::max<int64_t>(map->n_seq, (map->n_pages / 2) * q.chunks);
-    if ((st = sbt_cuda_check(sbt_launch_dependent(k_pages_compact_rows, dim3(move_grid(ctx, jobs)), dim3(kMoveThreads),
-                                                  0, stream, q, m, w, o),
-                             "pages_compact rows launch")))
-        return st;
-    return sbt_after_launch(ctx, "pages_compact rows");
+    return launched(ctx, "pages_compact rows",
+                    sbt_launch_dependent(k_pages_compact_rows, dim3(move_grid(ctx, jobs)), dim3(kMoveThreads), 0,
+                                         stream, q, m, w, o));
 }
