@@ -694,9 +694,9 @@ sbt_status sbt_attention_enqueue(sbt_context* ctx, AttnParams p, cudaStream_t st
     const int64_t longest = sbt_cdiv(p.window > 0 && p.window < p.max_len ? (int64_t)p.window + M::TOK : p.max_len, M::TOK);
     // A cluster per row where all clusters fit at once and a warp gets kClusterTiles tiles at most: below
     // that the second launch and the way through memory cost more than uneven work.
-    int ranks = kClusterMost;
-    while (ranks > 1 && rows * ranks > resident) ranks >>= 1;
-    while (ranks > 1 && (ranks >> 1) * WARPS >= longest) ranks >>= 1;
+    int ranks = (int)(resident / rows < kClusterMost ? resident / rows : kClusterMost);
+    if (ranks > sbt_cdiv(longest, WARPS)) ranks = (int)sbt_cdiv(longest, WARPS);
+    if (ranks < 1) ranks = 1;
     if (rows * ranks <= resident && longest <= (int64_t)ranks * WARPS * kClusterTiles) {
         p.cluster = ranks;
         sbt_resident_blocks<k_paged_attention_cluster<M, STAGES, WARPS, BLOCKS>>(ctx, 32 * WARPS, smem);

@@ -1,18 +1,21 @@
 // Paged attention, 32-bit caches: the tile math in fp32 multiply-adds, since a
 // tensor-core product would round the operands to fewer bits.
 //
-// A warp tile is eight positions.  Scores: four lanes share a position and take
-// every fourth 16-byte piece of its key; queries are read from shared memory
-// (one address per quarter of the warp).  Values: a lane owns DP / 32 elements
-// of the head and adds p v over the eight positions.
+// A warp tile is 8 MT positions.  Scores: four lanes share MT positions and take
+// every fourth 16-byte piece of their keys; queries are read from shared memory
+// (one address per quarter of the warp) once for the MT positions.  Values: a
+// lane owns DP / 32 elements of the head and adds p v over the positions.  With
+// one or two heads the copies bound the kernel and MT is 1, which leaves room
+// for more warps; from three heads on the reads of the query and the shuffles
+// do (64 ragged sequences, 64 query heads of 128: 275 us with MT 1).
 #include "k_paged_attention.cuh"
 
 namespace {
 
-template <int DP_, int HT>
+template <int DP_, int HT, int MT>
 struct Fma32 {
     typedef float T;
-    static constexpr int ES = 4, TOK = 8, DP = DP_, HEADS = HT;
+    static constexpr int ES = 4, TOK = 8 * MT, DP = DP_, HEADS = HT;
     static constexpr int PITCH = DP * 4;
     // scores read four 16-byte pieces of two rows at once: of odd rows the other half of the banks
     static __device__ __forceinline__ int swizzle(int t) { return (t & 1) << 2; }
@@ -47,37 +50,49 @@ struct Fma32 {
         const int lane = threadIdx.x & 31, t = lane >> 2, part = lane & 3;
         float* const s_p = s_q + HT * DP;
         const uint8_t* const kr = stage + t * PITCH;
-        const int k_x = part ^ swizzle(t);
-        float s[HT];
+        const int k_x = part ^ swizzle(t);  // of rows t and t + 8
+        float s[MT][HT];
 #pragma unroll
-        for (int h = 0; h < HT; ++h) s[h] = 0.f;
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < HT; ++h) s[m][h] = 0.f;
 #pragma unroll 4
         for (int i = 0; i < DP / 16; ++i) {
-            const float4 k4 = *reinterpret_cast<const float4*>(kr + ((i * 4) ^ k_x) * 16);
+            float4 k4[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                k4[m] = *reinterpret_cast<const float4*>(kr + m * 8 * PITCH + ((i * 4) ^ k_x) * 16);
 #pragma unroll
             for (int h = 0; h < HT; ++h) {
                 const float4 q4 = *reinterpret_cast<const float4*>(s_q + h * DP + i * 16 + part * 4);
-                s[h] = fmaf(k4.x, q4.x, fmaf(k4.y, q4.y, fmaf(k4.z, q4.z, fmaf(k4.w, q4.w, s[h]))));
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    s[m][h] = fmaf(k4[m].x, q4.x, fmaf(k4[m].y, q4.y, fmaf(k4[m].z, q4.z, fmaf(k4[m].w, q4.w, s[m][h]))));
             }
         }
-        const bool see = (bits >> t) & 1u;
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
-            float x = s[h];
-            x += __shfl_xor_sync(0xffffffffu, x, 1);
-            x += __shfl_xor_sync(0xffffffffu, x, 2);
-            x = see ? x * p.scale_log2 : -CUDART_INF_F;
-            float top = x;
+            float top = mx[h];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                s[m][h] += __shfl_xor_sync(0xffffffffu, s[m][h], 1);
+                s[m][h] += __shfl_xor_sync(0xffffffffu, s[m][h], 2);
+                s[m][h] = (bits >> (m * 8 + t)) & 1u ? s[m][h] * p.scale_log2 : -CUDART_INF_F;
+                top = fmaxf(top, s[m][h]);
+            }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            top = fmaxf(top, mx[h]);
             const float ts = top == -CUDART_INF_F ? 0.f : top;
             const float alpha = sbt_attn::exp2_fast(mx[h] - ts);
-            const float pr = sbt_attn::exp2_fast(x - ts);
             mx[h] = top;
-            l[h] = l[h] * alpha + pr;  // the four lanes of a position hold the same sum
-            if (part == 0) s_p[t * HT + h] = pr;
+            l[h] *= alpha;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const float pr = sbt_attn::exp2_fast(s[m][h] - ts);
+                l[h] += pr;  // the four lanes of a position hold the same sum
+                if (part == 0) s_p[(m * 8 + t) * HT + h] = pr;
+            }
 #pragma unroll
             for (int e = 0; e < EL; ++e) o[h][e] *= alpha;
         }
@@ -147,19 +162,22 @@ struct Fma32 {
     }
 };
 
-template <int DP, int STAGES, int WARPS, int BLOCKS>
+// WARPS and BLOCKS with one, WARPS2 and BLOCKS2 with two positions per lane: as many as two stages
+// and the query leave room for.
+template <int DP, int WARPS, int BLOCKS, int WARPS2, int BLOCKS2>
 sbt_status by_heads(sbt_context* ctx, const AttnParams& p, cudaStream_t stream) {
-    if (p.chunk <= 1) return sbt_attention_enqueue<Fma32<DP, 1>, STAGES, WARPS, BLOCKS>(ctx, p, stream);
-    if (p.chunk <= 2) return sbt_attention_enqueue<Fma32<DP, 2>, STAGES, WARPS, BLOCKS>(ctx, p, stream);
-    if (p.chunk <= 4) return sbt_attention_enqueue<Fma32<DP, 4>, STAGES, WARPS, BLOCKS>(ctx, p, stream);
-    return sbt_attention_enqueue<Fma32<DP, 8>, STAGES, WARPS, BLOCKS>(ctx, p, stream);
+    constexpr int MT = DP <= 128 ? 2 : 1;
+    if (p.chunk <= 1) return sbt_attention_enqueue<Fma32<DP, 1, 1>, 2, WARPS, BLOCKS>(ctx, p, stream);
+    if (p.chunk <= 2) return sbt_attention_enqueue<Fma32<DP, 2, 1>, 2, WARPS, BLOCKS>(ctx, p, stream);
+    if (p.chunk <= 4) return sbt_attention_enqueue<Fma32<DP, 4, MT>, 2, WARPS2, BLOCKS2>(ctx, p, stream);
+    return sbt_attention_enqueue<Fma32<DP, 8, MT>, 2, WARPS2, BLOCKS2>(ctx, p, stream);
 }
 
 }  // namespace
 
 sbt_status sbt_attention_f32(sbt_context* ctx, const AttnParams& p, cudaStream_t stream) {
-    if (p.head_dim <= 64) return by_heads<64, 2, 4, 3>(ctx, p, stream);
-    if (p.head_dim <= 96) return by_heads<96, 2, 4, 3>(ctx, p, stream);
-    if (p.head_dim <= 128) return by_heads<128, 2, 4, 2>(ctx, p, stream);
-    return by_heads<256, 2, 4, 1>(ctx, p, stream);
+    if (p.head_dim <= 64) return by_heads<64, 4, 3, 5, 2>(ctx, p, stream);
+    if (p.head_dim <= 96) return by_heads<96, 4, 3, 4, 2>(ctx, p, stream);
+    if (p.head_dim <= 128) return by_heads<128, 5, 2, 6, 1>(ctx, p, stream);
+    return by_heads<256, 5, 1, 5, 1>(ctx, p, stream);
 }
