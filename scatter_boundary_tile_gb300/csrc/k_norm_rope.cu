@@ -122,11 +122,11 @@ struct FwdParams {
 
 // Byte offset of a token's slot in the cache, or -1 where it has none.
 __device__ __forceinline__ int64_t cache_slot(const FwdParams& p, int64_t t, int32_t pos) {
-    const int64_t s = p.seq ? (int64_t)__ldg(p.seq + t) : t;
+    const int64_t s = p.seq ? (int64_t)sbt_ld(p.seq + t) : t;
     if (s < 0 || s >= p.n_seq || pos < 0) return -1;
     const uint32_t j = sbt_div(p.page_size, (uint32_t)pos);
     if (j >= (uint32_t)p.max_pages) return -1;
-    const int32_t page = __ldg(p.page_table + s * p.ld_table + j);
+    const int32_t page = sbt_ld(p.page_table + s * p.ld_table + j);
     if (page < 0 || page >= p.n_pages) return -1;
     return page * p.ld_page + (int64_t)(pos - (int32_t)(j * p.page_size.d)) * p.ld_slot;
 }
@@ -183,7 +183,7 @@ __device__ __forceinline__ void angles(const float2* row, const Place& q, float*
     for (int i = 0; i < V / 2; ++i) {
         const int first = q.pair[i / (V / 4)];
         float4 c = make_float4(1.f, 0.f, 1.f, 0.f);
-        if (first >= 0) c = __ldg(reinterpret_cast<const float4*>(row + first + 2 * (i % (V / 4))));
+        if (first >= 0) c = sbt_ld(reinterpret_cast<const float4*>(row + first + 2 * (i % (V / 4))));
         cs[2 * i] = c.x, sn[2 * i] = c.y, cs[2 * i + 1] = c.z, sn[2 * i + 1] = c.w;
     }
 }
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, HB == 1 ? 1 : kFwdBlocks) k_norm_rop
     for (int64_t t0 = (int64_t)blockIdx.y * GROUPS; t0 < p.tokens; t0 += (int64_t)gridDim.y * GROUPS) {
         const int64_t t = t0 + g;
         const bool on = t < p.tokens;
-        const int32_t pos = on ? __ldg(p.pos + t) : -1;
+        const int32_t pos = on ? sbt_ld(p.pos + t) : -1;
         const char* x = in.at(on ? t : 0, h0);
         uint4 va[HB], vb[HB];
 #pragma unroll
@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(kThreads, HB == 1 ? 1 : kFwdBlocks) k_norm_rop
 #pragma unroll
                     for (int e = 0; e < 2 * V; ++e) ss += f[e] * f[e];
                     const float r = rsqrtf(lanes_sum<LPR>(ss) / (float)p.D + p.eps);
-                    unpack<KIND>(at.a >= 0 ? __ldg(reinterpret_cast<const uint4*>(wp + at.a * ES)) : zero, w);
-                    unpack<KIND>(at.b >= 0 ? __ldg(reinterpret_cast<const uint4*>(wp + at.b * ES)) : zero, w + V);
+                    unpack<KIND>(at.a >= 0 ? sbt_ld(reinterpret_cast<const uint4*>(wp + at.a * ES)) : zero, w);
+                    unpack<KIND>(at.b >= 0 ? sbt_ld(reinterpret_cast<const uint4*>(wp + at.b * ES)) : zero, w + V);
 #pragma unroll
                     for (int e = 0; e < 2 * V; ++e) f[e] = f[e] * r * w[e];
                 }
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_elems(const FwdParams p)
         int h = (int)(row - t * total);
         const int kind = h < p.heads[0] ? 0 : h < p.heads[0] + p.heads[1] ? 1 : 2;
         h -= (kind >= 1 ? p.heads[0] : 0) + (kind == 2 ? p.heads[1] : 0);
-        const int32_t pos = __ldg(p.pos + t);
+        const int32_t pos = sbt_ld(p.pos + t);
         const bool real = pos >= 0 && (p.rot == 0 || pos < p.n_pos);
         const T* x = reinterpret_cast<const T*>(p.x[kind].at(t, h));
         float a[kMaxScalarPairs], b[kMaxScalarPairs], ss = 0.f;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_elems(const FwdParams p)
                 if (ib >= 0) v = v * r * Num<KIND>::get(w[ib]);
             }
             if (kind < 2 && pr < p.rot / 2 && real) {
-                const float2 cs = __ldg(p.table + (int64_t)pos * (p.rot / 2) + pr);
+                const float2 cs = sbt_ld(p.table + (int64_t)pos * (p.rot / 2) + pr);
                 const float uu = u * cs.x - v * cs.y;
                 v = v * cs.x + u * cs.y;
                 u = uu;
@@ -416,8 +416,8 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_bwd(const BwdParams p) {
     for (int e = 0; e < 2 * V; ++e) w[e] = 1.f, dw[e] = 0.f;
     if (wp) {
         const uint4 zero = make_uint4(0, 0, 0, 0);
-        unpack<KIND>(at.a >= 0 ? __ldg(reinterpret_cast<const uint4*>(wp + at.a * ES)) : zero, w);
-        unpack<KIND>(at.b >= 0 ? __ldg(reinterpret_cast<const uint4*>(wp + at.b * ES)) : zero, w + V);
+        unpack<KIND>(at.a >= 0 ? sbt_ld(reinterpret_cast<const uint4*>(wp + at.a * ES)) : zero, w);
+        unpack<KIND>(at.b >= 0 ? sbt_ld(reinterpret_cast<const uint4*>(wp + at.b * ES)) : zero, w + V);
     }
     const float inv_d = 1.f / (float)p.D;
     const int64_t items = p.tokens * hblocks;
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_bwd(const BwdParams p) {
     const Item step = item_at(stride, hblocks);
 
     Item in = item_at(first + g, hblocks);  // the next item to load
-    int32_t in_pos = in.t < p.tokens ? __ldg(p.pos + in.t) : -1;
+    int32_t in_pos = in.t < p.tokens ? sbt_ld(p.pos + in.t) : -1;
     auto load = [&](int stage) {
         const uint32_t dst = ring_u32 + stage * VECS * kThreads * 16;
         if (in.t < p.tokens) {
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_bwd(const BwdParams p) {
         copy_commit();
         s_pos[stage * kThreads] = in_pos;
         advance(in, step, hblocks);
-        if (in.t < p.tokens) in_pos = __ldg(p.pos + in.t);
+        if (in.t < p.tokens) in_pos = sbt_ld(p.pos + in.t);
     };
 #pragma unroll 1
     for (int s = 0; s < STAGES - 1; ++s) load(s);
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_bwd_elems(const BwdParam
          row += (int64_t)p.blocks[kind] * (kThreads / 32)) {
         const int64_t t = row / p.heads[kind];
         const int h = (int)(row - t * p.heads[kind]);
-        const int32_t pos = __ldg(p.pos + t);
+        const int32_t pos = sbt_ld(p.pos + t);
         const bool real = pos >= 0 && (p.rot == 0 || pos < p.n_pos);
         const T* gr = reinterpret_cast<const T*>(p.g[kind].at(t, h));
         const T* xr = w ? reinterpret_cast<const T*>(p.x[kind].at(t, h)) : nullptr;
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_bwd_elems(const BwdParam
             a[i] = ia >= 0 ? Num<KIND>::get(gr[ia]) : 0.f;
             b[i] = ib >= 0 ? Num<KIND>::get(gr[ib]) : 0.f;
             if (pr < p.rot / 2 && real) {
-                const float2 cs = __ldg(p.table + (int64_t)pos * (p.rot / 2) + pr);
+                const float2 cs = sbt_ld(p.table + (int64_t)pos * (p.rot / 2) + pr);
                 const float u = a[i] * cs.x + b[i] * cs.y;
                 b[i] = b[i] * cs.x - a[i] * cs.y;
                 a[i] = u;

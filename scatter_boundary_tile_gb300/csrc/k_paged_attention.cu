@@ -97,10 +97,10 @@ struct Mma16 {
                     uint32_t w = 0;
                     if (h < heads && d < p.head_dim) {
                         if (p.q_words) {
-                            w = __ldg(reinterpret_cast<const uint32_t*>(x + d));
+                            w = sbt_ld(reinterpret_cast<const uint32_t*>(x + d));
                         } else {
-                            w = __ldg(x + d);
-                            if (d + 1 < p.head_dim) w |= (uint32_t)__ldg(x + d + 1) << 16;
+                            w = sbt_ld(x + d);
+                            if (d + 1 < p.head_dim) w |= (uint32_t)sbt_ld(x + d + 1) << 16;
                         }
                     }
                     qf[k][n][i] = w;

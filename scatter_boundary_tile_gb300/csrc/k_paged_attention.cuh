@@ -90,10 +90,10 @@ template <int TOK>
 __device__ __forceinline__ AttnRow row_of(const AttnParams& p, int32_t b) {
     AttnRow r;
     r.b = b;
-    r.seq = p.seq ? __ldg(p.seq + b) : b;
+    r.seq = p.seq ? sbt_ld(p.seq + b) : b;
     r.lo = r.hi = r.base = r.tiles = 0;
     if (r.seq >= 0 && r.seq < p.n_seq) {
-        int32_t n = __ldg(p.lens + r.seq);
+        int32_t n = sbt_ld(p.lens + r.seq);
         n = n < 0 ? 0 : n > p.max_len ? p.max_len : n;
         r.hi = n;
         r.lo = (p.window > 0 && n > p.window) ? n - p.window : 0;
@@ -243,7 +243,7 @@ struct AttnLoader {
         if (left <= 0 || pos < row.lo || pos >= row.hi) return;
         const uint32_t pg = sbt_div(p.page_size, (uint32_t)pos);
         slot = pos - (int32_t)(pg * p.page_size.d);
-        page = __ldg(p.table + (int64_t)row.seq * p.ld_table + pg);
+        page = sbt_ld(p.table + (int64_t)row.seq * p.ld_table + pg);
     }
 
     // The query of a row, towards L2: the math reads it a tile or two later.
@@ -329,9 +329,9 @@ struct AttnLoader {
                 const int64_t o = __shfl_sync(0xffffffffu, off, t);
                 for (int e = lane; e < p.head_dim; e += 32) {
                     const int a = t * PITCH + (((e >> 3) ^ M::swizzle(t)) << 4) + (e & 7) * ES;
-                    *reinterpret_cast<T*>(st + a) = o < 0 ? T(0) : __ldg(reinterpret_cast<const T*>(p.k + o) + e);
+                    *reinterpret_cast<T*>(st + a) = o < 0 ? T(0) : sbt_ld(reinterpret_cast<const T*>(p.k + o) + e);
                     *reinterpret_cast<T*>(st + TOK * PITCH + a) =
-                        o < 0 ? T(0) : __ldg(reinterpret_cast<const T*>(p.v + o) + e);
+                        o < 0 ? T(0) : sbt_ld(reinterpret_cast<const T*>(p.v + o) + e);
                 }
             }
         }

@@ -33,7 +33,7 @@ struct Fma32 {
         __syncwarp();  // the last tile's reads
         for (int i = threadIdx.x & 31; i < HT * DP; i += 32) {
             const int h = i / DP, d = i - h * DP;
-            s_q[i] = h < heads && d < p.head_dim ? __ldg(base + h * p.ld_qh + d) : 0.f;
+            s_q[i] = h < heads && d < p.head_dim ? sbt_ld(base + h * p.ld_qh + d) : 0.f;
         }
 #pragma unroll
         for (int h = 0; h < HT; ++h) {

@@ -35,7 +35,7 @@ struct Pool {
 struct Pools {
     Pool p[SBT_MAX_PAGE_POOLS];
     int32_t n;
-    int32_t vec;             // every address and size is a multiple of 16 bytes
+    int32_t width;           // 16, 4 or 1: every address and size is a multiple of it
     int64_t chunks;          // chunks of one page number: over all pools and planes
 };
 
@@ -139,7 +139,7 @@ __device__ __forceinline__ void move_chunk(const Pools& q, int64_t r, int32_t sr
     char* d = o.base + plane * o.plane_stride + dst * o.page_stride + at;
     const int64_t left = o.page_bytes - at;
     const int n = left < kChunkBytes ? (int)left : kChunkBytes;
-    if (q.vec) {
+    if (q.width == 16) {
         uint4 v[kMoveVecs];
 #pragma unroll
         for (int i = 0; i < kMoveVecs; ++i) {
@@ -151,7 +151,12 @@ __device__ __forceinline__ void move_chunk(const Pools& q, int64_t r, int32_t sr
             const int b = (i * kMoveThreads + threadIdx.x) * 16;
             if (b < n) sbt_st_v4_cs(d + b, v[i]);
         }
+    } else if (q.width == 4) {
+#pragma unroll 8
+        for (int b = threadIdx.x * 4; b < n; b += kMoveThreads * 4)
+            *reinterpret_cast<uint32_t*>(d + b) = *reinterpret_cast<const uint32_t*>(s + b);
     } else {
+#pragma unroll 8
         for (int b = threadIdx.x; b < n; b += kMoveThreads) d[b] = s[b];
     }
 }
@@ -161,7 +166,7 @@ __device__ __forceinline__ void move_pages(const Pools& q, const int32_t* src, c
     const int64_t jobs = n * q.chunks;
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         const int64_t i = job / q.chunks;
-        const int32_t s = __ldcg(src + i), d = __ldcg(dst + i);  // a plan's lists are written just before: not the read-only path
+        const int32_t s = sbt_ld(src + i), d = sbt_ld(dst + i);
         if (s < 0 || s >= n_pages || d < 0 || d >= n_pages || s == d) continue;
         move_chunk(q, job - i * q.chunks, s, d);
     }
@@ -184,9 +189,9 @@ __global__ void __launch_bounds__(kMoveThreads) k_pages_moves(const __grid_const
 
 __global__ void __launch_bounds__(kMoveThreads) k_pages_free(const Map m, const int32_t* seqs, const int32_t* keep) {
     griddep_wait();
-    const int32_t s = __ldg(seqs + blockIdx.x);
+    const int32_t s = sbt_ld(seqs + blockIdx.x);
     if (s < 0 || s >= m.n_seq) return;
-    int32_t k = keep ? __ldg(keep + blockIdx.x) : 0;
+    int32_t k = keep ? sbt_ld(keep + blockIdx.x) : 0;
     if (k < 0) k = 0;
     // a sequence listed twice: both occurrences may see the old length; the exchange lets only one of
     // them release a page
@@ -212,7 +217,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_reserve(const Map m, con
         const int32_t b = b0 + threadIdx.x;
         int32_t need = 0, own = 0;
         if (b < m.n_seq) {
-            const int32_t n = m.lens[b], t = __ldg(target + b);
+            const int32_t n = m.lens[b], t = sbt_ld(target + b);
             if (t > n && m.pages_of(t) <= m.max_pages) {
                 need = m.pages_of(t) - m.pages_of(n);
                 if (n > 0 && n - (int32_t)(sbt_div(m.page_size, (uint32_t)n) * m.page_size.d) != 0) {
@@ -234,7 +239,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_reserve(const Map m, con
     // a warp per sequence: served if it needs no page or its pages end inside the list
     for (int32_t b = threadIdx.x >> 5; b < m.n_seq; b += kPlanThreads / 32) {
         const int lane = threadIdx.x & 31;
-        const int32_t n = m.lens[b], t = __ldg(target + b), need = w.a[b], own = w.b[b], at = w.c[b];
+        const int32_t n = m.lens[b], t = sbt_ld(target + b), need = w.a[b], own = w.b[b], at = w.c[b];
         if (t <= n || m.pages_of(t) > m.max_pages || (need && at + need > found)) continue;
         const int32_t first = m.pages_of(n) - own;
         for (int32_t i = lane; i < need; i += 32) {
@@ -263,7 +268,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_fork(const Map m, const 
     griddep_wait();
     __shared__ int32_t s_warp[32];
     auto ok = [&](int32_t i, int32_t& a, int32_t& c) {
-        a = __ldg(from + i), c = __ldg(to + i);
+        a = sbt_ld(from + i), c = sbt_ld(to + i);
         return a >= 0 && a < m.n_seq && c >= 0 && c < m.n_seq && a != c && m.lens[a] > 0 && m.lens[c] == 0;
     };
     int32_t a, c;
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_fork(const Map m, const 
         const int32_t len = w.a[i], at = w.b[i];
         int32_t src = -1, dst = -1;
         if (len > 0) {
-            a = __ldg(from + i), c = __ldg(to + i);
+            a = sbt_ld(from + i), c = sbt_ld(to + i);
             if (at >= found) {
                 w.a[i] = 0;  // no page left for its last tokens: not taken
             } else {
@@ -324,7 +329,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_pages_fork_rows(const __grid_c
     for (int32_t i = blockIdx.x; i < n; i += gridDim.x) {
         const int32_t len = w.a[i];
         if (len <= 0) continue;
-        const int32_t a = __ldg(from + i), c = __ldg(to + i), pages = m.held(len);
+        const int32_t a = sbt_ld(from + i), c = sbt_ld(to + i), pages = m.held(len);
         for (int32_t j = threadIdx.x; j < pages; j += kMoveThreads) {
             int32_t p = m.table[a * m.ld + j];
             if (j == pages - 1 && w.dst[i] >= 0) {
@@ -417,7 +422,8 @@ Map map_of(const sbt_page_map* map) {
 
 Pools pools_of(const sbt_page_pool* pools, int32_t n) {
     Pools q = {};
-    q.n = n, q.vec = 1;
+    q.n = n;
+    uint64_t bits = 16;
     for (int i = 0; i < n; ++i) {
         const sbt_page_pool& s = pools[i];
         Pool& d = q.p[i];
@@ -425,8 +431,9 @@ Pools pools_of(const sbt_page_pool* pools, int32_t n) {
         d.page_bytes = s.page_bytes, d.planes = (int32_t)s.n_planes;
         d.chunks = (int32_t)sbt_cdiv(s.page_bytes, kChunkBytes);
         q.chunks += s.n_planes * d.chunks;
-        if (!sbt_aligned16(s.base) || ((s.plane_stride | s.page_stride | s.page_bytes) & 15)) q.vec = 0;
+        bits |= reinterpret_cast<uintptr_t>(s.base) | (uint64_t)(s.plane_stride | s.page_stride | s.page_bytes);
     }
+    q.width = bits & 3 ? 1 : bits & 15 ? 4 : 16;
     return q;
 }
 

@@ -72,16 +72,22 @@ sbt_status sbt_create(int device, sbt_context** out) {
     if ((st = sbt_cuda_check(cudaSetDevice(device), "cudaSetDevice"))) return st;
     sbt_context* c = new sbt_context();
     c->device = device;
-    cudaDeviceProp prop;
-    if ((st = sbt_cuda_check(cudaGetDeviceProperties(&prop, device), "cudaGetDeviceProperties"))) {
-        delete c;
-        return st;
-    }
-    c->sm_count = prop.multiProcessorCount;
-    c->cc_major = prop.major;
-    c->cc_minor = prop.minor;
-    c->smem_optin = prop.sharedMemPerBlockOptin;
-    if (!(prop.major == 10 && prop.minor == 3)) {
+    // four attributes: the whole property record takes the runtime a tenth of a millisecond
+    int sms = 0, major = 0, minor = 0, optin = 0;
+    const struct { int* v; cudaDeviceAttr a; } want[] = {{&sms, cudaDevAttrMultiProcessorCount},
+                                                         {&major, cudaDevAttrComputeCapabilityMajor},
+                                                         {&minor, cudaDevAttrComputeCapabilityMinor},
+                                                         {&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin}};
+    for (const auto& w : want)
+        if ((st = sbt_cuda_check(cudaDeviceGetAttribute(w.v, w.a, device), "cudaDeviceGetAttribute"))) {
+            delete c;
+            return st;
+        }
+    c->sm_count = sms;
+    c->cc_major = major;
+    c->cc_minor = minor;
+    c->smem_optin = (size_t)optin;
+    if (!(major == 10 && minor == 3)) {
         delete c;
         return sbt_fail(SBT_ERR_UNSUPPORTED, "sbt_create: libsbt is built for sm_103a (compute capability 10.3)");
     }

@@ -279,6 +279,14 @@ template <int ES> struct sbt_elem;
 template <> struct sbt_elem<2> { typedef uint16_t T; };
 template <> struct sbt_elem<4> { typedef uint32_t T; };
 
+// Ordinary load.  Kernels that start before the one ahead has finished take
+// this and not the read-only path for what that one may have written: a
+// read-only load may be moved ahead of the wait, and may find an old line.
+template <typename T>
+__device__ __forceinline__ T sbt_ld(const T* p) {
+    return *p;
+}
+
 // Read-only 16-byte load that does not allocate in L1 (streamed data).
 __device__ __forceinline__ uint4 sbt_ld_nc_v4(const void* p) {
     uint4 v;

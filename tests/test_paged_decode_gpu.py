@@ -47,3 +47,40 @@ def test_decode_example(ctx):
     assert np.all(np.abs(ref.f64(last["heads"]) - want[0]) <= ref.attention_bounds(want, "bf16", d)[0])
     assert bool(torch.isfinite(last["y"].float()).all())
     ctx.check_status()
+
+
+def test_a_step_in_a_graph(ctx):
+    """Grow, append and attend captured once and replayed: the same bits as the calls made directly."""
+    import scatter_boundary_tile_gb300 as sbt
+    from paged_decode import PagedLayer
+
+    def state():
+        layer = PagedLayer(ctx)
+        g = torch.Generator(device="cuda").manual_seed(3)
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+        layer.grow(i32([20, 33] + [0] * 6))
+        seq = i32([0] * 20 + [1] * 33)
+        pos = i32(list(range(20)) + list(range(33)))
+        layer.append(torch.randn((53, layer.d_model), generator=g, device="cuda").to(torch.bfloat16), seq, pos)
+        x = torch.randn((2, layer.d_model), generator=g, device="cuda").to(torch.bfloat16)
+        return layer, x, i32([0, 1]), i32([20, 33]), i32([21, 34] + [0] * 6)
+
+    layer, x, seq, pos, target = state()
+    layer.grow(target)
+    want, _, _, heads = layer.step(x, seq, pos)
+    torch.cuda.synchronize()
+
+    layer, x, seq, pos, target = state()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.grow(target)
+        out, _, _, h = layer.step(x, seq, pos)
+    assert int(layer.lens[0]) == 20  # nothing has run yet
+    for _ in range(3):               # the second and third replay find the sequences grown already
+        graph.replay()
+    torch.cuda.synchronize()
+    assert [int(n) for n in layer.lens[:2]] == [21, 34]
+    assert torch.equal(h.view(torch.int16), heads.view(torch.int16))
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    ctx.check_status()
