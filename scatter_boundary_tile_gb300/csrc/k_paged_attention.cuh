@@ -9,10 +9,11 @@
 // rule, which is what lets one row be split.
 //
 // Split.  A row is one (sequence, key-value head, chunk of its query heads),
-// cut into tiles of TOK positions.  All tiles of all rows lie on one line, and
-// warp c of G takes U / G of the U tiles, in order: every warp reads the same
-// amount to within one tile, whatever the lengths are, and the lengths are read
-// on the device.  A row wholly inside one warp's range is written by that
+// cut into tiles of TOK positions.  All rows lie on one line, each as kRowCost
+// empty places (what starting and ending a row costs, in tiles) and a place per
+// tile; warp c of G takes the tiles at U / G of the U places, in order.  So
+// every warp has the same work whatever the lengths are, and the lengths are
+// read on the device.  A row wholly inside one warp's range is written by that
 // warp; of a row cut by range borders each warp writes its state to the
 // workspace and k_attention_join adds them in the order of the line (the result
 // does not depend on which warp finished first).
@@ -33,11 +34,14 @@
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
+#include <algorithm>
+
 #include "sbt_internal.cuh"
 #include "tc_ptx.cuh"
 
 constexpr int kAttnMaxWarps = 16;   // warps per SM the workspace is sized for
 constexpr int kClusterMost = 8, kClusterTiles = 16;
+constexpr int kRowCost = 3;
 constexpr int kAttnMaxHeads = 16;   // query heads of one key-value head that one row carries
 
 // A cut row: the warps first .. last hold its parts, in slot 2 first +
@@ -107,12 +111,12 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {  // a >= 0, b 
     return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
-// U tiles over G warps (1 <= G <= U): the first `more` warps take size + 1, the others size.
+// U places over G warps (1 <= G <= U): the first `more` warps take size + 1, the others size.
 struct Line {
     int64_t size, more;
     __device__ __forceinline__ Line(int64_t U, int64_t G) : size(divide(U, G)) { more = U - size * G; }
     __device__ __forceinline__ int64_t start(int64_t c) const { return c * size + (c < more ? c : more); }
-    // warp whose range holds tile u
+    // warp whose range holds place u
     __device__ __forceinline__ int32_t warp_of(int64_t u) const {
         const int64_t big = more * (size + 1);
         return (int32_t)(u < big ? divide(u, size + 1) : more + divide(u - big, size));
@@ -202,16 +206,18 @@ struct AttnLoader {
     const int32_t rows_per_seq;
     const int64_t v_minus_k;
     AttnRow row;
-    int32_t head, tile, left;
+    int32_t head, tile;
+    int64_t at;             // the next tile's place on the line
+    const int64_t end;      // of the warp's range
     int32_t page, slot;     // this lane's position in the next tile: its page (-1: masked) and slot
 
-    // `left` tiles from tile `tile` of row (row, head) on
+    // the tiles at the places [at, end) of the line, the first of which is tile `tile` of row (row, head)
     __device__ __forceinline__ AttnLoader(const AttnParams& p_, uint8_t* ring_, uint32_t* mask_, const AttnRow& row_,
-                                          int32_t head_, int32_t tile_, int32_t left_)
+                                          int32_t head_, int32_t tile_, int64_t at_, int64_t end_)
         : p(p_), ring(ring_), mask(mask_), ring_u32(sbt_ptx::smem_u32(ring_)), lane(threadIdx.x & 31),
           c0((threadIdx.x & 31) % LPR), r0((threadIdx.x & 31) / LPR), vecs(p_.head_dim * ES / 16),
           rows_per_seq(p_.kv_heads * p_.n_chunks), v_minus_k(p_.v - p_.k), row(row_), head(head_), tile(tile_),
-          left(left_) {
+          at(at_), end(end_) {
         // columns past the head size stay zero for the whole call
         if (p.head_dim < DP) {
             uint32_t* w = reinterpret_cast<uint32_t*>(ring);
@@ -223,10 +229,13 @@ struct AttnLoader {
         for (int s = 0; s < STAGES - 1; ++s) step(s);
     }
 
-    // The tile after (r, h, t) on the line.
-    __device__ __forceinline__ void next(AttnRow& r, int32_t& h, int32_t& t) const {
+    // The tile after (r, h, t) at place u.
+    __device__ __forceinline__ void next(AttnRow& r, int32_t& h, int32_t& t, int64_t& u) const {
+        ++u;
         if (++t < r.tiles) return;
         t = 0;
+        u += kRowCost;
+        if (u >= end) return;  // the range ends here
         if (++h < rows_per_seq) return;
         h = 0;
         int32_t b = r.b + 1;
@@ -240,7 +249,7 @@ struct AttnLoader {
     __device__ __forceinline__ void look_up() {
         const int32_t pos = row.base + tile * TOK + (lane & (TOK - 1));
         slot = 0, page = -1;
-        if (left <= 0 || pos < row.lo || pos >= row.hi) return;
+        if (at >= end || pos < row.lo || pos >= row.hi) return;
         const uint32_t pg = sbt_div(p.page_size, (uint32_t)pos);
         slot = pos - (int32_t)(pg * p.page_size.d);
         page = sbt_ld(p.table + (int64_t)row.seq * p.ld_table + pg);
@@ -257,12 +266,10 @@ struct AttnLoader {
 
     // Starts the next tile's copies into `stage`, then looks up the pages of the one after.
     __device__ __forceinline__ void step(int stage) {
-        if (left > 0) {
+        if (at < end) {
             issue(stage);
-            if (--left > 0) {
-                next(row, head, tile);
-                if (tile == 0) prefetch_q();
-            }
+            next(row, head, tile, at);
+            if (tile == 0 && at < end) prefetch_q();
             look_up();
         }
         sbt_attn::cp_commit();
@@ -385,15 +392,19 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention(const At
         reinterpret_cast<float*>(smem + (size_t)WARPS * STAGES * Loader::STAGE_BYTES) + (size_t)warp * M::SCRATCH;
     sbt_ptx::griddep_wait();
 
-    // ---- the line: tiles of all rows
-    const bool one_step = p.batch <= THREADS;  // every thread holds its own entry's tiles
+    // ---- the line: places of all rows (of one row of entry b: its tiles and kRowCost, or none)
+    auto places = [&](int32_t b) {
+        const int32_t n = row_of<TOK>(p, b).tiles;
+        return n ? n + kRowCost : 0;
+    };
+    const bool one_step = p.batch <= THREADS;  // every thread holds its own entry's places
     int64_t total = 0, at = 0;
     int32_t mine = 0;
     if (one_step) {
-        if ((int32_t)threadIdx.x < p.batch) mine = row_of<TOK>(p, threadIdx.x).tiles;
+        if ((int32_t)threadIdx.x < p.batch) mine = places(threadIdx.x);
         at = block_scan<WARPS>(mine, &total, s_warp);
     } else {
-        for (int32_t b = threadIdx.x; b < p.batch; b += THREADS) total += row_of<TOK>(p, b).tiles;
+        for (int32_t b = threadIdx.x; b < p.batch; b += THREADS) total += places(b);
         int64_t sum;
         block_scan<WARPS>(total, &sum, s_warp);
         total = sum;
@@ -401,11 +412,11 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention(const At
     const int64_t U = total * rows_per_seq;
     const int64_t all_warps = (int64_t)gridDim.x * WARPS, G = U < all_warps ? U : all_warps;
     const int64_t c = (int64_t)blockIdx.x * WARPS + warp;
-    const bool idle = c >= G;
+    bool idle = c >= G;
     const Line line(U, G > 0 ? G : 1);
     const int64_t u0 = idle ? U : line.start(c), u1 = idle ? U : line.start(c + 1);
 
-    // ---- the batch entry that holds tile u0, and its first tile
+    // ---- the batch entry that holds place u0, and its first place
     int32_t b_first = 0;
     int64_t u_first = 0;
     {
@@ -414,7 +425,7 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention(const At
             int64_t sum = total;
             if (!one_step) {
                 const int32_t b = b0 + threadIdx.x;
-                mine = b < p.batch ? row_of<TOK>(p, b).tiles : 0;
+                mine = b < p.batch ? places(b) : 0;
                 at = before + block_scan<WARPS>(mine, &sum, s_warp);
             }
             s_first[threadIdx.x] = at * rows_per_seq;
@@ -449,19 +460,27 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention(const At
         }
     };
     if (!p.desc_by_row && lane == 0) p.desc[c].valid = 0;
+
+    // ---- this warp's tiles
+    AttnRow cr;
+    int32_t c_head = 0, c_tile = 0;
+    int64_t at_u = 0;  // place of the tile the math is at
+    if (!idle) {
+        cr = row_of<TOK>(p, b_first);
+        const int64_t width = cr.tiles + kRowCost;
+        c_head = (int32_t)divide(u0 - u_first, width);
+        const int64_t row_u = u_first + c_head * width + kRowCost;
+        at_u = u0 > row_u ? u0 : row_u;
+        c_tile = (int32_t)(at_u - row_u);
+        idle = at_u >= u1;  // nothing but a row's empty places
+    }
     if (idle) {
         empty_rows();
         return;
     }
+    Loader loader(p, smem + (size_t)warp * STAGES * Loader::STAGE_BYTES, s_mask[warp], cr, c_head, c_tile, at_u, u1);
 
-    // ---- this warp's tiles
-    AttnRow cr = row_of<TOK>(p, b_first);
-    int32_t c_head = (int32_t)divide(u0 - u_first, cr.tiles);
-    int32_t c_tile = (int32_t)((u0 - u_first) - (int64_t)c_head * cr.tiles);
-    int32_t to_do = (int32_t)(u1 - u0);
-    Loader loader(p, smem + (size_t)warp * STAGES * Loader::STAGE_BYTES, s_mask[warp], cr, c_head, c_tile, to_do);
-
-    // block B lies wholly inside a row that covers the tiles [a, e) of the line
+    // block B's ranges lie wholly inside a row whose tiles are at the places [a, e)
     auto inside = [&](int64_t B, int64_t a, int64_t e) {
         return (B + 1) * WARPS <= G && a <= line.start(B * WARPS) && e >= line.start((B + 1) * WARPS);
     };
@@ -472,12 +491,15 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention(const At
     bool first = true;           // the current row is the range's first
     bool cut = c_tile != 0;      // it began in an earlier range
     bool join_block = false;     // this block's warps join their parts
+    bool more = true;
 #pragma unroll 1
-    while (to_do-- > 0) {
+    while (more) {
         loader.do_tile(m, stage, scratch);
         const bool row_end = c_tile + 1 == cr.tiles;
-        if (!row_end && to_do > 0) {
+        more = at_u + (row_end ? 1 + kRowCost : 1) < u1;
+        if (!row_end && more) {
             ++c_tile;
+            ++at_u;
             continue;
         }
         const int32_t kvh = c_head / p.n_chunks, chunk = c_head - kvh * p.n_chunks, h0 = chunk * p.chunk;
@@ -488,8 +510,8 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention(const At
             m.put_row(p, cr.b, qh, heads);
         } else {
             const int slot = first ? 0 : 1;
-            const int64_t row_a = u1 - 1 - to_do - c_tile, row_e = row_a + cr.tiles;  // the row on the line
-            join_block = first && to_do == 0 && inside(blockIdx.x, row_a, row_e);
+            const int64_t row_a = at_u - c_tile, row_e = row_a + cr.tiles;  // the row's tiles on the line
+            join_block = first && !more && inside(blockIdx.x, row_a, row_e);
             if (!join_block)
                 m.put_part(p.part_o + (2 * c + slot) * M::HEADS * DP, p.part_ml + (2 * c + slot) * M::HEADS);
             if (!cut) {
@@ -505,9 +527,9 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention(const At
             else if (e.valid)
                 p.desc[c] = e;
         }
-        if (to_do > 0) {
+        if (more) {
             first = cut = false;
-            loader.next(cr, c_head, c_tile);
+            loader.next(cr, c_head, c_tile, at_u);
             m.load_q(p, cr, c_head, scratch);
         }
     }
@@ -552,7 +574,7 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention_cluster(
     const int32_t w = WARPS * ranks, me = rank * WARPS + warp, size = row.tiles / w, more = row.tiles - size * w;
     const int32_t mine = size + (me < more);
     Loader loader(p, smem + (size_t)warp * STAGES * Loader::STAGE_BYTES, s_mask[warp], row, head,
-                  me * size + min(me, more), mine);
+                  me * size + min(me, more), 0, mine);
     M m;
     m.load_q(p, row, head, scratch);
     int stage = 0;
@@ -597,88 +619,152 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention_cluster(
     cluster.sync();  // no block leaves while another reads its shared memory
 }
 
-// Joins the parts of one cut row, in the order of the line.  Block (i, y) takes
-// the i-th descriptor.  Up to kJoinFew parts (the rule among many rows): a
-// float4 of the [DP][HEADS] state per thread, the blocks y = 0, 1, .. that this
-// takes.  More parts: 64 float4s per block, and GROUPS groups of 64 threads go
-// through the parts side by side, each with its running maximum, and meet in
-// shared memory.
-constexpr int kJoinFew = 8;
+// Joins the parts of the cut rows, each row's in the order of the line.  The
+// first blocks, one or two per descriptor, give the [DP][HEADS] state of a row of
+// up to kJoinFew parts to their threads, a float4 each.  Rows of more parts are
+// few (their parts are blocks' and add up to the grid's); the blocks after those
+// take them in pieces, whose parts groups of threads go through side by side and
+// join in shared memory.  With kJoinDirect descriptors or fewer there is a block
+// for every piece of every row (`piece` float4s: small, many groups); with more,
+// kJoinExtra blocks per SM first look which rows these are.
+constexpr int kJoinThreads = 256, kJoinFew = 8, kJoinDirect = 64, kJoinExtra = 2, kJoinMaxDesc = 8192;
 
-template <class M, int WARPS, int GROUPS>
-__global__ void __launch_bounds__(64 * GROUPS) k_attention_join(const AttnParams p) {
+template <class M, int WARPS>
+__global__ void __launch_bounds__(kJoinThreads) k_attention_join(const AttnParams p, int32_t n_desc, int32_t direct) {
     using namespace sbt_attn;
-    constexpr int HEADS = M::HEADS, DP = M::DP, MH = HEADS < 4 ? HEADS : 4;  // MH: different heads in one float4
-    __shared__ float s_m[GROUPS][64][MH], s_l[GROUPS][64][MH];
-    __shared__ float4 s_o[GROUPS][64];
+    constexpr int HEADS = M::HEADS, N = M::HEADS * M::DP, MH = HEADS < 4 ? HEADS : 4;  // MH: different heads in one float4
+    __shared__ float s_m[kJoinThreads][MH], s_l[kJoinThreads][MH];
+    __shared__ float4 s_o[kJoinThreads];
+    __shared__ uint32_t s_many[kJoinMaxDesc / 32];
     sbt_ptx::griddep_wait();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const AttnDesc e = p.desc[blockIdx.x];
-    if (!e.valid) return;
+
     // parts of the first's block, of the blocks between, of the last's
-    const int bf = e.first / WARPS, bl = e.last / WARPS;
-    const int nf = (e.joined & 1) ? 1 : min(e.last, bf * WARPS + WARPS - 1) - e.first + 1;
-    const int nb = bl > bf ? bl - bf - 1 : 0;
-    const int nl = bl == bf ? 0 : (e.joined & 2) ? 1 : e.last - bl * WARPS + 1;
-    const int n = nf + nb + nl;
-    const bool few = n <= kJoinFew;
-    const int t = few ? threadIdx.x : threadIdx.x & 63, g = few ? 0 : threadIdx.x >> 6, dg = few ? 1 : GROUPS;
-    const int at = (blockIdx.y * (few ? 64 * GROUPS : 64) + t) * 4, head = at % HEADS;  // of the float4's first element
-    const bool in = at < DP * HEADS;
-    if (few && !in) return;
-    auto slot = [&](int i) -> int64_t {
-        if (i < nf) return (e.joined & 1) ? 2ll * bf * WARPS : 2ll * (e.first + i) + (i == 0 ? e.first_slot : 0);
-        i -= nf;
-        return i < nb ? 2ll * (bf + 1 + i) * WARPS : 2ll * (bl * WARPS + i - nb);
+    struct Count {
+        int f, b, n;
     };
-    float m[MH], l[MH];
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
+    auto count = [](const AttnDesc& e) {
+        const int bf = e.first / WARPS, bl = e.last / WARPS;
+        Count c;
+        c.f = (e.joined & 1) ? 1 : min(e.last, bf * WARPS + WARPS - 1) - e.first + 1;
+        c.b = bl > bf ? bl - bf - 1 : 0;
+        c.n = c.f + c.b + (bl == bf ? 0 : (e.joined & 2) ? 1 : e.last - bl * WARPS + 1);
+        return c;
+    };
+    auto slot = [](const AttnDesc& e, const Count& c, int i) -> int64_t {
+        const int bf = e.first / WARPS;
+        if (i < c.f) return (e.joined & 1) ? 2ll * bf * WARPS : 2ll * (e.first + i) + (i == 0 ? e.first_slot : 0);
+        i -= c.f;
+        return i < c.b ? 2ll * (bf + 1 + i) * WARPS : 2ll * ((int64_t)(e.last / WARPS) * WARPS + i - c.b);
+    };
+    struct State {
+        float m[MH], l[MH], o[4];
+        __device__ __forceinline__ State() {
 #pragma unroll
-    for (int k = 0; k < MH; ++k) m[k] = -CUDART_INF_F, l[k] = 0.f;
-    auto add = [&](const float* pm, const float* pl, const float4& x) {
-        const float px[4] = {x.x, x.y, x.z, x.w};
-        float a[MH], b[MH];
+            for (int k = 0; k < MH; ++k) m[k] = -CUDART_INF_F, l[k] = 0.f;
 #pragma unroll
-        for (int k = 0; k < MH; ++k) {
-            const float top = fmaxf(m[k], pm[k]), ts = top == -CUDART_INF_F ? 0.f : top;
-            a[k] = exp2_fast(m[k] - ts), b[k] = exp2_fast(pm[k] - ts);
-            m[k] = top;
-            l[k] = l[k] * a[k] + pl[k] * b[k];
+            for (int k = 0; k < 4; ++k) o[k] = 0.f;
         }
+        __device__ __forceinline__ void add(const float* pm, const float* pl, const float4& x) {
+            const float px[4] = {x.x, x.y, x.z, x.w};
+            float a[MH], b[MH];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = o[k] * a[k % MH] + px[k] * b[k % MH];
+            for (int k = 0; k < MH; ++k) {
+                const float top = fmaxf(m[k], pm[k]), ts = top == -CUDART_INF_F ? 0.f : top;
+                a[k] = exp2_fast(m[k] - ts), b[k] = exp2_fast(pm[k] - ts);
+                m[k] = top;
+                l[k] = l[k] * a[k] + pl[k] * b[k];
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = o[k] * a[k % MH] + px[k] * b[k % MH];
+        }
     };
-    if (in)
+    // parts g, g + step, .. of the float4 that starts at element `at`
+    auto gather = [&](const AttnDesc& e, const Count& c, int at, int g, int step) {
+        State s;
+        const int head = at % HEADS;
 #pragma unroll 4
-        for (int i = g; i < n; i += dg) {
-            const int64_t s = slot(i);
+        for (int i = g; i < c.n; i += step) {
+            const int64_t q = slot(e, c, i);
             float pm[MH], pl[MH];
 #pragma unroll
             for (int k = 0; k < MH; ++k) {
-                const float2 ml = p.part_ml[s * HEADS + head + k];
+                const float2 ml = p.part_ml[q * HEADS + head + k];
                 pm[k] = ml.x, pl[k] = ml.y;
             }
-            add(pm, pl, *reinterpret_cast<const float4*>(p.part_o + s * HEADS * DP + at));
+            s.add(pm, pl, *reinterpret_cast<const float4*>(p.part_o + q * N + at));
         }
-    if (!few) {
+        return s;
+    };
+    auto write = [&](const AttnDesc& e, const State& s, int at) {
+        const int32_t h0 = e.chunk * p.chunk, heads = p.group - h0 < p.chunk ? p.group - h0 : p.chunk;
 #pragma unroll
-        for (int k = 0; k < MH; ++k) s_m[g][t][k] = m[k], s_l[g][t][k] = l[k];
-        s_o[g][t] = make_float4(o[0], o[1], o[2], o[3]);
+        for (int k = 0; k < 4; ++k) {
+            const int h = (at + k) % HEADS, d = (at + k) / HEADS;
+            if (h >= heads || d >= p.head_dim) continue;
+            const int32_t qh = e.kvh * p.group + h0 + h;
+            reinterpret_cast<typename M::T*>(p.out)[e.b * p.ld_out + qh * p.ld_oh + d] =
+                M::from_float(s.o[k] * inverse(s.l[k % MH]));
+            if (d == 0 && p.lse) p.lse[(int64_t)e.b * p.q_heads + qh] = log_sum(s.m[k % MH], s.l[k % MH]);
+        }
+    };
+
+    constexpr int PER_ROW = (N + 4 * kJoinThreads - 1) / (4 * kJoinThreads);
+    const int first = n_desc * PER_ROW;
+    if ((int32_t)blockIdx.x < first) {
+        const AttnDesc e = p.desc[blockIdx.x / PER_ROW];
+        if (!e.valid) return;
+        const Count c = count(e);
+        const int at = ((blockIdx.x % PER_ROW) * kJoinThreads + threadIdx.x) * 4;
+        if (c.n <= kJoinFew && at < N) write(e, gather(e, c, at, 0, 1), at);
+        return;
+    }
+    // piece number i of a row of many parts
+    auto do_piece = [&](const AttnDesc& e, const Count& c, int piece, int i) {
+        const int t = threadIdx.x & (piece - 1), g = threadIdx.x / piece, groups = kJoinThreads / piece;
+        const int at = (i * piece + t) * 4;
+        State s;
+        if (at < N) s = gather(e, c, at, g, groups);
+#pragma unroll
+        for (int k = 0; k < MH; ++k) s_m[threadIdx.x][k] = s.m[k], s_l[threadIdx.x][k] = s.l[k];
+        s_o[threadIdx.x] = make_float4(s.o[0], s.o[1], s.o[2], s.o[3]);
         __syncthreads();
+        if (g == 0 && at < N) {
+            for (int w = 1; w < groups && w < c.n; ++w)
+                s.add(s_m[w * piece + t], s_l[w * piece + t], s_o[w * piece + t]);
+            write(e, s, at);
+        }
+        __syncthreads();
+    };
+    if (direct) {
+        const int pieces = (N / 4 + direct - 1) / direct, item = blockIdx.x - first;
+        const AttnDesc e = p.desc[item / pieces];
+        if (!e.valid) return;
+        const Count c = count(e);
+        if (c.n > kJoinFew) do_piece(e, c, direct, item % pieces);
+        return;
     }
-    if (g != 0 || !in) return;
-    if (!few)
-        for (int w = 1; w < GROUPS; ++w) add(s_m[w][t], s_l[w][t], s_o[w][t]);
-    const int32_t h0 = e.chunk * p.chunk, heads = p.group - h0 < p.chunk ? p.group - h0 : p.chunk;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int h = (at + k) % HEADS, d = (at + k) / HEADS;
-        if (h >= heads || d >= p.head_dim) continue;
-        const int32_t qh = e.kvh * p.group + h0 + h;
-        reinterpret_cast<typename M::T*>(p.out)[e.b * p.ld_out + qh * p.ld_oh + d] =
-            M::from_float(o[k] * inverse(l[k % MH]));
-        if (d == 0 && p.lse) p.lse[(int64_t)e.b * p.q_heads + qh] = log_sum(m[k % MH], l[k % MH]);
+    // which descriptors have many parts, the same list in every block
+    int rows = 0;
+    for (int d0 = 0; d0 < n_desc; d0 += kJoinThreads) {
+        const int d = d0 + threadIdx.x;
+        bool many = false;
+        if (d < n_desc) {
+            const AttnDesc e = p.desc[d];
+            many = e.valid && count(e).n > kJoinFew;
+        }
+        const uint32_t bits = __ballot_sync(0xffffffffu, many);
+        if ((threadIdx.x & 31) == 0 && d < n_desc) s_many[d >> 5] = bits;
+        rows += __syncthreads_count(many);
     }
+    const int blocks = gridDim.x - first;
+    const int piece = rows * (N / 64) <= blocks ? 16 : 64, pieces = (N / 4 + piece - 1) / piece;
+    int item = blockIdx.x - first, base = 0;    // of the pieces of all listed rows; first one of the row at hand
+    for (int w = 0; w * 32 < n_desc && base < rows * pieces; ++w)
+        for (uint32_t bits = s_many[w]; bits; bits &= bits - 1, base += pieces)
+            for (; item < base + pieces; item += blocks) {
+                const AttnDesc e = p.desc[w * 32 + __ffs(bits) - 1];
+                do_piece(e, count(e), piece, item - base);
+            }
 }
 
 // Enqueues the kernel and the join, or the cluster form, for one instantiation.
@@ -708,18 +794,21 @@ sbt_status sbt_attention_enqueue(sbt_context* ctx, AttnParams p, cudaStream_t st
             return st;
         return sbt_after_launch(ctx, "paged_attention");
     }
-    const int most = ctx->sm_count * kAttnMaxWarps / WARPS, grid = resident < most ? resident : most;
+    int grid = std::min(resident, ctx->sm_count * kAttnMaxWarps / WARPS);
+    grid = std::min(grid, kJoinMaxDesc / WARPS);
     p.desc_by_row = rows <= (int64_t)grid * WARPS;
     sbt_status st = sbt_cuda_check(sbt_launch_dependent(k_paged_attention<M, STAGES, WARPS, BLOCKS>, dim3(grid),
                                                         dim3(32 * WARPS), smem, stream, p),
                                    "paged_attention launch");
     if (st || (st = sbt_after_launch(ctx, "paged_attention"))) return st;
-    // few rows may have many parts each: more groups
-    const dim3 join((unsigned)(p.desc_by_row ? rows : (int64_t)grid * WARPS), (M::DP * M::HEADS + 255) / 256);
-    const cudaError_t err =
-        rows <= 64 ? sbt_launch_dependent(k_attention_join<M, WARPS, 16>, join, dim3(1024), 0, stream, p)
-                   : sbt_launch_dependent(k_attention_join<M, WARPS, 4>, join, dim3(256), 0, stream, p);
-    if ((st = sbt_cuda_check(err, "paged_attention join launch"))) return st;
+    const int n_desc = p.desc_by_row ? (int)rows : grid * WARPS;
+    const int direct = n_desc > kJoinDirect ? 0 : n_desc <= 8 ? 8 : 16, quads = M::HEADS * M::DP / 4;
+    const int per_row = (int)sbt_cdiv(quads, kJoinThreads);
+    const int extra = direct ? n_desc * ((quads + direct - 1) / direct) : kJoinExtra * ctx->sm_count;
+    if ((st = sbt_cuda_check(sbt_launch_dependent(k_attention_join<M, WARPS>, dim3(n_desc * per_row + extra),
+                                                  dim3(kJoinThreads), 0, stream, p, n_desc, direct),
+                             "paged_attention join launch")))
+        return st;
     return sbt_after_launch(ctx, "paged_attention join");
 }
 
