@@ -28,11 +28,17 @@
 namespace {
 
 constexpr int kThreads = 128;
-// Forward: heads per group, and blocks per SM the registers are held to.
+// Forward: heads per group, and blocks per SM the registers are held to.  30011
+// fp16 tokens of 32 + 8 + 8 heads of 128 with 4 heads: 113 us at 7 blocks, 117 at 6, 131
+// at 4; with 3 heads 121, with 2 heads 124, with one 167.
 constexpr int kFwdHeads = 4, kFwdBlocks = 7;
-// Rows per SM and group of lanes from which a group takes several heads.
-constexpr int kManyRows = 16;
-// Gradient: heads per item, stages of the ring.
+// Rows per SM and group of lanes from which a group takes several heads, if not more than a
+// quarter of the places stay empty.  bf16, 32 + 8 + 8 heads: 256 tokens 3.9 us with four
+// heads, 3.0 with one; 512 tokens 4.3 and 4.4; 1024 tokens 5.8 and 7.1.  8 + 1 + 1 heads (four
+// leave 6 of 16 places empty): 1024 tokens 4.2 and 3.0, 8192 tokens 10.6 and 10.4.
+constexpr int kManyRows = 10;
+// Gradient: heads per item, stages of the ring.  16384 bf16 tokens of 32 + 8 heads of 128: 84 us
+// with (2, 2); 103 with (1, 2), 121 with (4, 2), 110 with (2, 3).
 constexpr int kBwdHeads = 2, kStages = 2;
 constexpr int kMaxScalarPairs = 8;  // pairs per lane of the element path: 512 elements
 
@@ -619,21 +625,24 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_bwd_elems(const BwdParam
     }
 }
 
-// dw[kind][d] = the blocks' sums, in block order within each of 32 strands and then over the strands.
+// dw[kind][d] = the blocks' sums: 128 strands of blocks side by side for eight
+// elements, then the strands in a fixed order.
 __global__ void __launch_bounds__(1024) k_norm_rope_dw(const BwdParams p) {
-    __shared__ float s[32][33];
+    __shared__ float s[32][8];
     sbt_ptx::griddep_wait();
-    const int kind = blockIdx.y, c = threadIdx.x & 31, strand = threadIdx.x >> 5;
-    const int d = blockIdx.x * 32 + c;
+    const int kind = blockIdx.y, c = threadIdx.x & 7, strand = threadIdx.x >> 3;
+    const int d = blockIdx.x * 8 + c;
     if (!p.dw[kind]) return;
     const float* part = p.partial + (int64_t)(kind ? p.blocks[0] : 0) * p.D;
     float sum = 0.f;
     if (d < p.D)
 #pragma unroll 4
-        for (int i = strand; i < p.blocks[kind]; i += 32) sum += part[(int64_t)i * p.D + d];
-    s[strand][c] = sum;
+        for (int i = strand; i < p.blocks[kind]; i += 128) sum += part[(int64_t)i * p.D + d];
+    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+    if ((threadIdx.x & 31) < 8) s[threadIdx.x >> 5][c] = sum;
     __syncthreads();
-    if (strand == 0 && d < p.D) {
+    if (threadIdx.x < 8 && d < p.D) {
         float t = 0.f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) t += s[i][c];
@@ -712,12 +721,11 @@ void fwd_launch(const sbt_context* ctx, const FwdParams& p, cudaStream_t stream)
     constexpr int GROUPS = kThreads / LPR, HB = kFwdHeads;
     const int64_t total = p.heads[0] + p.heads[1] + p.heads[2];
     const unsigned ty = (unsigned)std::min<int64_t>(sbt_cdiv(p.tokens, GROUPS), 65535);
-    if (p.tokens * total >= (int64_t)ctx->sm_count * kManyRows * GROUPS) {
-        const int64_t hb = sbt_cdiv(p.heads[0], HB) + sbt_cdiv(p.heads[1], HB) + sbt_cdiv(p.heads[2], HB);
+    const int64_t hb = sbt_cdiv(p.heads[0], HB) + sbt_cdiv(p.heads[1], HB) + sbt_cdiv(p.heads[2], HB);
+    if (p.tokens * total >= (int64_t)ctx->sm_count * kManyRows * GROUPS && 3 * hb <= total)
         sbt_launch_dependent(k_norm_rope<KIND, INTER, LPR, HB>, dim3((unsigned)hb, ty), dim3(kThreads), 0, stream, p);
-    } else {
+    else
         sbt_launch_dependent(k_norm_rope<KIND, INTER, LPR, 1>, dim3((unsigned)total, ty), dim3(kThreads), 0, stream, p);
-    }
 }
 
 template <int KIND, bool INTER, int LPR>
@@ -858,7 +866,7 @@ sbt_status sbt_launch_norm_rope_bwd(sbt_context* ctx, sbt_dtype dtype, const Sbt
         st = sbt_after_launch(ctx, "qk_norm_rope_backward");
     }
     if (st || (!dwq && !dwk)) return st;
-    if ((st = sbt_cuda_check(sbt_launch_dependent(k_norm_rope_dw, dim3((D + 31) / 32, 2), dim3(1024), 0, stream, p),
+    if ((st = sbt_cuda_check(sbt_launch_dependent(k_norm_rope_dw, dim3((D + 7) / 8, 2), dim3(1024), 0, stream, p),
                              "qk_norm_rope_backward sums launch")))
         return st;
     return sbt_after_launch(ctx, "qk_norm_rope_backward sums");

@@ -20,11 +20,11 @@
 //
 // After the first prefix sum no warp waits for another: each has a private ring
 // of shared-memory stages filled by cp.async, which runs ahead of the math and
-// across row ends.  Ranges per block with a join of its warps at each row end
-// were measured first: 103 us against 90 on 64 ragged sequences, 142 against 61
-// on 1024 short ones (bf16, 32 query and 8 key-value heads of 128).  Rows
-// fetched by the bulk-copy engine, one 256-byte row a lane, took 136 us there:
-// the engine starts about one row per 15 cycles.
+// across row ends.  Measured before it, bf16, 32 query and 8 key-value heads of
+// 128: ranges per block with a join of its warps at each row end, 103 us on 64
+// ragged sequences up to 4096 and 142 us on 1024 up to 128 (now 94-97 and 68);
+// rows fetched by the bulk-copy engine, one 256-byte row a lane, 136 us on the
+// former: the engine starts about one row per 15 cycles.
 //
 // Positions that are masked (past the length, outside the window, on an
 // unmapped page) are never read from the cache and are zero in shared memory,
@@ -41,6 +41,7 @@
 
 constexpr int kAttnMaxWarps = 16;   // warps per SM the workspace is sized for
 constexpr int kClusterMost = 8, kClusterTiles = 16;
+// 1024 sequences up to 128: 98 us at 0, 68 at 2 and 3, 70 at 5; 64 up to 4096: the same at all four.
 constexpr int kRowCost = 3;
 constexpr int kAttnMaxHeads = 16;   // query heads of one key-value head that one row carries
 
@@ -627,6 +628,7 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention_cluster(
 // join in shared memory.  With kJoinDirect descriptors or fewer there is a block
 // for every piece of every row (`piece` float4s: small, many groups); with more,
 // kJoinExtra blocks per SM first look which rows these are.
+// kJoinFew: 64 sequences up to 4096 112 us at 4, 97 at 8 and 16; 8 up to 8192 36 us at 8, 41 at 16.
 constexpr int kJoinThreads = 256, kJoinFew = 8, kJoinDirect = 64, kJoinExtra = 2, kJoinMaxDesc = 8192;
 
 template <class M, int WARPS>
@@ -779,7 +781,8 @@ sbt_status sbt_attention_enqueue(sbt_context* ctx, AttnParams p, cudaStream_t st
     // The longest row there can be, in tiles.
     const int64_t longest = sbt_cdiv(p.window > 0 && p.window < p.max_len ? (int64_t)p.window + M::TOK : p.max_len, M::TOK);
     // A cluster per row where all clusters fit at once and a warp gets kClusterTiles tiles at most: below
-    // that the second launch and the way through memory cost more than uneven work.
+    // that the second launch and the way through memory cost more than uneven work.  bf16, 32 and 8 heads
+    // of 128: one sequence of 512 7.3 us and 11.5 without, of 4096 11.0 and 12.8; 16 of 2048 26.7 and 32.4.
     int ranks = (int)(resident / rows < kClusterMost ? resident / rows : kClusterMost);
     if (ranks > sbt_cdiv(longest, WARPS)) ranks = (int)sbt_cdiv(longest, WARPS);
     if (ranks < 1) ranks = 1;
