@@ -191,6 +191,18 @@ def test_long_rows_are_split_and_joined(ctx, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("lens,dim,heads", [([40000, 1, 3000], 64, 1),        # few rows of many parts
+                                            ([30000] + [5, 0, 40] * 30, 128, 1),  # one of them among many short ones
+                                            ([2600] * 40, 96, 3),               # every row cut
+                                            ([17000, 9000], 256, 1)])
+def test_rows_cut_over_the_whole_gpu(ctx, kind, lens, dim, heads):
+    c = Case(21, kind, lens, 3 * heads, heads, dim, 24)
+    a = c.check(ctx)
+    b, _ = c.run(ctx)
+    assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_large_scores_and_one_dominant_position(ctx, kind):
     c = Case(15, kind, [500, 500], 4, 2, 64, 16, scale=30.0)
     c.check(ctx)
