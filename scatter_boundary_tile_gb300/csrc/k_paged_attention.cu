@@ -338,7 +338,7 @@ sbt_status sbt_launch_paged_attention(sbt_context* ctx, sbt_dtype dtype, const S
     p.scale_log2 = scale * 1.4426950408889634f;
     const int64_t bits = (reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) |
                          ((int64_t)p.head_dim | p.ld_page | p.ld_slot | p.ld_head) * es;
-    p.copy_bytes = ctx->path == SBT_PATH_SCALAR ? es : bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : es;
+    p.copy_bytes = ctx->path == SBT_PATH_SCALAR ? es : bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : es;
     p.q_words = (reinterpret_cast<uintptr_t>(p.q) | ((int64_t)p.head_dim | p.ld_q | p.ld_qh) * es) % 4 == 0;
     p.out_words = (reinterpret_cast<uintptr_t>(p.out) | ((int64_t)p.head_dim | p.ld_out | p.ld_oh) * es) % 4 == 0;
     const size_t g = (size_t)ctx->sm_count * kAttnMaxWarps;
