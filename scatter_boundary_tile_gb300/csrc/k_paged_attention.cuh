@@ -635,14 +635,14 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention_cluster(
     cluster.sync();  // no block leaves while another reads its shared memory
 }
 
-// Joins the parts of the cut rows, each row's in the order of the line.  The
-// first blocks, one or two per descriptor, give the [DP][HEADS] state of a row of
-// up to kJoinFew parts to their threads, a float4 each.  Rows of more parts are
-// few (their parts are blocks' and add up to the grid's); the blocks after those
-// take them in pieces, whose parts groups of threads go through side by side and
-// join in shared memory.  With kJoinDirect descriptors or fewer there is a block
-// for every piece of every row (`piece` float4s: small, many groups); with more,
-// kJoinExtra blocks per SM first look which rows these are.
+// Joins the parts of the cut rows, each row's in the order of the line.  With
+// kJoinDirect descriptors or fewer there is a block for every piece (`direct`
+// float4s of the [DP][HEADS] state) of every row; groups of threads go through
+// its parts side by side and join in shared memory.  With more, the first blocks,
+// one or two per descriptor, give a row of up to kJoinFew parts to their threads,
+// a float4 each; rows of more parts are few (their parts are blocks' and add up
+// to the grid's), and kJoinExtra blocks per SM look which they are and share
+// their pieces out.
 // kJoinFew: 64 sequences up to 4096 112 us at 4, 97 at 8 and 16; 8 up to 8192 36 us at 8, 41 at 16.
 constexpr int kJoinThreads = 256, kJoinFew = 8, kJoinDirect = 64, kJoinExtra = 2, kJoinMaxDesc = 8192;
 
@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const AttnParam
     };
 
     constexpr int PER_ROW = (N + 4 * kJoinThreads - 1) / (4 * kJoinThreads);
-    const int first = n_desc * PER_ROW;
+    const int first = direct ? 0 : n_desc * PER_ROW;
     if ((int32_t)blockIdx.x < first) {
         const AttnDesc e = p.desc[blockIdx.x / PER_ROW];
         if (!e.valid) return;
@@ -756,8 +756,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const AttnParam
         const int pieces = (N / 4 + direct - 1) / direct, item = blockIdx.x - first;
         const AttnDesc e = p.desc[item / pieces];
         if (!e.valid) return;
-        const Count c = count(e);
-        if (c.n > kJoinFew) do_piece(e, c, direct, item % pieces);
+        do_piece(e, count(e), direct, item % pieces);
         return;
     }
     // which descriptors have many parts, the same list in every block
@@ -820,10 +819,16 @@ sbt_status sbt_attention_enqueue(sbt_context* ctx, AttnParams p, cudaStream_t st
                                    "paged_attention launch");
     if (st || (st = sbt_after_launch(ctx, "paged_attention"))) return st;
     const int n_desc = p.desc_by_row ? (int)rows : grid * WARPS;
-    const int direct = n_desc > kJoinDirect ? 0 : n_desc <= 8 ? 8 : 16, quads = M::HEADS * M::DP / 4;
-    const int per_row = (int)sbt_cdiv(quads, kJoinThreads);
-    const int extra = direct ? n_desc * ((quads + direct - 1) / direct) : kJoinExtra * ctx->sm_count;
-    if ((st = sbt_cuda_check(sbt_launch_dependent(k_attention_join<M, WARPS>, dim3(n_desc * per_row + extra),
+    const int quads = M::HEADS * M::DP / 4;
+    int direct = 0, blocks = n_desc * (int)sbt_cdiv(quads, kJoinThreads) + kJoinExtra * ctx->sm_count;
+    if (n_desc <= kJoinDirect) {
+        // the smallest pieces of which two blocks per SM are enough: 8 sequences up to 8192 34.2 us; 35.8 with
+        // fixed pieces for long rows and a thread per float4 for rows of up to kJoinFew parts
+        direct = 8;
+        while (direct < 64 && n_desc * sbt_cdiv(quads, direct) > 2 * ctx->sm_count) direct *= 2;
+        blocks = n_desc * (int)sbt_cdiv(quads, direct);
+    }
+    if ((st = sbt_cuda_check(sbt_launch_dependent(k_attention_join<M, WARPS>, dim3(blocks),
                                                   dim3(kJoinThreads), 0, stream, p, n_desc, direct),
                              "paged_attention join launch")))
         return st;
