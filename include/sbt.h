@@ -410,7 +410,9 @@ typedef struct {
  * for b < batch, h < q_heads.  A row that sees no position (length 0, seq[b]
  * outside [0, n_seq), no mapped page), or whose scores are all minus infinity,
  * gets out = 0 and lse = minus infinity.  Cache contents at positions that are
- * not visible are never read: NaN there reaches nothing.
+ * not visible are never read: NaN there reaches nothing.  A score of plus
+ * infinity or NaN gives NaN in its row; an infinite V at a visible position
+ * gives infinity or NaN in its column.  out must not overlap q or the cache.
  *
  * dtype: of q, the cache and out.  Products and sums are fp32; with SBT_BF16
  * and SBT_F16 the probabilities enter the second product with 16 and 11

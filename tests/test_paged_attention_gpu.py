@@ -286,3 +286,40 @@ def test_refusals(ctx):
         assert e.value.status == status, kw
     assert ctx.launch_count == before
 
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("lens,dim,group", [([1, 17, 300], 64, 4), ([20000, 3, 2500], 128, 3), ([900] * 40, 80, 9)])
+@pytest.mark.parametrize("what", ["key nan", "key inf", "query nan", "value inf", "value nan"])
+def test_infinities_and_nan_that_are_visible(ctx, kind, lens, dim, group, what):
+    """They reach the rows (or the column, for values) that they belong to, and no others."""
+    heads = 2
+    c = Case(11, kind, lens, heads * group, heads, dim, 16)
+    s, h, d = len(lens) - 1, 1, dim - 1  # sequence, key-value head, element
+    rows = np.zeros((c.B, c.Hq), bool)
+    x = float(what[-3:])
+    t = lens[s] // 2
+    at = c.offset + c.table[s, t // 16] * c.ld_page + (t % 16) * c.ld_slot + h * c.ld_head + d
+    rows[s, h * group:] = True
+    if what.startswith("key"):
+        c.q[s, h * group:, d] = 1.0  # scores of plus infinity or NaN
+        c.kbuf[at] = x
+    elif what.startswith("query"):
+        rows[s, h * group:] = False
+        rows[s, -1] = True
+        c.q[s, -1, d] = x
+    want = c.want()  # before the values are touched: what the other columns hold
+    if what.startswith("value"):
+        c.vbuf[at] = x
+    out, lse = c.run(ctx)
+    out = ref.f64(out)
+    ob, lb = ref.attention_bounds(want, kind, dim)
+    cells = np.broadcast_to(rows[..., None], out.shape).copy()
+    if what.startswith("value"):
+        cells[..., :d] = False
+        assert not np.isfinite(out[cells]).any()
+        rows[:] = False
+    else:
+        assert np.isnan(out[cells]).all() and np.isnan(lse[rows]).all()
+    assert np.all(np.abs(out - want[0])[~cells] <= ob[~cells])
+    assert np.all(np.abs(lse - want[1])[~rows] <= lb[~rows])
