@@ -415,8 +415,9 @@ typedef struct {
  * gives infinity or NaN in its column.  out must not overlap q or the cache.
  *
  * dtype: of q, the cache and out.  Products and sums are fp32; with SBT_BF16
- * and SBT_F16 the probabilities enter the second product with 16 and 11
- * significant bits.  1 <= head_dim <= 256; cache->heads divides q_heads.
+ * and SBT_F16 a probability enters the second product as the sum of two 16-bit
+ * numbers, 16 and 22 significant bits (with SBT_F16 in steps of 2^-39 of the
+ * row's largest one at least).  1 <= head_dim <= 256; cache->heads divides q_heads.
  * q, out: strides in elements per batch entry (ld_q, ld_out) and head (ld_qh,
  * ld_oh).  lse: device fp32, dense [batch][q_heads], or NULL.
  * workspace: device scratch of sbt_paged_attention_workspace_size() bytes,
