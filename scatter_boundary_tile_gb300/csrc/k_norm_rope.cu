@@ -195,10 +195,12 @@ __device__ __forceinline__ void angles(const float2* row, const Place& q, float*
 }
 
 // Turns the lane's 2 V elements (x[0..V) of vector a, x[V..2V) of vector b); sign -1: the transpose.
+// Pairs that are not turned are left alone, not turned by an angle of 0: 0 times an infinite partner is NaN.
 template <int V, bool INTER>
-__device__ __forceinline__ void turn(float* x, const float* cs, const float* sn, float sign) {
+__device__ __forceinline__ void turn(float* x, const Place& q, const float* cs, const float* sn, float sign) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+        if (q.pair[i / (V / 2)] < 0) continue;
         const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : V + i;
         const float a = x[ia], b = x[ib], s = sign * sn[i];
         x[ia] = a * cs[i] - b * s;
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, HB == 1 ? 1 : kFwdBlocks) k_norm_rop
 #pragma unroll
                     for (int e = 0; e < 2 * V; ++e) f[e] = f[e] * r * w[e];
                 }
-                turn<V, INTER>(f, cs, sn, 1.f);
+                turn<V, INTER>(f, at, cs, sn, 1.f);
                 a = real ? pack<KIND>(f) : zero;
                 b = real ? pack<KIND>(f + V) : zero;
             }
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_bwd(const BwdParams p) {
             float u[2 * V];
             unpack<KIND>(row && real && at.a >= 0 ? v[(4 * i) * kThreads] : zero, u);
             unpack<KIND>(row && real && at.b >= 0 ? v[(4 * i + 1) * kThreads] : zero, u + V);
-            turn<V, INTER>(u, cs, sn, -1.f);
+            turn<V, INTER>(u, at, cs, sn, -1.f);
             if (wp) {
                 float x[2 * V], ss = 0.f, dot = 0.f;
                 unpack<KIND>(row && real && at.a >= 0 ? v[(4 * i + 2) * kThreads] : zero, x);
