@@ -85,21 +85,22 @@ Plan plan_of(void* ws, int32_t n_seq, int64_t n_pages) {
 }
 
 // Exclusive prefix of one value per thread over the block, and the block's sum.
-__device__ __forceinline__ int32_t scan(int32_t v, int32_t* total, int32_t* s_warp) {
+template <typename T>
+__device__ __forceinline__ T scan(T v, T* total, T* s_warp) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int32_t x = v;
+    T x = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int32_t y = __shfl_up_sync(0xffffffffu, x, d);
+        const T y = __shfl_up_sync(0xffffffffu, x, d);
         if (lane >= d) x += y;
     }
     __syncthreads();
     if (lane == 31) s_warp[warp] = x;
     __syncthreads();
-    int32_t w = s_warp[lane], t = w;
+    T w = s_warp[lane], t = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int32_t y = __shfl_up_sync(0xffffffffu, t, d);
+        const T y = __shfl_up_sync(0xffffffffu, t, d);
         if (lane >= d) t += y;
     }
     *total = __shfl_sync(0xffffffffu, t, 31);
@@ -115,7 +116,7 @@ __device__ int32_t collect_free(const Map& m, int32_t want, int32_t* list, int32
         bool f[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = p + i < m.n_pages && m.refs[p + i] <= 0;
-        int32_t total, at = found + scan(f[0] + f[1] + f[2] + f[3], &total, s_warp);
+        int32_t total, at = found + scan<int32_t>(f[0] + f[1] + f[2] + f[3], &total, s_warp);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (f[i]) list[at++] = (int32_t)(p + i);
@@ -209,10 +210,12 @@ __global__ void __launch_bounds__(kMoveThreads) k_pages_free(const Map m, const 
 __global__ void __launch_bounds__(kPlanThreads) k_pages_reserve(const Map m, const Plan w, const int32_t* target) {
     griddep_wait();
     __shared__ int32_t s_warp[32];
+    __shared__ int64_t s_warp64[32];
     __shared__ int32_t s_moves;
     if (threadIdx.x == 0) s_moves = 0;
-    // need[b]: pages past the ones held, and one more where the last page is part full and shared
-    int32_t total = 0;
+    // need[b]: pages past the ones held, and one more where the last page is part full and shared.  What all
+    // sequences ask for may add up to n_seq * max_pages, far more than any pool holds: 64 bits.
+    int64_t total = 0;
     for (int32_t b0 = 0; b0 < m.n_seq; b0 += kPlanThreads) {
         const int32_t b = b0 + threadIdx.x;
         int32_t need = 0, own = 0;
@@ -229,18 +232,18 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_reserve(const Map m, con
             w.a[b] = need;
             w.b[b] = own;
         }
-        int32_t sum;
-        const int32_t at = total + scan(need, &sum, s_warp);
-        if (b < m.n_seq) w.c[b] = at;
+        int64_t sum;
+        const int64_t at = total + scan<int64_t>(need, &sum, s_warp64);
+        if (b < m.n_seq) w.c[b] = (int32_t)min(at, (int64_t)INT32_MAX);  // there: past every list
         total += sum;
     }
-    const int32_t found = total ? collect_free(m, total, w.free, s_warp) : 0;
+    const int32_t found = total ? collect_free(m, (int32_t)min(total, (int64_t)m.n_pages), w.free, s_warp) : 0;
     __syncthreads();
     // a warp per sequence: served if it needs no page or its pages end inside the list
     for (int32_t b = threadIdx.x >> 5; b < m.n_seq; b += kPlanThreads / 32) {
         const int lane = threadIdx.x & 31;
         const int32_t n = m.lens[b], t = sbt_ld(target + b), need = w.a[b], own = w.b[b], at = w.c[b];
-        if (t <= n || m.pages_of(t) > m.max_pages || (need && at + need > found)) continue;
+        if (t <= n || m.pages_of(t) > m.max_pages || (need && need > found - at)) continue;
         const int32_t first = m.pages_of(n) - own;
         for (int32_t i = lane; i < need; i += 32) {
             const int32_t p = w.free[at + i];
