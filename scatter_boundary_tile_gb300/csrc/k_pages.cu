@@ -7,6 +7,8 @@
 // served in order, and the counts change by integer atomics whose order cannot
 // be seen.
 //
+// Extents go up to 2^31 - 1, so counters that step past one have 64 bits.
+//
 // Deciding is a few prefix sums over the sequences and the pages; one block of
 // 1024 threads does it (a pass over 65,536 counts is 256 KB) and leaves a plan
 // in the workspace.  Moving the pages' bytes is memory-bound; the second
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_pages_free(const Map m, const 
     // a sequence listed twice: both occurrences may see the old length; the exchange lets only one of
     // them release a page
     const int32_t end = m.held(*(volatile int32_t*)(m.lens + s));
-    for (int32_t j = m.pages_of(k) + threadIdx.x; j < end; j += kMoveThreads) {
+    for (int64_t j = (int64_t)m.pages_of(k) + threadIdx.x; j < end; j += kMoveThreads) {
         const int32_t p = atomicExch(m.table + s * m.ld + j, -1);
         if (m.page_ok(p)) atomicSub(m.refs + p, 1);
     }
@@ -216,8 +218,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_reserve(const Map m, con
     // need[b]: pages past the ones held, and one more where the last page is part full and shared.  What all
     // sequences ask for may add up to n_seq * max_pages, far more than any pool holds: 64 bits.
     int64_t total = 0;
-    for (int32_t b0 = 0; b0 < m.n_seq; b0 += kPlanThreads) {
-        const int32_t b = b0 + threadIdx.x;
+    for (int64_t b0 = 0; b0 < m.n_seq; b0 += kPlanThreads) {
+        const int64_t b = b0 + threadIdx.x;
         int32_t need = 0, own = 0;
         if (b < m.n_seq) {
             const int32_t n = m.lens[b], t = sbt_ld(target + b);
@@ -240,12 +242,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_reserve(const Map m, con
     const int32_t found = total ? collect_free(m, (int32_t)min(total, (int64_t)m.n_pages), w.free, s_warp) : 0;
     __syncthreads();
     // a warp per sequence: served if it needs no page or its pages end inside the list
-    for (int32_t b = threadIdx.x >> 5; b < m.n_seq; b += kPlanThreads / 32) {
+    for (int64_t b = threadIdx.x >> 5; b < m.n_seq; b += kPlanThreads / 32) {
         const int lane = threadIdx.x & 31;
         const int32_t n = m.lens[b], t = sbt_ld(target + b), need = w.a[b], own = w.b[b], at = w.c[b];
         if (t <= n || m.pages_of(t) > m.max_pages || (need && need > found - at)) continue;
         const int32_t first = m.pages_of(n) - own;
-        for (int32_t i = lane; i < need; i += 32) {
+        for (int64_t i = lane; i < need; i += 32) {
             const int32_t p = w.free[at + i];
             if (i == 0 && own) {
                 const int32_t old = m.table[b * m.ld + first];
@@ -270,21 +272,21 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_fork(const Map m, const 
                                                              const int32_t* to, int32_t n) {
     griddep_wait();
     __shared__ int32_t s_warp[32];
-    auto ok = [&](int32_t i, int32_t& a, int32_t& c) {
+    auto ok = [&](int64_t i, int32_t& a, int32_t& c) {
         a = sbt_ld(from + i), c = sbt_ld(to + i);
         return a >= 0 && a < m.n_seq && c >= 0 && c < m.n_seq && a != c && m.lens[a] > 0 && m.lens[c] == 0;
     };
     int32_t a, c;
-    for (int32_t i = threadIdx.x; i < n; i += kPlanThreads)
+    for (int64_t i = threadIdx.x; i < n; i += kPlanThreads)
         if (ok(i, a, c)) w.claim[c] = 0x7fffffff;
     __syncthreads();
-    for (int32_t i = threadIdx.x; i < n; i += kPlanThreads)
-        if (ok(i, a, c)) atomicMin(w.claim + c, i);
+    for (int64_t i = threadIdx.x; i < n; i += kPlanThreads)
+        if (ok(i, a, c)) atomicMin(w.claim + c, (int32_t)i);
     __syncthreads();
     // a[i]: parent's length or 0 (pair not taken); b[i]: place of the child's last page in the free list or -1
     int32_t total = 0;
-    for (int32_t i0 = 0; i0 < n; i0 += kPlanThreads) {
-        const int32_t i = i0 + threadIdx.x;
+    for (int64_t i0 = 0; i0 < n; i0 += kPlanThreads) {
+        const int64_t i = i0 + threadIdx.x;
         int32_t len = 0, part = 0;
         if (i < n && ok(i, a, c) && w.claim[c] == i) {
             len = m.lens[a];
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_fork(const Map m, const 
     }
     const int32_t found = total ? collect_free(m, total, w.free, s_warp) : 0;
     __syncthreads();
-    for (int32_t i = threadIdx.x; i < n; i += kPlanThreads) {
+    for (int64_t i = threadIdx.x; i < n; i += kPlanThreads) {
         const int32_t len = w.a[i], at = w.b[i];
         int32_t src = -1, dst = -1;
         if (len > 0) {
@@ -329,11 +331,11 @@ __global__ void __launch_bounds__(kMoveThreads) k_pages_fork_rows(const __grid_c
                                                                   const Plan w, const int32_t* from, const int32_t* to,
                                                                   int32_t n) {
     griddep_wait();
-    for (int32_t i = blockIdx.x; i < n; i += gridDim.x) {
+    for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
         const int32_t len = w.a[i];
         if (len <= 0) continue;
         const int32_t a = sbt_ld(from + i), c = sbt_ld(to + i), pages = m.held(len);
-        for (int32_t j = threadIdx.x; j < pages; j += kMoveThreads) {
+        for (int64_t j = threadIdx.x; j < pages; j += kMoveThreads) {
             int32_t p = m.table[a * m.ld + j];
             if (j == pages - 1 && w.dst[i] >= 0) {
                 p = w.dst[i];
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_compact(const Map m, con
     griddep_wait();
     __shared__ int32_t s_warp[32];
     int32_t mine = 0, live;
-    for (int32_t p = threadIdx.x; p < m.n_pages; p += kPlanThreads) mine += m.refs[p] > 0;
+    for (int64_t p = threadIdx.x; p < m.n_pages; p += kPlanThreads) mine += m.refs[p] > 0;
     scan(mine, &live, s_warp);
     int32_t holes = 0, movers = 0;
     for (int64_t p0 = 0; p0 < m.n_pages; p0 += kPlanThreads) {
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_compact(const Map m, con
         movers += sum >> 16;
     }
     __syncthreads();
-    for (int32_t p = threadIdx.x; p < m.n_pages; p += kPlanThreads) {
+    for (int64_t p = threadIdx.x; p < m.n_pages; p += kPlanThreads) {
         const int32_t to = o.page_to[p];
         if (to >= 0) {
             o.refs[p] = m.refs[p];
@@ -403,9 +405,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_compact(const Map m, con
 __global__ void __launch_bounds__(kMoveThreads) k_pages_compact_rows(const __grid_constant__ Pools q, const Map m,
                                                                      const Plan w, const Packed o) {
     griddep_wait();
-    for (int32_t s = blockIdx.x; s < m.n_seq; s += gridDim.x) {
+    for (int64_t s = blockIdx.x; s < m.n_seq; s += gridDim.x) {
         const int32_t pages = m.held(m.lens[s]);
-        for (int32_t j = threadIdx.x; j < pages; j += kMoveThreads) {
+        for (int64_t j = threadIdx.x; j < pages; j += kMoveThreads) {
             const int32_t p = m.table[s * m.ld + j];
             o.table[s * o.ld + j] = m.page_ok(p) ? o.page_to[p] : -1;
         }
