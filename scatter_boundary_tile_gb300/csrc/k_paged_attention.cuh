@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention(const At
         if ((int32_t)threadIdx.x < p.batch) mine = places(threadIdx.x);
         at = block_scan<WARPS>(mine, &total, s_warp);
     } else {
-        for (int32_t b = threadIdx.x; b < p.batch; b += THREADS) total += places(b);
+        for (uint32_t b = threadIdx.x; b < (uint32_t)p.batch; b += THREADS) total += places((int32_t)b);
         int64_t sum;
         block_scan<WARPS>(total, &sum, s_warp);
         total = sum;
@@ -437,11 +437,11 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention(const At
     int64_t u_first = 0;
     {
         int64_t before = 0;
-        for (int32_t b0 = 0; b0 < p.batch; b0 += THREADS) {
+        for (uint32_t b0 = 0; b0 < (uint32_t)p.batch; b0 += THREADS) {  // unsigned: the last step may pass 2^31
             int64_t sum = total;
             if (!one_step) {
-                const int32_t b = b0 + threadIdx.x;
-                mine = b < p.batch ? places(b) : 0;
+                const uint32_t b = b0 + threadIdx.x;
+                mine = b < (uint32_t)p.batch ? places((int32_t)b) : 0;
                 at = before + block_scan<WARPS>(mine, &sum, s_warp);
             }
             s_first[threadIdx.x] = at * rows_per_seq;
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention(const At
                     const int64_t end = i + 1 < THREADS ? s_first[i + 1] : (before + sum) * rows_per_seq;
                     const uint32_t hit = __ballot_sync(0xffffffffu, s_first[i] <= u0 && u0 < end);
                     if (hit) {
-                        b_first = b0 + (i & ~31) + __ffs(hit) - 1;
+                        b_first = (int32_t)b0 + (i & ~31) + __ffs(hit) - 1;
                         u_first = s_first[(i & ~31) + __ffs(hit) - 1];
                     }
                 }
@@ -465,14 +465,14 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) k_paged_attention(const At
     auto empty_rows = [&]() {
         for (int64_t b = c; b < p.batch; b += all_warps) {
             if (row_of<TOK>(p, (int32_t)b).tiles != 0) continue;
-            for (int32_t i = lane; i < p.q_heads * p.head_dim; i += 32) {
-                const int32_t h = i / p.head_dim, d = i - h * p.head_dim;
+            for (uint32_t i = lane; i < (uint32_t)(p.q_heads * p.head_dim); i += 32) {
+                const uint32_t h = i / (uint32_t)p.head_dim, d = i - h * (uint32_t)p.head_dim;
                 reinterpret_cast<typename M::T*>(p.out)[b * p.ld_out + h * p.ld_oh + d] = typename M::T(0);
             }
             if (p.lse)
-                for (int32_t h = lane; h < p.q_heads; h += 32) p.lse[b * p.q_heads + h] = -CUDART_INF_F;
+                for (uint32_t h = lane; h < (uint32_t)p.q_heads; h += 32) p.lse[b * p.q_heads + h] = -CUDART_INF_F;
             if (p.desc_by_row)
-                for (int32_t h = lane; h < rows_per_seq; h += 32) p.desc[b * rows_per_seq + h].valid = 0;
+                for (uint32_t h = lane; h < (uint32_t)rows_per_seq; h += 32) p.desc[b * rows_per_seq + h].valid = 0;
         }
     };
     if (!p.desc_by_row && lane == 0) p.desc[c].valid = 0;

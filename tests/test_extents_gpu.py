@@ -31,3 +31,23 @@ def test_grow_to_more_than_a_row_holds(ctx, P):
     s.reserve([4, 1, TOP - 40, -(2**31)])
     s.check()
     s.held_consistent()
+
+
+def test_an_empty_row_of_as_many_elements_as_there_may_be(ctx):
+    """2^31 - 1 query heads of one element: the last steps over out and lse pass 2^31."""
+    n = TOP
+    x = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((n + 65,), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n + 65,), 3.0, device="cuda")
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    table, lens = i32([[-1]]), i32([0])
+    size = sbt.paged_attention_workspace_size(ctx, n, 1, 1)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    sbt.paged_attention(ctx, x, 0, 0, 1, n, sbt.kv_cache(x, x, 1, 1, 1, 1, 1), sbt.page_map(table, 1, 1, 1, lens, 1, 1),
+                        1.0, out, n, 1, lse=lse, workspace=ws, workspace_bytes=size)
+    torch.cuda.synchronize()
+    assert bool((out[n:] == 3).all()) and bool((lse[n:] == 3).all())
+    step = 1 << 28
+    for i in range(0, n, step):
+        e = min(n, i + step)
+        assert not bool(out[i:e].any()) and bool(torch.isneginf(lse[i:e]).all())
