@@ -455,8 +455,8 @@ typedef struct {
     int32_t layout;    /* sbt_rope_layout */
 } sbt_rope;
 
-/* Fills table[n_pos][rot_dim/2][2] with amplitude * (cos, sin)(t * f_i), angles
- * formed in 64 bits and rounded once.  base > 0, factor > 0; low, high and
+/* Fills table[n_pos][rot_dim/2][2] (2^40 pairs at most) with amplitude * (cos,
+ * sin)(t * f_i), angles formed in 64 bits and rounded once.  base > 0, factor > 0; low, high and
  * orig_len are read by SBT_ROPE_BY_PARTS only (high > low, orig_len > 0). */
 SBT_API sbt_status sbt_rope_table(sbt_context* ctx, float* table, int64_t n_pos, int32_t rot_dim, double base,
                                   sbt_rope_scaling scaling, double factor, int64_t orig_len, double low, double high,
@@ -484,7 +484,8 @@ SBT_API sbt_status sbt_rope_table(sbt_context* ctx, float* table, int64_t n_pos,
  * and head, so that they may be parts of one packed projection; k and v have
  * k_heads heads.  q_out may be q and k_out may be k (same strides).
  * 1 <= head_dim <= 512; with a cache, cache->heads = k_heads and
- * cache->head_dim = head_dim.  k_heads = 0 or q_heads = 0 leaves that part out.
+ * cache->head_dim = head_dim.  k_heads = 0 or q_heads = 0 leaves that part out;
+ * q_heads + 2 k_heads is at most 2^30.
  */
 SBT_API sbt_status sbt_qk_norm_rope(sbt_context* ctx, sbt_dtype dtype, const void* q, int64_t ld_q, int64_t ld_qh,
                                     const void* k, int64_t ld_k, int64_t ld_kh, int64_t tokens, int32_t q_heads,

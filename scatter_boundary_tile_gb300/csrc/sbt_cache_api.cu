@@ -63,6 +63,13 @@ sbt_status check_rows(const SbtHeadRows& r, int64_t tokens, int32_t heads, int32
     return SBT_OK;
 }
 
+// A launch has a block for every head of the queries, keys and values at most, and counts them in 32 bits.
+sbt_status check_heads(int64_t tokens, int32_t q_heads, int32_t k_heads, const char* what) {
+    SBT_REQUIRE(tokens >= 0 && q_heads >= 0 && k_heads >= 0, say(what, ": negative extent"));
+    SBT_REQUIRE((int64_t)q_heads + 2 * (int64_t)k_heads <= 1 << 30, say(what, ": q_heads + 2 k_heads too large"));
+    return SBT_OK;
+}
+
 sbt_status check_rope(const sbt_rope* r, int32_t head_dim, const char* what) {
     if (!r || r->rot_dim == 0) return SBT_OK;
     SBT_REQUIRE(r->rot_dim > 0 && r->rot_dim % 2 == 0 && r->rot_dim <= head_dim,
@@ -145,6 +152,7 @@ sbt_status sbt_rope_table(sbt_context* ctx, float* table, int64_t n_pos, int32_t
         return sbt_fail(SBT_ERR_UNSUPPORTED, "rope_table: unknown scaling");
     SBT_REQUIRE(n_pos >= 0 && n_pos < (1ll << 40), "rope_table: n_pos out of range");
     SBT_REQUIRE(rot_dim >= 0 && rot_dim % 2 == 0, "rope_table: rot_dim must be even");
+    SBT_REQUIRE(rot_dim < 2 || n_pos <= (1ll << 40) / (rot_dim / 2), "rope_table: table too large");
     SBT_REQUIRE(base > 0.0 && factor > 0.0, "rope_table: base and factor must be positive");
     SBT_REQUIRE(scaling != SBT_ROPE_BY_PARTS || (high > low && orig_len > 0),
                 "rope_table: scaling by parts needs high > low and orig_len > 0");
@@ -167,7 +175,7 @@ sbt_status sbt_qk_norm_rope(sbt_context* ctx, sbt_dtype dtype, const void* q, in
     SBT_REQUIRE(ctx, "ctx is NULL");
     SBT_TRY(check_dtype(dtype, w));
     const int es = sbt_dtype_size(dtype);
-    SBT_REQUIRE(tokens >= 0 && q_heads >= 0 && k_heads >= 0, "qk_norm_rope: negative extent");
+    SBT_TRY(check_heads(tokens, q_heads, k_heads, w));
     SBT_REQUIRE(head_dim >= 1 && head_dim <= 512, "qk_norm_rope: head_dim must be in [1, 512]");
     SBT_TRY(check_rope(rope, head_dim, w));
     SBT_REQUIRE(eps >= 0.f, "qk_norm_rope: negative eps");
@@ -218,7 +226,7 @@ sbt_status sbt_qk_norm_rope_backward(sbt_context* ctx, sbt_dtype dtype, const vo
     SBT_REQUIRE(ctx, "ctx is NULL");
     SBT_TRY(check_dtype(dtype, w));
     const int es = sbt_dtype_size(dtype);
-    SBT_REQUIRE(tokens >= 0 && q_heads >= 0 && k_heads >= 0, "qk_norm_rope_backward: negative extent");
+    SBT_TRY(check_heads(tokens, q_heads, k_heads, w));
     SBT_REQUIRE(head_dim >= 1 && head_dim <= 512, "qk_norm_rope_backward: head_dim must be in [1, 512]");
     SBT_TRY(check_rope(rope, head_dim, w));
     SBT_REQUIRE(eps >= 0.f, "qk_norm_rope_backward: negative eps");
