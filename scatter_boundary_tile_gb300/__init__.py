@@ -165,7 +165,11 @@ _torch = None  # the torch module, its raw-stream query and its dtypes' codes, o
 def _load_torch():
     global _torch, _raw_stream, _device_index, _CODES
     import torch
-    _raw_stream, _device_index = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+    _device_index = torch.cuda.current_device
+    # not a public name of torch: without it a Stream object is built per call
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if _raw_stream is None:
+        _raw_stream = lambda device: torch.cuda.current_stream(device).cuda_stream
     _CODES = {torch.float32: SBT_F32, torch.bfloat16: SBT_BF16, torch.float16: SBT_F16}
     _torch = torch
 
