@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_reserve(const Map m, con
         const int64_t b = b0 + threadIdx.x;
         int32_t need = 0, own = 0;
         if (b < m.n_seq) {
-            const int32_t n = m.lens[b], t = sbt_ld(target + b);
+            const int32_t n = max(m.lens[b], 0), t = sbt_ld(target + b);
             if (t > n && m.pages_of(t) <= m.max_pages) {
                 need = m.pages_of(t) - m.pages_of(n);
                 if (n > 0 && n - (int32_t)(sbt_div(m.page_size, (uint32_t)n) * m.page_size.d) != 0) {
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_reserve(const Map m, con
     // a warp per sequence: served if it needs no page or its pages end inside the list
     for (int64_t b = threadIdx.x >> 5; b < m.n_seq; b += kPlanThreads / 32) {
         const int lane = threadIdx.x & 31;
-        const int32_t n = m.lens[b], t = sbt_ld(target + b), need = w.a[b], own = w.b[b], at = w.c[b];
+        const int32_t n = max(m.lens[b], 0), t = sbt_ld(target + b), need = w.a[b], own = w.b[b], at = w.c[b];
         if (t <= n || m.pages_of(t) > m.max_pages || (need && need > found - at)) continue;
         const int32_t first = m.pages_of(n) - own;
         for (int64_t i = lane; i < need; i += 32) {
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_fork(const Map m, const 
     __shared__ int32_t s_warp[32];
     auto ok = [&](int64_t i, int32_t& a, int32_t& c) {
         a = sbt_ld(from + i), c = sbt_ld(to + i);
-        return a >= 0 && a < m.n_seq && c >= 0 && c < m.n_seq && a != c && m.lens[a] > 0 && m.lens[c] == 0;
+        return a >= 0 && a < m.n_seq && c >= 0 && c < m.n_seq && a != c && m.lens[a] > 0 && m.lens[c] <= 0;
     };
     int32_t a, c;
     for (int64_t i = threadIdx.x; i < n; i += kPlanThreads)
