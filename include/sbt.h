@@ -402,7 +402,7 @@ typedef struct {
  *
  *   visible(b) = positions t of sequence s = seq[b] (s = b if seq is NULL) with
  *                max(0, len - window) <= t < len (0 <= t < len if window is 0)
- *                on a page of the pool
+ *                on a page of the pool (and t < 2^31 - 1024)
  *   score[t]   = scale * sum_d q[b][h][d] * K[t][h / (q_heads / heads)][d]
  *   out[b][h]  = sum_t softmax(score)[t] * V[t][h / (q_heads / heads)]
  *   lse[b][h]  = log(sum_t exp(score[t]))

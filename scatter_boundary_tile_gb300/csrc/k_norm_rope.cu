@@ -29,16 +29,16 @@ namespace {
 
 constexpr int kThreads = 128;
 // Forward: heads per group, and blocks per SM the registers are held to.  30011
-// fp16 tokens of 32 + 8 + 8 heads of 128 with 4 heads: 113 us at 7 blocks, 117 at 6, 131
-// at 4; with 3 heads 121, with 2 heads 124, with one 167.
+// fp16 tokens of 32 + 8 + 8 heads of 128 with 4 heads: 113 us at 7 blocks, 115 at 6, 129
+// at 4; with 3 heads 120, with 2 heads 122, with one 188.
 constexpr int kFwdHeads = 4, kFwdBlocks = 7;
 // Rows per SM and group of lanes from which a group takes several heads, if not more than a
 // quarter of the places stay empty.  bf16, 32 + 8 + 8 heads: 256 tokens 3.9 us with four
-// heads, 3.0 with one; 512 tokens 4.3 and 4.4; 1024 tokens 5.8 and 7.1.  8 + 1 + 1 heads (four
-// leave 6 of 16 places empty): 1024 tokens 4.2 and 3.0, 8192 tokens 10.6 and 10.4.
+// heads, 3.1 with one; 512 tokens 4.5 and 4.7; 1024 tokens 6.2 and 7.5.  8 + 1 + 1 heads (four
+// leave 6 of 16 places empty): 1024 tokens 4.5 and 3.0, 8192 tokens 12.0 and 11.7.
 constexpr int kManyRows = 10;
-// Gradient: heads per item, stages of the ring.  16384 bf16 tokens of 32 + 8 heads of 128: 84 us
-// with (2, 2); 103 with (1, 2), 121 with (4, 2), 110 with (2, 3).
+// Gradient: heads per item, stages of the ring.  16384 bf16 tokens of 32 + 8 heads of 128: 80 us
+// with (2, 2); 94 with (1, 2), 99 with (4, 2), 114 with (2, 3).
 constexpr int kBwdHeads = 2, kStages = 2;
 constexpr int kMaxScalarPairs = 8;  // pairs per lane of the element path: 512 elements
 
