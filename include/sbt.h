@@ -582,6 +582,121 @@ SBT_API sbt_status sbt_pages_compact(sbt_context* ctx, const sbt_page_map* map, 
                                      int32_t* page_to, int32_t* n_live, void* workspace, size_t workspace_bytes,
                                      void* stream);
 
+/*
+ * Slot maps: what a step's calls read about its new tokens, from the requests'
+ * lengths.  Entry b of the batch (sequence s = seqs[b], or b where seqs is NULL)
+ * brings n = max(n_new[b], 0) tokens; the tokens of all entries follow one
+ * another.  The tokens of entry b stand at positions first .. first + n - 1 of
+ * its sequence, with first = start[b] or, where start is NULL, lens[s] - n (they
+ * are the last of what the sequence holds, as after sbt_pages_reserve).
+ *
+ *   cu[b]         tokens before entry b, cu[batch] all; at most capacity
+ *   seq[t]        the token's sequence
+ *   positions[t]  its position
+ *   slots[t]      page * page_size + slot of its position in the pool
+ *   last[b]       the entry's last token
+ *
+ * for t < capacity, b < batch; outputs that are NULL are left out.  -1 stands in
+ * seq, positions and slots of the places past the last token (padding, as every
+ * call here reads it) and of tokens whose sequence is outside [0, n_seq); in
+ * positions and slots where the position is negative or at 2^31 or more; in
+ * slots where the position has no page; in last where the entry has no token or
+ * its last one is past the capacity.  slots needs n_pages * page_size <= 2^31.
+ * map->refs is not needed, map->lens only where start is NULL.
+ */
+SBT_API sbt_status sbt_pages_slots(sbt_context* ctx, const sbt_page_map* map, const int32_t* n_new, int32_t batch,
+                                   const int32_t* seqs, const int32_t* start, int32_t capacity, int32_t* cu,
+                                   int32_t* seq, int32_t* positions, int32_t* slots, int32_t* last, void* stream);
+
+/*
+ * Trees of drafted tokens: entry b's tokens are the rows cu[b] .. cu[b+1] - 1
+ * (cu ascending), parents[row] is the number within the entry of the token that
+ * the row's token continues, an earlier one; any other value (such as -1) makes
+ * it continue the sequence itself.
+ *
+ *   mask[row * ld_mask + w], bit j: token 32 w + j of the entry is the row's token
+ *                 or one of its ancestors (w < ld_mask; later tokens have no bit)
+ *   turned[row]   positions[row] less what siblings count twice: the position of
+ *                 the entry's first token plus the token's depth in its tree, by
+ *                 which its query and key are turned; -1 where positions[row] < 0
+ *
+ * for row < rows.  mask or turned may be NULL; positions is read for turned only.
+ * Rows of no entry get no bits and -1.
+ */
+SBT_API sbt_status sbt_tree_plan(sbt_context* ctx, const int32_t* parents, const int32_t* cu, int32_t batch,
+                                 int32_t rows, const int32_t* positions, int32_t* turned, int32_t* mask,
+                                 int64_t ld_mask, void* stream);
+
+/*
+ * Root-mean-square norm of rows with the residual's addition:
+ *
+ *   h = x + r (x where r is NULL),   y = h * weight / sqrt(mean(h^2) + eps)
+ *
+ * per row of `cols` elements, in fp32 (weight NULL: 1); h_out and y get h and y,
+ * each rounded once, and codes (where given) y in 8 bits with a scale per block
+ * of columns, which is what sbt_gemm_block_scaled reads as A and a_scale with
+ * K_s = cols / block:
+ *
+ *   scales[row][j] = 2^e, the least power of two (2^-124 at least; 1 for a block of
+ *                    zeros) with which no |y| of columns j*block .. (j+1)*block - 1
+ *                    passes largest * 2^e, largest = 448 (E4M3) or 57344 (E5M2), as E8M0
+ *   codes[row][c]  = y / 2^e to nearest even; a block that holds an infinity or NaN
+ *                    gets the scale NaN (0xFF) and NaN codes
+ *
+ * h_out, y and codes may be NULL, but not both y and codes.  h_out or y (not
+ * both) may be x or r itself (same stride).  Strides in elements, at least cols
+ * for what is written; 1 <= cols <= 2^24, rows < 2^31.
+ */
+typedef struct {
+    void* codes;         /* [rows][ld] bytes, ld >= cols */
+    int64_t ld;
+    uint8_t* scales;     /* [rows][ld_scale] bytes, ld_scale >= cols / block */
+    int64_t ld_scale;
+    int32_t format;      /* SBT_FMT_E4M3 or SBT_FMT_E5M2 */
+    int32_t block;       /* 16, 32, 64 or 128; divides cols */
+} sbt_code_rows;
+SBT_API sbt_status sbt_add_rms_norm(sbt_context* ctx, sbt_dtype dtype, const void* x, int64_t ld_x, const void* r,
+                                    int64_t ld_r, int64_t rows, int32_t cols, const void* weight, float eps,
+                                    void* h_out, int64_t ld_h, void* y, int64_t ld_y, const sbt_code_rows* codes,
+                                    void* stream);
+
+/*
+ * Gradient of sbt_add_rms_norm at h (its h_out, or x where there is no r): with
+ * gy the gradient of y and gh that of h_out (NULL: zero), dx gets the gradient
+ * of h, which is that of x and of r, in `dtype`, and dweight (fp32 [cols],
+ * required exactly where weight is given) the weight's, summed over the rows in
+ * fp32 in an order that is fixed on one device.  dx may be gy, gh or h (same
+ * stride).  workspace as elsewhere, of
+ * sbt_add_rms_norm_backward_workspace_size() bytes.
+ */
+SBT_API sbt_status sbt_add_rms_norm_backward_workspace_size(sbt_context* ctx, int64_t rows, int32_t cols,
+                                                            size_t* bytes);
+SBT_API sbt_status sbt_add_rms_norm_backward(sbt_context* ctx, sbt_dtype dtype, const void* gy, int64_t ld_gy,
+                                             const void* gh, int64_t ld_gh, const void* h, int64_t ld_h, int64_t rows,
+                                             int32_t cols, const void* weight, float eps, void* dx, int64_t ld_dx,
+                                             float* dweight, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A few rows times a matrix of 4-bit weights with group scales, the B operand of
+ * sbt_gemm_block_scaled as it stands there (E2M1 codes, K x N, two columns a byte,
+ * ldb even; scales K_s x N in E8M0 or E4M3, one per K / K_s weights of a column):
+ *
+ *   y[t][n] = alpha * sum_k x[t][k] * B[k][n] * b_scale[k / (K / K_s)][n]
+ *
+ * for t < tokens, n < N.  dtype: of x; y_dtype: of y, SBT_F32, SBT_BF16 or
+ * SBT_F16.  K_s divides K and K / K_s is a multiple of 16; any number of tokens
+ * (the weights are read once per 16 of them).  Sums are fp32, in an order that is
+ * fixed on one device; a row of x enters the products exactly with SBT_F16, and
+ * with SBT_BF16 and SBT_F32 as one and two fp16 numbers scaled by a power of two:
+ * off by at most 2^-39 of its largest finite |x| (and, SBT_F32, 2^-21 of itself).  An
+ * infinity or NaN in x reaches its own row only; a NaN scale (E8M0 0xFF, E4M3
+ * 0x7F and 0xFF) its own column.
+ */
+SBT_API sbt_status sbt_matvec_e2m1(sbt_context* ctx, sbt_dtype dtype, const void* x, int64_t ld_x, int64_t tokens,
+                                   const void* B, int64_t ldb, sbt_lowp_format s_fmt, const void* b_scale,
+                                   int64_t ld_sb, int64_t K_s, float alpha, void* y, int64_t ld_y, sbt_dtype y_dtype,
+                                   int64_t N, int64_t K, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

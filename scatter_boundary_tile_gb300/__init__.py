@@ -9,7 +9,9 @@ Op names match the C ABI in ``include/sbt.h`` without the ``sbt_`` prefix:
 ``tile_load_padded``, ``tile_store_clipped``, ``gather_rows``, ``gather_cols``,
 ``scatter_rows_masked``, ``scatter_add_rows``, ``ragged_tile_load``, ``ragged_tile_store``, ``gemm_bounded`` (plus
 ``gemm_bounded_workspace_size``), ``gemm_bounded_noalloc``, ``gemm_block_scaled`` (plus
-``gemm_block_scaled_workspace_size``).  Arrays are torch tensors on the device
+``gemm_block_scaled_workspace_size``); of the paged cache and the layer around it ``paged_attention``,
+``rope_table``, ``qk_norm_rope``, ``tree_plan``, ``pages_*``, ``add_rms_norm`` and
+``matvec_e2m1``, gradients and workspace sizes beside them.  Arrays are torch tensors on the device
 (only their data pointer is used; shapes and strides are the explicit
 arguments, in elements).
 """
@@ -38,7 +40,8 @@ EXPORTS = ("sbt_create", "sbt_destroy", "sbt_set_path", "sbt_set_wait_limit_ns",
            "sbt_gemm_bounded_noalloc", "sbt_paged_attention_workspace_size", "sbt_paged_attention", "sbt_rope_table",
            "sbt_qk_norm_rope", "sbt_qk_norm_rope_backward_workspace_size", "sbt_qk_norm_rope_backward",
            "sbt_pages_workspace_size", "sbt_pages_copy", "sbt_pages_reserve", "sbt_pages_fork", "sbt_pages_free",
-           "sbt_pages_compact")
+           "sbt_pages_compact", "sbt_pages_slots", "sbt_tree_plan", "sbt_add_rms_norm", "sbt_add_rms_norm_backward_workspace_size",
+           "sbt_add_rms_norm_backward", "sbt_matvec_e2m1")
 LOWP_FORMATS = {"e4m3": 0, "e5m2": 1, "e8m0": 2, "e2m1": 3}  # sbt_lowp_format
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}  # sbt_rope_layout
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}  # sbt_rope_scaling
@@ -76,6 +79,12 @@ class PagePool(ctypes.Structure):
     """``sbt_page_pool`` (arrays of them are made by ``page_pools``)."""
     _fields_ = [("base", ctypes.c_void_p), ("n_planes", ctypes.c_int64), ("plane_stride", ctypes.c_int64),
                 ("page_stride", ctypes.c_int64), ("page_bytes", ctypes.c_int64)]
+
+
+class CodeRows(ctypes.Structure):
+    """``sbt_code_rows``: 8-bit codes and their scales (made by ``code_rows``)."""
+    _fields_ = [("codes", ctypes.c_void_p), ("ld", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("ld_scale", ctypes.c_int64), ("format", ctypes.c_int32), ("block", ctypes.c_int32)]
 
 
 _lib = None
@@ -134,6 +143,12 @@ def load_library(path: str = LIB_PATH):
             "sbt_pages_fork": [p, pmap, pool, i32, p, p, i32, p, sz, p],
             "sbt_pages_free": [p, pmap, p, p, i32, p],
             "sbt_pages_compact": [p, pmap, pool, i32, p, i64, p, p, p, p, sz, p],
+            "sbt_pages_slots": [p, pmap, p, i32, p, p, i32, p, p, p, p, p, p],
+            "sbt_tree_plan": [p, p, p, i32, i32, p, p, p, i64, p],
+            "sbt_add_rms_norm": [p, ci, p, i64, p, i64, i64, i32, p, f32, p, i64, p, i64, pp(CodeRows), p],
+            "sbt_add_rms_norm_backward_workspace_size": [p, i64, i32, pp(sz)],
+            "sbt_add_rms_norm_backward": [p, ci, p, i64, p, i64, p, i64, i64, i32, p, f32, p, i64, p, p, sz, p],
+            "sbt_matvec_e2m1": [p, ci, p, i64, i64, p, i64, ci, p, i64, i64, f32, p, i64, ci, i64, i64, p],
         })
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -485,3 +500,58 @@ def pages_compact(ctx, map, pools, table_out, ld_out, refs_out, page_to, n_live,
     _check(load_library().sbt_pages_compact(ctx.handle, _ref(map), pools, len(pools), _ptr(table_out), ld_out,
                                             _ptr(refs_out), _ptr(page_to), _ptr(n_live), _ptr(workspace),
                                             workspace_bytes, _stream(stream)))
+
+
+def pages_slots(ctx, map, n_new, batch, capacity, seqs=None, start=None, cu=None, seq=None, positions=None, slots=None,
+                last=None, stream=None):
+    """sbt_pages_slots: prefix sums of n_new, and each new token's sequence, position and slot; -1 pads to capacity."""
+    _check(load_library().sbt_pages_slots(ctx.handle, _ref(map), _ptr(n_new), batch, _ptr(seqs), _ptr(start), capacity,
+                                          _ptr(cu), _ptr(seq), _ptr(positions), _ptr(slots), _ptr(last),
+                                          _stream(stream)))
+
+
+def tree_plan(ctx, parents, cu, batch, rows, mask=None, ld_mask=0, positions=None, turned=None, stream=None):
+    """sbt_tree_plan: ancestor bits (int32 [rows][ld_mask]) and rotation positions of trees of drafted tokens."""
+    _check(load_library().sbt_tree_plan(ctx.handle, _ptr(parents), _ptr(cu), batch, rows, _ptr(positions),
+                                        _ptr(turned), _ptr(mask), ld_mask, _stream(stream)))
+
+
+# --------------------------------------------------------------------------- around the attention
+
+def code_rows(codes, ld, scales, ld_scale, fmt="e4m3", block=32) -> CodeRows:
+    """sbt_code_rows: 8-bit codes [rows][ld] with an E8M0 scale per `block` columns [rows][ld_scale]."""
+    c = CodeRows(_ptr(codes), ld, _ptr(scales), ld_scale, LOWP_FORMATS[fmt] if isinstance(fmt, str) else int(fmt), block)
+    c.tensors = (codes, scales)
+    return c
+
+
+def add_rms_norm(ctx, x, ld_x, rows, cols, weight=None, eps=1e-6, r=None, ld_r=0, h_out=None, ld_h=0, y=None, ld_y=0,
+                 codes=None, dtype=None, stream=None):
+    """sbt_add_rms_norm: h = x + r and its RMS norm, as numbers (y) and as 8-bit codes with block scales (codes)."""
+    code = _dtype_code(x, dtype)
+    _check(load_library().sbt_add_rms_norm(ctx.handle, code, _ptr(x), ld_x, _ptr(r), ld_r, rows, cols, _ptr(weight),
+                                           eps, _ptr(h_out), ld_h, _ptr(y), ld_y, _ref(codes), _stream(stream)))
+
+
+def add_rms_norm_backward_workspace_size(ctx, rows, cols) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().sbt_add_rms_norm_backward_workspace_size(ctx.handle, rows, cols, ctypes.byref(n)))
+    return int(n.value)
+
+
+def add_rms_norm_backward(ctx, gy, ld_gy, h, ld_h, rows, cols, dx, ld_dx, gh=None, ld_gh=0, weight=None, eps=1e-6,
+                          dweight=None, workspace=None, workspace_bytes=0, dtype=None, stream=None):
+    """sbt_add_rms_norm_backward: gradient of x (and of r) from those of y and h_out, and, fp32, the weight's."""
+    code = _dtype_code(gy, dtype)
+    _check(load_library().sbt_add_rms_norm_backward(ctx.handle, code, _ptr(gy), ld_gy, _ptr(gh), ld_gh, _ptr(h), ld_h,
+                                                    rows, cols, _ptr(weight), eps, _ptr(dx), ld_dx, _ptr(dweight),
+                                                    _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def matvec_e2m1(ctx, x, ld_x, tokens, B, ldb, b_scale, ld_sb, K_s, y, ld_y, N, K, s_fmt="e8m0", alpha=1.0, dtype=None,
+                y_dtype=None, stream=None):
+    """sbt_matvec_e2m1: y = alpha * x (B .* b_scale) for a few tokens; B and b_scale as gemm_block_scaled takes them."""
+    code, y_code = _dtype_code(x, dtype), _dtype_code(y, y_dtype)
+    s = LOWP_FORMATS[s_fmt] if isinstance(s_fmt, str) else int(s_fmt)
+    _check(load_library().sbt_matvec_e2m1(ctx.handle, code, _ptr(x), ld_x, tokens, _ptr(B), ldb, s, _ptr(b_scale),
+                                          ld_sb, K_s, alpha, _ptr(y), ld_y, y_code, N, K, _stream(stream)))

@@ -1,25 +1,10 @@
 // C ABI of the paged cache's operators: argument validation and dispatch.
 // Every check here runs before any launch; a failing call launches nothing.
-#include "sbt_internal.cuh"
+#include "sbt_checks.cuh"
 
 namespace {
 
-// Messages are put together only where a check fails.
-std::string say(const char* what, const char* text) { return std::string(what) + text; }
-
-sbt_status check_dtype(sbt_dtype dtype, const char* what) {
-    const int es = sbt_dtype_size(dtype);
-    if (es != 2 && es != 4) return sbt_fail(SBT_ERR_UNSUPPORTED, say(what, ": unsupported dtype"));
-    return SBT_OK;
-}
-
-sbt_status check_workspace(const void* ws, size_t bytes, size_t need, const char* what) {
-    if (!ws || bytes < need)
-        return sbt_fail(SBT_ERR_ALIGNMENT, say(what, ": workspace smaller than its size query"));
-    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
-        return sbt_fail(SBT_ERR_ALIGNMENT, say(what, ": workspace must be 256-byte aligned"));
-    return SBT_OK;
-}
+using namespace sbt_checks;
 
 sbt_status check_map(const sbt_page_map* m, bool lens, bool refs, const char* what) {
     SBT_REQUIRE(m, say(what, ": map is NULL"));
@@ -97,12 +82,6 @@ sbt_status check_pools(const sbt_page_pool* pools, int32_t n, int64_t n_pages, c
 }
 
 }  // namespace
-
-#define SBT_TRY(call)                   \
-    do {                                \
-        const sbt_status st_ = (call);  \
-        if (st_) return st_;            \
-    } while (0)
 
 extern "C" {
 
@@ -352,6 +331,49 @@ sbt_status sbt_pages_compact(sbt_context* ctx, const sbt_page_map* map, const sb
     SBT_TRY(sbt_use_device(ctx));
     return sbt_launch_pages_compact(ctx, map, pools, n_pools, table_out, ld_out, refs_out, page_to, n_live, workspace,
                                     (cudaStream_t)stream);
+}
+
+sbt_status sbt_pages_slots(sbt_context* ctx, const sbt_page_map* map, const int32_t* n_new, int32_t batch,
+                           const int32_t* seqs, const int32_t* start, int32_t capacity, int32_t* cu, int32_t* seq,
+                           int32_t* positions, int32_t* slots, int32_t* last, void* stream) {
+    const char* const w = "pages_slots";
+    SBT_REQUIRE(ctx, "ctx is NULL");
+    SBT_TRY(check_map(map, !start, false, w));
+    SBT_REQUIRE(batch >= 0 && capacity >= 0, "pages_slots: negative batch or capacity");
+    SBT_REQUIRE(batch == 0 || n_new, "pages_slots: n_new is NULL");
+    SBT_REQUIRE(!slots || map->n_pages * map->page_size <= (1ll << 31),
+                "pages_slots: slots needs n_pages * page_size <= 2^31");
+    SBT_REQUIRE_ALIGNED(n_new, 4, "pages_slots: n_new is not 4-byte aligned");
+    SBT_REQUIRE_ALIGNED(seqs, 4, "pages_slots: seqs is not 4-byte aligned");
+    SBT_REQUIRE_ALIGNED(start, 4, "pages_slots: start is not 4-byte aligned");
+    SBT_REQUIRE_ALIGNED(cu, 4, "pages_slots: cu is not 4-byte aligned");
+    SBT_REQUIRE_ALIGNED(seq, 4, "pages_slots: seq is not 4-byte aligned");
+    SBT_REQUIRE_ALIGNED(positions, 4, "pages_slots: positions is not 4-byte aligned");
+    SBT_REQUIRE_ALIGNED(slots, 4, "pages_slots: slots is not 4-byte aligned");
+    SBT_REQUIRE_ALIGNED(last, 4, "pages_slots: last is not 4-byte aligned");
+    const bool tokens = (seq || positions || slots) && capacity > 0;
+    if (!tokens && !cu && (!last || batch == 0)) return SBT_OK;
+    SBT_TRY(sbt_use_device(ctx));
+    return sbt_launch_pages_slots(ctx, map, n_new, batch, seqs, start, capacity, cu, seq, positions, slots, last,
+                                  (cudaStream_t)stream);
+}
+
+sbt_status sbt_tree_plan(sbt_context* ctx, const int32_t* parents, const int32_t* cu, int32_t batch, int32_t rows,
+                         const int32_t* positions, int32_t* turned, int32_t* mask, int64_t ld_mask, void* stream) {
+    SBT_REQUIRE(ctx, "ctx is NULL");
+    SBT_REQUIRE(batch >= 0 && rows >= 0, "tree_plan: negative batch or rows");
+    SBT_REQUIRE(ld_mask >= 0 && ld_mask <= 1 << 20, "tree_plan: ld_mask must be in [0, 2^20]");
+    SBT_REQUIRE(!mask || ld_mask >= 1, "tree_plan: ld_mask must be at least 1");
+    if (rows == 0 || (!mask && !turned)) return SBT_OK;
+    SBT_REQUIRE(batch == 0 || (parents && cu), "tree_plan: parents or cu is NULL");
+    SBT_REQUIRE(!turned || batch == 0 || positions, "tree_plan: positions is NULL");
+    SBT_REQUIRE_ALIGNED(parents, 4, "tree_plan: parents is not 4-byte aligned");
+    SBT_REQUIRE_ALIGNED(cu, 4, "tree_plan: cu is not 4-byte aligned");
+    SBT_REQUIRE_ALIGNED(positions, 4, "tree_plan: positions is not 4-byte aligned");
+    SBT_REQUIRE_ALIGNED(turned, 4, "tree_plan: turned is not 4-byte aligned");
+    SBT_REQUIRE_ALIGNED(mask, 4, "tree_plan: mask is not 4-byte aligned");
+    SBT_TRY(sbt_use_device(ctx));
+    return sbt_launch_tree_plan(ctx, parents, cu, batch, rows, positions, turned, mask, ld_mask, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -211,6 +211,40 @@ sbt_status sbt_launch_pages_compact(sbt_context* ctx, const sbt_page_map* map, c
                                     int32_t n_pools, int32_t* table_out, int64_t ld_out, int32_t* refs_out,
                                     int32_t* page_to, int32_t* n_live, void* workspace, cudaStream_t stream);
 
+sbt_status sbt_launch_pages_slots(sbt_context* ctx, const sbt_page_map* map, const int32_t* n_new, int32_t batch,
+                                  const int32_t* seqs, const int32_t* start, int32_t capacity, int32_t* cu,
+                                  int32_t* seq, int32_t* positions, int32_t* slots, int32_t* last,
+                                  cudaStream_t stream);
+sbt_status sbt_launch_tree_plan(sbt_context* ctx, const int32_t* parents, const int32_t* cu, int32_t batch,
+                                int32_t rows, const int32_t* positions, int32_t* turned, int32_t* mask,
+                                int64_t ld_mask, cudaStream_t stream);
+sbt_status sbt_launch_tree_attention(sbt_context* ctx, sbt_dtype dtype, const SbtHeadRows& q, int32_t rows,
+                                     const int32_t* cu, int32_t batch, int32_t max_new, int32_t q_heads,
+                                     const sbt_kv_cache* cache, const sbt_page_map* map, const int32_t* seq,
+                                     float scale, const int32_t* mask, int64_t ld_mask, const SbtHeadRows& out,
+                                     float* lse, void* workspace, cudaStream_t stream);
+size_t sbt_tree_attention_workspace_bytes(const sbt_context* ctx, int32_t max_new, int32_t q_heads, int32_t kv_heads,
+                                          int32_t head_dim);
+
+// Operators of a decoding layer around the attention (k_add_norm.cu, k_matvec.cu).
+// Rows of a matrix, element stride.
+struct SbtRows {
+    const void* p;
+    int64_t ld;
+};
+sbt_status sbt_launch_add_norm(sbt_context* ctx, sbt_dtype dtype, const SbtRows& x, const SbtRows& r, int64_t rows,
+                               int32_t cols, const void* w, float eps, const SbtRows& h, const SbtRows& y,
+                               const sbt_code_rows* codes, cudaStream_t stream);
+size_t sbt_add_norm_bwd_bytes(const sbt_context* ctx, int64_t rows, int32_t cols);
+sbt_status sbt_launch_add_norm_bwd(sbt_context* ctx, sbt_dtype dtype, const SbtRows& gy, const SbtRows& gh,
+                                   const SbtRows& h, int64_t rows, int32_t cols, const void* w, float eps,
+                                   const SbtRows& dx, float* dw, void* workspace, cudaStream_t stream);
+
+sbt_status sbt_launch_matvec(sbt_context* ctx, sbt_dtype dtype, const SbtRows& x, int64_t tokens, const void* B,
+                             int64_t ldb, bool e4m3_scales, const void* scales, int64_t ld_sb, int64_t K_s,
+                             float alpha, const SbtRows& y, sbt_dtype y_dtype, int64_t N, int64_t K,
+                             cudaStream_t stream);
+
 // Blocks of a kernel with dynamic shared memory that the device holds at once.
 // Asked of the runtime on a kernel's first use on a device, remembered after.
 template <auto KERN>
