@@ -81,8 +81,8 @@ SBT_API sbt_status sbt_set_path(sbt_context* ctx, sbt_path path);
 /* Limit of every bounded device-side wait, in nanoseconds (default 2e9). */
 SBT_API sbt_status sbt_set_wait_limit_ns(sbt_context* ctx, uint64_t ns);
 /* Test hook for the bounded device waits.  SBT_TEST_WITHHOLD_LOAD makes the
- * next GEMM (bf16 or block-scaled tensor path) and bulk row launches on this
- * context skip their first copy, so
+ * next GEMM (bf16 or block-scaled tensor path), bulk row and tree attention
+ * launches on this context skip their first copy (its signal), so
  * a consumer's bounded wait runs out (no fault, no hang): the kernel sets the
  * status flag, drains and returns, and sbt_check_status() reports
  * SBT_ERR_DEVICE_TIMEOUT.  Stays set until reset with SBT_TEST_NONE. */
@@ -626,6 +626,39 @@ SBT_API sbt_status sbt_pages_slots(sbt_context* ctx, const sbt_page_map* map, co
 SBT_API sbt_status sbt_tree_plan(sbt_context* ctx, const int32_t* parents, const int32_t* cu, int32_t batch,
                                  int32_t rows, const int32_t* positions, int32_t* turned, int32_t* mask,
                                  int64_t ld_mask, void* stream);
+
+/*
+ * Attention of several new tokens per sequence over the cache, which holds them
+ * already: a prompt's next piece, or a tree of drafted tokens.
+ *
+ * Entry b's tokens are the rows cu[b] .. cu[b+1] - 1 of q and out, n of them; with
+ * L the length of sequence s = seq[b] (b where seq is NULL), token j of the entry
+ * stands at position L - n + j.  Token i sees the positions t of its sequence on
+ * a page of the pool with
+ *   0 <= t < L - n                 (what was held before), or
+ *   t = L - n + j, t >= 0, j < n   and bit j of its mask row set (j <= i where mask is NULL).
+ * Scores, out and lse are those of sbt_paged_attention over these positions, in
+ * the same arithmetic; lse is dense fp32 [rows][q_heads] or NULL.  A token that
+ * sees nothing gets zeros and minus infinity.  Contents at positions that no
+ * token of the entry sees are never read.  An entry with more than max_new
+ * tokens, or with rows outside [0, rows), is left out; rows of no entry and of
+ * entries left out are not written.
+ *
+ * dtype: SBT_BF16 or SBT_F16.  mask: int32 [rows][ld_mask], bit 32 w + j as
+ * sbt_tree_plan writes it (tokens from 32 ld_mask on are seen by none).
+ * 1 <= head_dim <= 256, cache->heads divides q_heads, max_new * (q_heads /
+ * cache->heads) < 2^24.  workspace as for sbt_paged_attention; its size depends
+ * on neither the batch nor the lengths.
+ */
+SBT_API sbt_status sbt_paged_tree_attention_workspace_size(sbt_context* ctx, int32_t max_new, int32_t q_heads,
+                                                           int32_t kv_heads, int32_t head_dim, size_t* bytes);
+SBT_API sbt_status sbt_paged_tree_attention(sbt_context* ctx, sbt_dtype dtype, const void* q, int64_t ld_q,
+                                            int64_t ld_qh, int32_t rows, const int32_t* cu, int32_t batch,
+                                            int32_t max_new, int32_t q_heads, const sbt_kv_cache* cache,
+                                            const sbt_page_map* map, const int32_t* seq, float scale,
+                                            const int32_t* mask, int64_t ld_mask, void* out, int64_t ld_out,
+                                            int64_t ld_oh, float* lse, void* workspace, size_t workspace_bytes,
+                                            void* stream);
 
 /*
  * Root-mean-square norm of rows with the residual's addition:

@@ -10,7 +10,7 @@ Op names match the C ABI in ``include/sbt.h`` without the ``sbt_`` prefix:
 ``scatter_rows_masked``, ``scatter_add_rows``, ``ragged_tile_load``, ``ragged_tile_store``, ``gemm_bounded`` (plus
 ``gemm_bounded_workspace_size``), ``gemm_bounded_noalloc``, ``gemm_block_scaled`` (plus
 ``gemm_block_scaled_workspace_size``); of the paged cache and the layer around it ``paged_attention``,
-``rope_table``, ``qk_norm_rope``, ``tree_plan``, ``pages_*``, ``add_rms_norm`` and
+``paged_tree_attention``, ``rope_table``, ``qk_norm_rope``, ``tree_plan``, ``pages_*``, ``add_rms_norm`` and
 ``matvec_e2m1``, gradients and workspace sizes beside them.  Arrays are torch tensors on the device
 (only their data pointer is used; shapes and strides are the explicit
 arguments, in elements).
@@ -40,7 +40,8 @@ EXPORTS = ("sbt_create", "sbt_destroy", "sbt_set_path", "sbt_set_wait_limit_ns",
            "sbt_gemm_bounded_noalloc", "sbt_paged_attention_workspace_size", "sbt_paged_attention", "sbt_rope_table",
            "sbt_qk_norm_rope", "sbt_qk_norm_rope_backward_workspace_size", "sbt_qk_norm_rope_backward",
            "sbt_pages_workspace_size", "sbt_pages_copy", "sbt_pages_reserve", "sbt_pages_fork", "sbt_pages_free",
-           "sbt_pages_compact", "sbt_pages_slots", "sbt_tree_plan", "sbt_add_rms_norm", "sbt_add_rms_norm_backward_workspace_size",
+           "sbt_pages_compact", "sbt_pages_slots", "sbt_tree_plan", "sbt_paged_tree_attention_workspace_size",
+           "sbt_paged_tree_attention", "sbt_add_rms_norm", "sbt_add_rms_norm_backward_workspace_size",
            "sbt_add_rms_norm_backward", "sbt_matvec_e2m1")
 LOWP_FORMATS = {"e4m3": 0, "e5m2": 1, "e8m0": 2, "e2m1": 3}  # sbt_lowp_format
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}  # sbt_rope_layout
@@ -145,6 +146,9 @@ def load_library(path: str = LIB_PATH):
             "sbt_pages_compact": [p, pmap, pool, i32, p, i64, p, p, p, p, sz, p],
             "sbt_pages_slots": [p, pmap, p, i32, p, p, i32, p, p, p, p, p, p],
             "sbt_tree_plan": [p, p, p, i32, i32, p, p, p, i64, p],
+            "sbt_paged_tree_attention_workspace_size": [p, i32, i32, i32, i32, pp(sz)],
+            "sbt_paged_tree_attention": [p, ci, *rows, i32, p, i32, i32, i32, cache, pmap, p, f32, p, i64, *rows, p, p,
+                                         sz, p],
             "sbt_add_rms_norm": [p, ci, p, i64, p, i64, i64, i32, p, f32, p, i64, p, i64, pp(CodeRows), p],
             "sbt_add_rms_norm_backward_workspace_size": [p, i64, i32, pp(sz)],
             "sbt_add_rms_norm_backward": [p, ci, p, i64, p, i64, p, i64, i64, i32, p, f32, p, i64, p, p, sz, p],
@@ -514,6 +518,24 @@ def tree_plan(ctx, parents, cu, batch, rows, mask=None, ld_mask=0, positions=Non
     """sbt_tree_plan: ancestor bits (int32 [rows][ld_mask]) and rotation positions of trees of drafted tokens."""
     _check(load_library().sbt_tree_plan(ctx.handle, _ptr(parents), _ptr(cu), batch, rows, _ptr(positions),
                                         _ptr(turned), _ptr(mask), ld_mask, _stream(stream)))
+
+
+def paged_tree_attention_workspace_size(ctx, max_new, q_heads, kv_heads, head_dim) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().sbt_paged_tree_attention_workspace_size(ctx.handle, max_new, q_heads, kv_heads, head_dim,
+                                                                  ctypes.byref(n)))
+    return int(n.value)
+
+
+def paged_tree_attention(ctx, q, ld_q, ld_qh, rows, cu, batch, max_new, q_heads, cache, map, scale, out, ld_out, ld_oh,
+                         mask=None, ld_mask=0, lse=None, seq=None, workspace=None, workspace_bytes=0, dtype=None,
+                         stream=None):
+    """sbt_paged_tree_attention: rows cu[b] .. cu[b+1] - 1 are the last tokens of entry b's sequence (a tree or a chain)."""
+    code = _dtype_code(q, dtype)
+    _check(load_library().sbt_paged_tree_attention(ctx.handle, code, _ptr(q), ld_q, ld_qh, rows, _ptr(cu), batch,
+                                                   max_new, q_heads, _ref(cache), _ref(map), _ptr(seq), scale,
+                                                   _ptr(mask), ld_mask, _ptr(out), ld_out, ld_oh, _ptr(lse),
+                                                   _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 # --------------------------------------------------------------------------- around the attention

@@ -66,6 +66,15 @@ sbt_status check_rope(const sbt_rope* r, int32_t head_dim, const char* what) {
     return SBT_OK;
 }
 
+// Extents of attention of several new tokens: a block's rows are counted in 24 bits.
+sbt_status check_tree(int32_t max_new, int32_t q_heads, int32_t kv_heads, int32_t head_dim, const char* what) {
+    SBT_REQUIRE(kv_heads >= 1 && q_heads >= 1 && q_heads % kv_heads == 0, say(what, ": kv_heads must divide q_heads"));
+    SBT_REQUIRE(head_dim >= 1 && head_dim <= 256, say(what, ": head_dim must be in [1, 256]"));
+    SBT_REQUIRE(max_new >= 1 && (int64_t)max_new * (q_heads / kv_heads) < 1 << 24,
+                say(what, ": max_new must be positive and max_new * (q_heads / kv_heads) below 2^24"));
+    return SBT_OK;
+}
+
 sbt_status check_pools(const sbt_page_pool* pools, int32_t n, int64_t n_pages, const char* what) {
     SBT_REQUIRE(n >= 1 && n <= SBT_MAX_PAGE_POOLS && pools, say(what, ": between 1 and SBT_MAX_PAGE_POOLS pools"));
     for (int32_t i = 0; i < n; ++i) {
@@ -374,6 +383,46 @@ sbt_status sbt_tree_plan(sbt_context* ctx, const int32_t* parents, const int32_t
     SBT_REQUIRE_ALIGNED(mask, 4, "tree_plan: mask is not 4-byte aligned");
     SBT_TRY(sbt_use_device(ctx));
     return sbt_launch_tree_plan(ctx, parents, cu, batch, rows, positions, turned, mask, ld_mask, (cudaStream_t)stream);
+}
+
+sbt_status sbt_paged_tree_attention_workspace_size(sbt_context* ctx, int32_t max_new, int32_t q_heads,
+                                                   int32_t kv_heads, int32_t head_dim, size_t* bytes) {
+    const char* const w = "paged_tree_attention_workspace_size";
+    SBT_REQUIRE(ctx && bytes, "paged_tree_attention_workspace_size: NULL argument");
+    SBT_TRY(check_tree(max_new, q_heads, kv_heads, head_dim, w));
+    *bytes = sbt_tree_attention_workspace_bytes(ctx, max_new, q_heads, kv_heads, head_dim);
+    return SBT_OK;
+}
+
+sbt_status sbt_paged_tree_attention(sbt_context* ctx, sbt_dtype dtype, const void* q, int64_t ld_q, int64_t ld_qh,
+                                    int32_t rows, const int32_t* cu, int32_t batch, int32_t max_new, int32_t q_heads,
+                                    const sbt_kv_cache* cache, const sbt_page_map* map, const int32_t* seq,
+                                    float scale, const int32_t* mask, int64_t ld_mask, void* out, int64_t ld_out,
+                                    int64_t ld_oh, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* const w = "paged_tree_attention";
+    SBT_REQUIRE(ctx, "ctx is NULL");
+    if (dtype != SBT_BF16 && dtype != SBT_F16)
+        return sbt_fail(SBT_ERR_UNSUPPORTED, "paged_tree_attention: dtype must be SBT_BF16 or SBT_F16");
+    SBT_TRY(check_map(map, true, false, w));
+    SBT_TRY(check_cache(cache, map, 2, w));
+    SBT_REQUIRE(rows >= 0 && batch >= 0, "paged_tree_attention: negative rows or batch");
+    SBT_TRY(check_tree(max_new, q_heads, cache->heads, cache->head_dim, w));
+    SBT_REQUIRE((int64_t)batch * cache->heads < (1ll << 31), "paged_tree_attention: batch too large");
+    SBT_REQUIRE(!mask || ld_mask >= 1, "paged_tree_attention: ld_mask must be at least 1");
+    if (rows == 0 || batch == 0) return SBT_OK;
+    const SbtHeadRows rq = {q, ld_q, ld_qh}, ro = {out, ld_out, ld_oh};
+    SBT_TRY(check_rows(rq, rows, q_heads, cache->head_dim, 2, false, "q", w));
+    SBT_TRY(check_rows(ro, rows, q_heads, cache->head_dim, 2, true, "out", w));
+    SBT_REQUIRE(cu, "paged_tree_attention: cu is NULL");
+    SBT_REQUIRE_ALIGNED(cu, 4, "paged_tree_attention: cu is not 4-byte aligned");
+    SBT_REQUIRE_ALIGNED(seq, 4, "paged_tree_attention: seq is not 4-byte aligned");
+    SBT_REQUIRE_ALIGNED(mask, 4, "paged_tree_attention: mask is not 4-byte aligned");
+    SBT_REQUIRE_ALIGNED(lse, 4, "paged_tree_attention: lse is not 4-byte aligned");
+    SBT_TRY(check_workspace(workspace, workspace_bytes,
+                            sbt_tree_attention_workspace_bytes(ctx, max_new, q_heads, cache->heads, cache->head_dim), w));
+    SBT_TRY(sbt_use_device(ctx));
+    return sbt_launch_tree_attention(ctx, dtype, rq, rows, cu, batch, max_new, q_heads, cache, map, seq, scale, mask,
+                                     ld_mask, ro, lse, workspace, (cudaStream_t)stream);
 }
 
 }  // extern "C"

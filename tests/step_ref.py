@@ -125,3 +125,75 @@ def tree_plan(parents, cu, rows, words, positions):
             if positions[row] >= 0:
                 turned[row] = positions[row] - i + depth
     return mask, turned
+
+
+# ---------------------------------------------------------------------------- attention of several new tokens
+
+def visible(i, n, length, mask_row):
+    """bool [length]: what token i of n sees of the positions; mask_row: its int32 words, or None for a chain."""
+    t = np.arange(length)
+    j = t - (length - n)
+    if mask_row is None:
+        return j <= i
+    words = np.asarray(mask_row).view(np.uint32)
+    bit = np.zeros(length, bool)
+    inside = (j >= 0) & (j < min(n, 32 * len(words)))
+    bit[inside] = words[j[inside] // 32] >> (j[inside] % 32).astype(np.uint32) & 1
+    return (j < 0) | bit
+
+
+def tree_attention(q, k, v, table, lens, page_size, scale, cu, max_new, mask=None, seq=None):
+    """q [rows][Hq][D]; k, v [n_pages][page_size][H][D], float64.
+
+    Returns out, lse, the rows that are written, and for the error bound what cache_ref.attention returns."""
+    rows, Hq, D = q.shape
+    n_pages, _, H, _ = k.shape
+    out, lse = np.zeros((rows, Hq, D)), np.full((rows, Hq), -np.inf)
+    x = dict(absv=np.zeros((rows, Hq, D)), mag=np.zeros((rows, Hq)), count=np.zeros((rows, Hq)), vmax=np.zeros((rows, Hq)))
+    written = np.zeros(rows, bool)
+    for b in range(len(cu) - 1):
+        n = int(cu[b + 1]) - int(cu[b])
+        if n <= 0 or n > max_new or cu[b] < 0 or cu[b + 1] > rows:
+            continue
+        written[cu[b]:cu[b + 1]] = True
+        s = b if seq is None else int(seq[b])
+        if not 0 <= s < len(lens):
+            continue
+        length = min(max(int(lens[s]), 0), table.shape[1] * page_size)
+        t = np.arange(length)
+        page = table[s, t // page_size]
+        held = (page >= 0) & (page < n_pages)
+        kk = np.where(held[:, None, None], k[np.where(held, page, 0), t % page_size], 0)
+        vv = np.where(held[:, None, None], v[np.where(held, page, 0), t % page_size], 0)
+        for i in range(n):
+            row = cu[b] + i
+            sees = held & visible(i, n, length, None if mask is None else mask[row])
+            if not sees.any():
+                continue
+            for h in range(Hq):
+                g = h // (Hq // H)
+                with np.errstate(invalid="ignore", over="ignore"):
+                    score = kk[sees, g] @ q[row, h] * scale
+                    m = score.max()
+                    if m == -np.inf:
+                        continue
+                    e = np.exp(score - m)
+                    out[row, h] = e @ vv[sees, g] / e.sum()
+                    lse[row, h] = m + np.log(e.sum())
+                    x["absv"][row, h] = e @ np.abs(vv[sees, g]) / e.sum()
+                x["mag"][row, h] = (np.abs(kk[sees, g]) @ np.abs(q[row, h])).max() * abs(scale)
+                x["vmax"][row, h] = np.abs(vv[sees, g]).max()
+                x["count"][row, h] = sees.sum()
+    return out, lse, written, x
+
+
+def tree_attention_bounds(ref, kind, D):
+    """As cache_ref.attention_bounds: probabilities of 16 (bf16) or 22 (fp16) bits, fp16 ones in steps of 2^-33 at least."""
+    out, lse, _, x = ref
+    score = (D + 3) * 2.0**-23 * x["mag"]
+    rel = 2 * score + (x["count"] + 64) * 2.0**-23 + {"bf16": 2.0**-16, "f16": 2.0**-21}[kind]
+    o = rel[..., None] * x["absv"] + HALF_ULP[kind] * np.abs(out) * 1.01 + TINY[kind]
+    if kind == "f16":
+        o = o + (x["count"] * 2.0**-34 * x["vmax"])[..., None]
+    s = score + (x["count"] + 64) * 2.0**-23 + 2.0**-20 * (1 + np.where(np.isfinite(lse), np.abs(lse), 0))
+    return o, s

@@ -22,6 +22,7 @@ BACK = [BF16, p(0), 128, p(1), 128, p(2), 128, 5, 128, p(3), 1e-6, p(4), 128, p(
 MATVEC = [BF16, p(0), 256, 3, p(1), 64, E8M0, p(2), 64, 8, 1.0, p(3), 64, F32, 64, 256, None]
 SLOTS = [pmap, p(7), 3, p(8), p(9), 100, p(10), p(11), p(12), p(13), p(14), None]
 PLAN = [p(7), p(8), 3, 50, p(9), p(10), p(11), 2, None]
+TREE = [BF16, p(7), 256, 64, 50, p(8), 3, 16, 4, cache, pmap, p(9), 0.125, p(10), 1, p(11), 256, 64, p(12), *WS, None]
 
 CASES = [  # (call, valid arguments, {index: value}, expected status)
     ("sbt_add_rms_norm", NORM, {}, CUDA),
@@ -139,6 +140,38 @@ CASES = [  # (call, valid arguments, {index: value}, expected status)
     ("sbt_tree_plan", PLAN, {6: None, 7: 0}, CUDA),
     ("sbt_tree_plan", PLAN, {7: (1 << 20) + 1}, BAD),
     *[("sbt_tree_plan", PLAN, {i: p(7 + i, 1)}, ALN) for i in (0, 1, 4, 5, 6)],
+    ("sbt_paged_tree_attention", TREE, {}, CUDA),
+    ("sbt_paged_tree_attention", TREE, {0: F32}, UNS),
+    ("sbt_paged_tree_attention", TREE, {0: F16}, CUDA),
+    ("sbt_paged_tree_attention", TREE, {1: None}, BAD),
+    ("sbt_paged_tree_attention", TREE, {1: p(7, 1)}, ALN),
+    ("sbt_paged_tree_attention", TREE, {2: -1}, BAD),
+    ("sbt_paged_tree_attention", TREE, {4: 0}, OK),
+    ("sbt_paged_tree_attention", TREE, {4: -1}, BAD),
+    ("sbt_paged_tree_attention", TREE, {5: None}, BAD),
+    ("sbt_paged_tree_attention", TREE, {5: p(8, 2)}, ALN),
+    ("sbt_paged_tree_attention", TREE, {6: 0}, OK),
+    ("sbt_paged_tree_attention", TREE, {6: -1}, BAD),
+    ("sbt_paged_tree_attention", TREE, {6: 1 << 30}, BAD),
+    ("sbt_paged_tree_attention", TREE, {7: 0}, BAD),
+    ("sbt_paged_tree_attention", TREE, {7: 1 << 23}, BAD),
+    ("sbt_paged_tree_attention", TREE, {7: (1 << 23) - 1}, CUDA),
+    ("sbt_paged_tree_attention", TREE, {8: 3}, BAD),
+    ("sbt_paged_tree_attention", TREE, {9: None}, BAD),
+    ("sbt_paged_tree_attention", TREE, {9: lambda: cache(head_dim=257, ld_slot=600, ld_head=300)}, BAD),
+    ("sbt_paged_tree_attention", TREE, {9: lambda: cache(k=p(0, 1))}, ALN),
+    ("sbt_paged_tree_attention", TREE, {10: None}, BAD),
+    ("sbt_paged_tree_attention", TREE, {10: lambda: pmap(lens=None)}, BAD),
+    ("sbt_paged_tree_attention", TREE, {11: p(9, 2)}, ALN),
+    ("sbt_paged_tree_attention", TREE, {13: None, 14: 0}, CUDA),
+    ("sbt_paged_tree_attention", TREE, {14: 0}, BAD),
+    ("sbt_paged_tree_attention", TREE, {13: p(10, 1)}, ALN),
+    ("sbt_paged_tree_attention", TREE, {15: None}, BAD),
+    ("sbt_paged_tree_attention", TREE, {17: 63}, BAD),
+    ("sbt_paged_tree_attention", TREE, {18: None}, CUDA),
+    ("sbt_paged_tree_attention", TREE, {18: p(12, 2)}, ALN),
+    ("sbt_paged_tree_attention", TREE, {19: None}, ALN),
+    ("sbt_paged_tree_attention", TREE, {19: p(64, 8)}, ALN),
 ]
 
 

@@ -61,3 +61,23 @@ def test_tree_by_hand():
     mask, turned = ref.tree_plan([-1, 0, -1, 1, 2], [0, 5], 5, 1, np.arange(10, 15))
     assert mask[:, 0].tolist() == [0b1, 0b11, 0b100, 0b1011, 0b10100]
     assert turned.tolist() == [10, 11, 10, 12, 11]
+
+
+def test_tree_attention_against_torch():
+    """A chain is causal attention over a contiguous cache; bits past the words and the entry count for nothing."""
+    rng = np.random.default_rng(0)
+    n, ctx, H, D = 5, 11, 2, 4
+    k, v = (rng.standard_normal((4, 4, H, D)) for _ in "kv")
+    q = rng.standard_normal((n, 4, D))
+    table = np.array([[2, 0, 3, 1]])
+    flat = lambda x: torch.from_numpy(x[table[0]].reshape(16, H, D).copy()).permute(1, 0, 2).repeat_interleave(2, 0)
+    see = torch.ones(n, 16, dtype=torch.bool).tril(ctx)
+    want = torch.nn.functional.scaled_dot_product_attention(torch.from_numpy(q).permute(1, 0, 2), flat(k), flat(v), see,
+                                                            scale=0.3).permute(1, 0, 2).numpy()
+    out, lse, written, x = ref.tree_attention(q, k, v, table, [16], 4, 0.3, [0, n], n)
+    assert np.allclose(out, want, rtol=1e-12) and written.all() and (x["count"][:, 0] == np.arange(12, 17)).all()
+    mask = ((1 << np.arange(1, n + 1)) - 1).astype(np.int32)[:, None]
+    mask[4] |= 0x7000
+    assert np.array_equal(ref.tree_attention(q, k, v, table, [16], 4, 0.3, [0, n], n, mask)[0], out)
+    assert ref.visible(1, 3, 5, np.array([0b101], np.int32)).tolist() == [True, True, True, False, True]
+    assert ref.visible(0, 40, 40, np.array([-1], np.int32)).sum() == 32
