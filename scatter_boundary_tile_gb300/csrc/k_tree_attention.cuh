@@ -1,0 +1,961 @@
+// Attention of several new tokens per sequence over a paged key-value cache: a
+// prompt's next piece or a tree of drafted tokens.
+//
+// For a query row (a token's query head) with scores s_t = scale q . k_t over
+// the positions it sees, one pass over the cache keeps a reference m, the sum
+// l = sum 2^(s'_t - m) and the vector o = sum 2^(s'_t - m) v_t (s' = s log2 e).
+// m is the largest score seen when it was last taken; it is taken again, and l
+// and o rescaled, only when a score passes it by 2^kSlack, so a 2^(s' - m) is at
+// most that and o rarely has to be touched outside the matrix unit.  Two such
+// states over disjoint positions join by the rule of the softmax.
+//
+// The rows of one sequence and key-value head, n tokens times `group` query
+// heads, go through tcgen05 in tiles of 128: S = Q K^T and O += P V with K and V
+// tiles of 64 positions in shared memory (rows of 128 bytes, swizzled: K read
+// K-major, V MN-major), S, P and O in TMEM.  P enters as the sum of two 16-bit
+// numbers (16 significant bits with bf16, 22 with fp16), since one would add to
+// the output's error as much as the output's own rounding; both take the place
+// of S, so the second costs matrix time only.  fp16 ones are 2^kShift p, so that
+// small ones are not lost among the subnormals.
+//
+// Roles.  Three warps copy (cp.async, 16 bytes a lane, from any page order and
+// stride), one thread issues the matrix instructions, and a warp for every 32
+// rows does the softmax, a row a thread.  S is double: while tile k is in the
+// softmax, tile k + 1 is already multiplied.  MT = 1: 128 rows, two blocks an SM
+// (the one's softmax runs under the other's products); MT = 2: 256 rows share a
+// tile of K and V.  More rows go to other blocks, which run at the same time on
+// the same range and find K and V in L2.
+//
+// Split.  All (sequence, key-value head) lines, cut into tiles, lie on one line
+// on which every block gets an even range; lengths are read on the device.  Rows
+// wholly inside a range are written by their block; of a line cut by range
+// borders each block writes its state to the workspace and k_tree_join adds them
+// in the order of the line.
+//
+// A masked position's score is replaced before the softmax, its P is zero.  Its
+// V would still meet that zero: among the new tokens, which one row sees and
+// another does not, infinities and NaN are taken out of the tile and put, after
+// the softmax, on the rows that do see them.
+//
+// Every wait is bounded; one that runs out sets the device status word, and the
+// kernel drains and returns.
+#pragma once
+
+#include "k_paged_attention.cuh"
+#include "sbt_num.cuh"
+
+namespace sbt_tree {
+
+using namespace sbt_ptx;
+using namespace sbt_num;
+using sbt_attn::Line;
+
+constexpr int kTok = 64, kRows = 128, kLoaders = 96;
+constexpr int kLineCost = 3;      // what starting and ending a line costs, in tiles
+constexpr int kBits = 16;         // tiles whose visible positions are remembered
+constexpr int kJoin = 256;
+
+struct TreeDesc {
+    int32_t valid, b, h, plane, first, last, first_slot, pad;
+};
+
+struct TreeAttnParams {
+    const char *q, *k, *v;
+    char* out;
+    float* lse;
+    const int32_t *cu, *table, *lens, *seq;
+    const uint32_t* mask;
+    int64_t ld_q, ld_qh, ld_out, ld_oh;        // elements
+    int64_t ld_page, ld_slot, ld_head;         // elements
+    int64_t ld_table, n_pages, ld_mask;
+    int32_t rows, batch, max_new, q_heads, kv_heads, n_seq, head_dim, max_len;
+    int32_t planes;                            // tiles of MT * 128 rows that an entry may need
+    int32_t ranges;                            // blocks per plane
+    int32_t copy_q, copy_kv, out_vec;          // bytes of one copy into shared memory; out as 16-byte vectors
+    int32_t desc_by_line;                      // descriptors by line (there are no more lines than blocks), else by block
+    sbt_fastdiv group, page_size;
+    float scale;                               // |scale| log2 e
+    int32_t negate;
+    unsigned int* status;
+    uint64_t wait_ns;
+    int32_t withhold;                          // test hook: no block signals its first tile
+    TreeDesc* desc;
+    float2* part_ml;                           // [2 blocks][MT * 128]
+    float* part_o;                             // [2 blocks][MT * 128][DP]
+};
+
+// Entry b's rows of one plane: tokens are the rows q0 .. q0 + n - 1 of q, the last n of len positions.
+struct TreeRow {
+    int32_t b, q0, n, len, seq, tiles;
+    int32_t count;                             // query rows of the plane
+};
+
+__device__ __forceinline__ TreeRow row_of(const TreeAttnParams& p, int32_t b, int32_t plane, int32_t plane_rows) {
+    TreeRow r = {b, 0, 0, 0, -1, 0, 0};
+    const int32_t c0 = sbt_ld(p.cu + b), c1 = sbt_ld(p.cu + b + 1);
+    const int64_t n = (int64_t)c1 - c0;
+    if (c0 < 0 || c1 > p.rows || n <= 0 || n > p.max_new) return r;
+    const int64_t all = n * p.group.d, first = (int64_t)plane * plane_rows;
+    if (first >= all) return r;
+    r.q0 = c0, r.n = (int32_t)n;
+    r.count = (int32_t)min((int64_t)plane_rows, all - first);
+    const int32_t s = p.seq ? sbt_ld(p.seq + b) : b;
+    if (s < 0 || s >= p.n_seq) return r;
+    r.seq = s;
+    r.len = min(max(sbt_ld(p.lens + s), 0), p.max_len);
+    // without a mask no row of the plane sees past its last token
+    const int32_t last = (int32_t)sbt_div(p.group, (uint32_t)(first + r.count - 1));
+    const int32_t hi = p.mask ? r.len : r.len - r.n + last + 1;
+    r.tiles = hi > 0 ? (hi + kTok - 1) / kTok : 0;
+    return r;
+}
+
+// The lines of a range, one after another; every role walks it by itself.
+struct Walk {
+    const TreeAttnParams& p;
+    int32_t plane, plane_rows;
+    TreeRow row;
+    int32_t h, t;          // key-value head; first tile of the segment
+    int64_t u, end;        // its place; the range's end
+
+    // The tiles of the segment at hand.
+    __device__ __forceinline__ int32_t tiles() const { return (int32_t)min((int64_t)(row.tiles - t), end - u); }
+    __device__ __forceinline__ void next(int32_t done) {
+        u += done;
+        t += done;
+        if (t < row.tiles) return;
+        u += kLineCost;
+        t = 0;
+        if (u >= end) return;
+        if (++h < p.kv_heads) return;
+        h = 0;
+        for (int32_t b = row.b + 1; b < p.batch; ++b) {
+            row = row_of(p, b, plane, plane_rows);
+            if (row.tiles) break;
+        }
+    }
+};
+
+// D (+)= A B, A in shared memory (`a` the low half of its descriptor) or, _ts, in TMEM (`a` its address); the high
+// halves of the descriptors are the same for all tiles.  The issuing thread has a few instructions for each of these,
+// so the operands come as sums of a word that the warp shares and a constant.
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(hi), "r"(idesc), "n"(ACC)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// 32 lanes x 32 consecutive 32-bit columns, from thread i of the warp to lane (base lane + i).
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+          "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+          "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two fp32 operations at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+// The largest of three; NaN counts for nothing.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+template <int KIND>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if (KIND == kBF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int KIND>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if (KIND == kBF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+// Infinity or NaN.
+template <int KIND>
+__device__ __forceinline__ bool special(uint16_t x) {
+    constexpr uint16_t e = KIND == kBF16 ? 0x7F80 : 0x7C00;
+    return (x & e) == e;
+}
+
+template <int KIND, int DP, int MT>
+struct TreeShape {
+    static constexpr int WARPS = 4 * MT + kLoaders / 32 + 1, THREADS = 32 * WARPS;
+    static constexpr int BLOCKS = MT == 1 && DP <= 128 ? 2 : 1;
+    static constexpr int R = MT * kRows;
+    static constexpr uint32_t Q_TILE = kRows * DP * 2, SLOT = kTok * DP * 2;
+    static constexpr uint32_t MOST = (BLOCKS == 2 ? 113 : 227) * 1024 - 8192 - 1536 - MT * Q_TILE;
+    static constexpr int SLOTS = MOST / SLOT < 8 ? MOST / SLOT : 8;
+    static constexpr size_t SMEM = 1024 + 512 + MT * Q_TILE + SLOTS * SLOT;
+    static constexpr uint32_t O_COL = MT * 2 * kTok;            // S (and P): [MT][2][64], then O: [MT][DP]
+    static constexpr uint32_t COLS = O_COL + MT * DP <= 256 ? 256 : 512;
+    static constexpr int BARS = 2 * SLOTS + 2 + 6 * MT;
+    static constexpr float SLACK = KIND == kF16 ? 6.f : 8.f;    // see the head of the file
+    static constexpr float SHIFT = KIND == kF16 ? 9.f : 0.f;
+    static_assert(SLOTS >= 4, "K two tiles ahead of V, and two more on their way");
+    static_assert(BARS * 8 + kBits * 8 + 16 + SLOTS * 4 <= 512, "barriers and notes fit their place");
+};
+
+enum : unsigned int { kCodeTreeLoad = 0x10000, kCodeTreeMma = 0x20000, kCodeTreeSoft = 0x40000 };
+
+template <int KIND, int DP, int MT>
+__global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KIND, DP, MT>::BLOCKS)
+    k_tree_attention(const TreeAttnParams p) {
+    typedef TreeShape<KIND, DP, MT> S;
+    constexpr int WARPS = S::WARPS, THREADS = S::THREADS, R = S::R, NS = S::SLOTS;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int64_t s_warp[WARPS];
+    __shared__ int64_t s_first[THREADS];
+    __shared__ int64_t s_offsets[kLoaders / 32][2 * kTok];
+    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* const q_s = smem;
+    uint8_t* const ring = smem + MT * S::Q_TILE;
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(ring + NS * S::SLOT);
+    uint64_t* const s_bits = bars + S::BARS;                              // [kBits] positions of a tile that are on a page
+    int32_t* const s_new = reinterpret_cast<int32_t*>(s_bits + kBits);    // [SLOTS] first new position of a V tile
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(s_new + NS);
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* const s_special = abort_flag + 1;                       // a V among the new positions held infinity or NaN
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (NS + s); };
+    const uint32_t q_full = bar0 + 8u * (2 * NS), q_empty = q_full + 8;
+    auto s_full = [&](int m, int buf) { return q_empty + 8u + 8u * (6 * m + buf); };
+    auto p_ready = [&](int m, int buf) { return q_empty + 8u + 8u * (6 * m + 2 + buf); };
+    // one for each of two tiles: a wait for tile k comes after tile k - 2 is done and before k + 2 can be, so that
+    // the parity names the phase
+    auto pv_done = [&](int m, int buf) { return q_empty + 8u + 8u * (6 * m + 4 + buf); };
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x / 32), 0), lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) mbar_init(full(s), kLoaders), mbar_init(empty(s), 1);
+        mbar_init(q_full, kLoaders), mbar_init(q_empty, 1);
+        for (int m = 0; m < MT; ++m)
+            for (int b = 0; b < 2; ++b) mbar_init(s_full(m, b), 1), mbar_init(p_ready(m, b), kRows), mbar_init(pv_done(m, b), 1);
+        *abort_flag = 0;
+        *s_special = 0;
+        fence_mbar_init();
+    }
+    if (warp == WARPS - 1) {
+        tmem_alloc(smem_u32(tmem_slot), S::COLS);
+        tmem_relinquish();
+    }
+    if (p.head_dim < DP) {  // columns past the head size stay zero for the whole call
+        uint4* const w = reinterpret_cast<uint4*>(smem);
+        for (uint32_t i = threadIdx.x; i < (MT * S::Q_TILE + NS * S::SLOT) / 16; i += THREADS) w[i] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+
+    // ---- the line of this plane, and this block's range of it
+    const int32_t plane = blockIdx.x % p.planes, c = blockIdx.x / p.planes;
+    auto places = [&](int32_t b) {
+        const int32_t n = row_of(p, b, plane, R).tiles;
+        return n ? (int64_t)(n + kLineCost) * p.kv_heads : 0;
+    };
+    int64_t total = 0;
+    for (uint32_t b = threadIdx.x; b < (uint32_t)p.batch; b += THREADS) total += places((int32_t)b);
+    {
+        int64_t sum;
+        sbt_attn::block_scan<WARPS>(total, &sum, s_warp);
+        total = sum;
+    }
+    const int64_t G = min(total, (int64_t)p.ranges);
+    bool idle = c >= G;
+    const Line line(total, G > 0 ? G : 1);
+    const int64_t u0 = idle ? total : line.start(c), u1 = idle ? total : line.start(c + 1);
+    int32_t b_first = 0;
+    int64_t u_first = 0;
+    {
+        int64_t before = 0;
+        for (uint32_t b0 = 0; b0 < (uint32_t)p.batch && before <= u0; b0 += THREADS) {
+            const uint32_t b = b0 + threadIdx.x;
+            int64_t sum;
+            const int64_t at = before + sbt_attn::block_scan<WARPS>(b < (uint32_t)p.batch ? places((int32_t)b) : 0, &sum, s_warp);
+            s_first[threadIdx.x] = at;
+            __syncthreads();
+            if (before <= u0 && u0 < before + sum) {
+                for (int i = lane; i < THREADS; i += 32) {
+                    const int64_t e = i + 1 < THREADS ? s_first[i + 1] : before + sum;
+                    const uint32_t hit = __ballot_sync(0xffffffffu, s_first[i] <= u0 && u0 < e);
+                    if (hit) {
+                        b_first = (int32_t)b0 + (i & ~31) + __ffs(hit) - 1;
+                        u_first = s_first[(i & ~31) + __ffs(hit) - 1];
+                    }
+                }
+            }
+            __syncthreads();
+            before += sum;
+        }
+    }
+    if (!p.desc_by_line && threadIdx.x == 0) p.desc[blockIdx.x].valid = 0;
+
+    Walk start = {p, plane, R, {}, 0, 0, 0, u1};
+    if (!idle) {
+        start.row = row_of(p, b_first, plane, R);
+        const int64_t width = start.row.tiles + kLineCost;
+        start.h = (int32_t)sbt_attn::divide(u0 - u_first, width);
+        const int64_t line_u = u_first + start.h * width + kLineCost;
+        start.u = u0 > line_u ? u0 : line_u;
+        start.t = (int32_t)(start.u - line_u);
+        idle = start.u >= u1;  // nothing but a line's empty places
+    }
+
+    if (idle) {
+    } else if (warp >= 4 * MT && warp < 4 * MT + kLoaders / 32) {
+        // ------------------------------------------------------------ copies
+        const int tid = threadIdx.x - 4 * MT * 32;
+        int item = 0, landed = 0;          // tiles begun, and signalled as landed
+        uint32_t scan = 0;                 // slots whose V holds new positions
+        bool ok = true;
+        int q_uses = 0;
+        int tile_no = 0;
+        const uint32_t ring_u32 = smem_u32(ring), q_u32 = smem_u32(q_s);
+        constexpr int LPR = DP <= 64 ? 8 : DP <= 128 ? 16 : 32, RPI = 32 / LPR;  // lanes of a row, 16 bytes each; rows at a time
+        const int lw = tid >> 5, byte0 = (lane % LPR) * 16, r0 = lane / LPR, row_bytes = p.head_dim * 2;
+        int64_t* const s_off = s_offsets[lw];  // of the rows of two tiles: byte offsets, -1 where there is none
+        // place of piece `w` (of BYTES) of row `r` in a tile of `rows` rows
+        auto place = [](uint32_t base, int rows, int r, int byte) {
+            return base + (uint32_t)(byte >> 7) * rows * 128u + r * 128u + ((((byte >> 4) & 7) ^ (r & 7)) << 4) + (byte & 15);
+        };
+        // This lane's rows of a tile are row0, row0 + STEP, ..; their places, less the rows' pitch, repeat.
+        constexpr int STEP = RPI * (kLoaders / 32), N = (kTok + STEP - 1) / STEP;
+        constexpr int PERIOD = STEP % 8 == 4 ? 2 : STEP % 4 == 2 ? 4 : 8;
+        const int row0 = lw * RPI + r0;
+        uint32_t at_place[PERIOD];
+#pragma unroll
+        for (int i = 0; i < PERIOD; ++i) at_place[i] = place(0, kTok, row0 + i * STEP, byte0) - i * STEP * 128;
+        // A whole tile in 16-byte pieces, every row of which is on a page: as few instructions as a copy can take, since
+        // three warps start all copies of an SM.
+        auto copy_tile = [&](uint32_t dst, const char* src, const int64_t* o) {
+            constexpr int BATCH = 6;
+            src += byte0;
+            if (byte0 < row_bytes)
+#pragma unroll
+                for (int i0 = 0; i0 < N; i0 += BATCH) {
+                    const char* a[BATCH];
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i)
+                        if (i0 + i < N) a[i] = src + o[min(row0 + (i0 + i) * STEP, kTok - 1)];
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i)
+                        if (i0 + i < N && ((i0 + i + 1) * STEP <= kTok || row0 + (i0 + i) * STEP < kTok))
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + at_place[(i0 + i) % PERIOD] +
+                                                                                           (i0 + i) * STEP * 128),
+                                         "l"(a[i])
+                                         : "memory");
+                }
+        };
+        auto wait_landed = [&](int in_flight) {  // at most so many of this thread's tiles are still on their way
+            switch (in_flight) {
+                case 0: sbt_attn::cp_wait<0>(); break;
+                case 1: sbt_attn::cp_wait<1>(); break;
+                case 2: sbt_attn::cp_wait<2>(); break;
+                case 3: sbt_attn::cp_wait<3>(); break;
+                case 4: sbt_attn::cp_wait<4>(); break;
+                case 5: sbt_attn::cp_wait<5>(); break;
+                case 6: sbt_attn::cp_wait<6>(); break;
+                default: sbt_attn::cp_wait<7>(); break;
+            }
+        };
+        // Copies the rows of a tile: at(r) is a row's address (NULL: zeros).
+        auto copy_rows = [&](uint32_t dst, uint8_t* dst_p, int rows, int bytes, auto at) {
+            if (bytes == 16) {
+                if (byte0 < row_bytes)
+                    for (int r = row0; r < rows; r += STEP) {
+                        const char* const a = at(r);
+                        sbt_attn::cp_async16(place(dst, rows, r, byte0), a ? a + byte0 : p.q, a ? 16 : 0);
+                    }
+            } else {
+                for (int r = lw; r < rows; r += kLoaders / 32) {
+                    const char* const a = at(r);
+                    for (int byte = lane * bytes; byte < row_bytes; byte += 32 * bytes) {
+                        if (bytes == 8)
+                            sbt_attn::cp_async8(place(dst, rows, r, byte), a ? a + byte : p.q, a ? 8 : 0);
+                        else if (bytes == 4)
+                            sbt_attn::cp_async4(place(dst, rows, r, byte), a ? a + byte : p.q, a ? 4 : 0);
+                        else
+                            *reinterpret_cast<uint16_t*>(dst_p + (place(0, rows, r, byte))) =
+                                a ? sbt_ld(reinterpret_cast<const uint16_t*>(a + byte)) : (uint16_t)0;
+                    }
+                }
+            }
+        };
+        // The oldest tile on its way has landed: it is signalled.
+        auto signal = [&]() {
+            wait_landed(item - landed - 1);
+            const int s = landed % NS;
+            if (scan >> s & 1) {
+                // this thread's own pieces of the rows of new positions: infinities and NaN become zero
+                scan &= ~(1u << s);
+                const int from = s_new[s];
+                uint8_t* const base = ring + s * S::SLOT;
+                auto clean = [&](int r, int byte, int bytes) {
+                    if (byte >= row_bytes) return;
+                    uint16_t* const x = reinterpret_cast<uint16_t*>(base + place(0, kTok, r, byte));
+                    for (int i = 0; i < bytes / 2; ++i)
+                        if (special<KIND>(x[i])) x[i] = 0, *s_special = 1;
+                };
+                if (p.copy_kv == 16) {
+                    for (int r = row0; r < kTok; r += STEP)
+                        if (r >= from) clean(r, byte0, 16);
+                } else {
+                    for (int r = lw; r < kTok; r += kLoaders / 32)
+                        for (int byte = lane * p.copy_kv; r >= from && byte < row_bytes; byte += 32 * p.copy_kv)
+                            clean(r, byte, p.copy_kv);
+                }
+            }
+            fence_proxy_async_smem();
+            if (!(p.withhold && landed == 0)) mbar_arrive(full(s));
+            ++landed;
+        };
+        // A free slot for the next tile; tiles that land meanwhile are signalled.
+        auto slot_of = [&]() {
+            const int s = item % NS, use = item / NS;
+            while (use > 0) {
+                const bool free = mbar_test_wait(empty(s), (use - 1) & 1);  // must not sleep: tiles may wait to be signalled
+                if (__all_sync(0xffffffffu, free)) break;
+                if (landed < item) {
+                    signal();
+                } else if (!__all_sync(0xffffffffu, mbar_wait_bounded(empty(s), (use - 1) & 1, p.wait_ns, abort_flag,
+                                                                      p.status, kCodeTreeLoad))) {
+                    ok = false;
+                    break;
+                }
+            }
+            return s;
+        };
+
+        for (Walk w = start; ok && w.u < w.end;) {
+            const TreeRow& row = w.row;
+            const int32_t T = w.tiles(), new0 = row.len - row.n;
+            // this lane's two positions of a tile and their pages, -1 where there is none
+            int32_t at[2], page[2];
+            auto look_up = [&](int32_t it) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int32_t pos = (w.t + it) * kTok + j * 32 + lane;
+                    page[j] = -1;
+                    if (it < T && pos < row.len) {
+                        const uint32_t pg = sbt_div(p.page_size, (uint32_t)pos);
+                        at[j] = pos - (int32_t)(pg * p.page_size.d);
+                        page[j] = sbt_ld(p.table + (int64_t)row.seq * p.ld_table + pg);  // read when the tile is begun
+                    }
+                }
+            };
+            bool all[2] = {false, false};  // of two tiles: every row is on a page
+            // tile it of K or V
+            auto tile = [&](const char* src, int32_t it, bool is_v) {
+                const int s = slot_of();
+                if (!ok) return;
+                if (is_v && (w.t + it + 1) * kTok > new0) {
+                    scan |= 1u << s;
+                    if (lane == 0) s_new[s] = max(0, new0 - (w.t + it) * kTok);
+                    __syncwarp();
+                }
+                const int64_t* const o = s_off + (it & 1) * kTok;
+                if (all[it & 1] && p.copy_kv == 16)
+                    copy_tile(ring_u32 + s * S::SLOT, src, o);
+                else
+                    copy_rows(ring_u32 + s * S::SLOT, ring + s * S::SLOT, kTok, p.copy_kv, [&](int r) {
+                    const int64_t x = o[r];
+                    return x < 0 ? nullptr : src + x;
+                });
+                sbt_attn::cp_commit();
+                ++item;
+            };
+            auto k_tile = [&](int32_t it) {  // the positions looked up last are this tile's
+                bool ok[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    ok[j] = page[j] >= 0 && page[j] < p.n_pages;
+                    s_off[(it & 1) * kTok + j * 32 + lane] =
+                        ok[j] ? (page[j] * p.ld_page + at[j] * p.ld_slot + w.h * p.ld_head) * 2 : -1;
+                }
+                const uint32_t lo = __ballot_sync(0xffffffffu, ok[0]), hi = __ballot_sync(0xffffffffu, ok[1]);
+                if (tid == 0) s_bits[tile_no & (kBits - 1)] = lo | (uint64_t)hi << 32;
+                all[it & 1] = (lo & hi) == ~0u;
+                ++tile_no;
+                __syncwarp();
+                look_up(it + 1);
+                tile(p.k, it, false);
+            };
+            look_up(0);
+            // queries, once nothing reads the last segment's
+            if (q_uses > 0) {
+                while (landed < item) signal();
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(q_empty, (q_uses - 1) & 1, p.wait_ns, abort_flag, p.status,
+                                                               kCodeTreeLoad))) {
+                    ok = false;
+                    break;
+                }
+            }
+            const int64_t first = (int64_t)plane * R;
+            for (int m = 0; m < MT; ++m)
+                copy_rows(q_u32 + m * S::Q_TILE, q_s + m * S::Q_TILE, kRows, p.copy_q, [&](int r) -> const char* {
+                    r += m * kRows;
+                    if (r >= row.count) return nullptr;
+                    const uint32_t i = sbt_div(p.group, (uint32_t)(first + r));
+                    const int32_t g = (int32_t)(first + r - (int64_t)i * p.group.d);
+                    return p.q + ((row.q0 + (int64_t)i) * p.ld_q + (int64_t)(w.h * (int32_t)p.group.d + g) * p.ld_qh) * 2;
+                });
+            sbt_attn::cp_commit();
+            // K runs two tiles ahead of V, as the products do
+            k_tile(0);
+            if (ok && T > 1) k_tile(1);
+            if (!ok) break;
+            wait_landed(T > 1 ? 2 : 1);
+            fence_proxy_async_smem();
+            mbar_arrive(q_full);
+            ++q_uses;
+            for (int32_t it = 0; ok && it < T; ++it) {
+                tile(p.v, it, true);
+                __syncwarp();  // its offsets make room for those of two tiles on
+                if (ok && it + 2 < T) k_tile(it + 2);
+            }
+            w.next(T);
+        }
+        while (ok && landed < item) signal();
+        sbt_attn::cp_wait<0>();
+    } else if (warp == WARPS - 1) {
+        // ------------------------------------------------------------ matrix instructions
+        // The whole warp walks and waits, so that what the instructions take is the same for all lanes; one lane issues.
+        const bool leader = lane == 0;
+        const uint32_t type = KIND == kBF16 ? (1u << 7) | (1u << 10) : 0u;
+        const uint32_t idesc_s = (1u << 4) | type | ((kTok >> 3) << 17) | ((kRows >> 4) << 24);
+        const uint32_t idesc_o = (1u << 4) | type | ((DP >> 3) << 17) | ((kRows >> 4) << 24) | kIdescBMnMajor;
+        const uint64_t k_desc = smem_desc_sw128(0), v_desc = smem_desc_mn_sw128(0, kTok * 128);
+        const uint32_t k_lo = (uint32_t)k_desc, k_hi = (uint32_t)(k_desc >> 32);
+        const uint32_t v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32);
+        const uint32_t ring_a = smem_u32(ring) >> 4, q_a = k_lo + (smem_u32(q_s) >> 4);
+        int q_uses = 0, q_frees = 0, slot = 0;
+        uint32_t full_phase = 0;
+        int64_t k_no = 0, pv_no = 0;   // tiles multiplied with Q, and with P
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, p.wait_ns, abort_flag, p.status, kCodeTreeMma));
+            if (ok) tc_fence_after();
+            return ok;
+        };
+        auto next_slot = [&]() {
+            if (++slot == NS) slot = 0, full_phase ^= 1;
+        };
+        auto scores = [&](bool last) {
+            const int buf = (int)(k_no & 1);
+            if (!wait(full(slot), full_phase)) return;
+            const uint32_t b = k_lo + ring_a + slot * (S::SLOT >> 4);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                // this S still holds the P of two tiles ago until its product is done
+                if (k_no >= 2 && !wait(pv_done(m, buf), (uint32_t)((k_no - 2) >> 1) & 1)) return;
+                const uint32_t d = tmem + (m * 2 + buf) * kTok;
+                if (leader) {
+#pragma unroll
+                    for (int j = 0; j < DP / 16; ++j) {
+                        const uint32_t qj = (m * S::Q_TILE + (j / 4) * kRows * 128 + (j % 4) * 32) >> 4;
+                        const uint32_t kj = ((j / 4) * kTok * 128 + (j % 4) * 32) >> 4;
+                        if (j == 0)
+                            mma_ss<false>(d, q_a + qj, b + kj, k_hi, idesc_s);
+                        else
+                            mma_ss<true>(d, q_a + qj, b + kj, k_hi, idesc_s);
+                    }
+                    tc_commit(s_full(m, buf));
+                }
+                __syncwarp();
+            }
+            if (leader) {
+                tc_commit(empty(slot));
+                if (last) tc_commit(q_empty);
+            }
+            __syncwarp();
+            if (last) ++q_frees;
+            next_slot();
+            ++k_no;
+        };
+        for (Walk w = start; ok && w.u < w.end;) {
+            const int32_t T = w.tiles();
+            if (!wait(q_full, q_uses++ & 1)) break;
+            scores(T == 1);
+            if (ok && T > 1) scores(T == 2);
+            for (int32_t it = 0; ok && it < T; ++it) {
+                const int buf = (int)(pv_no & 1);
+                if (!wait(full(slot), full_phase)) break;
+                const uint32_t b = v_lo + ring_a + slot * (S::SLOT >> 4);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    if (!wait(p_ready(m, buf), (uint32_t)(pv_no >> 1) & 1)) break;
+                    const uint32_t a = tmem + (m * 2 + buf) * kTok, d = tmem + S::O_COL + m * DP;
+                    if (leader) {
+#pragma unroll
+                        for (int j = 0; j < 2 * kTok / 16; ++j)  // the first numbers, then the second ones
+                            mma_ts(d, a + j * 8, b + ((j % 4) * 2048 >> 4), v_hi, idesc_o, j > 0 ? 1u : it > 0);
+                        tc_commit(pv_done(m, buf));
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (leader) tc_commit(empty(slot));
+                __syncwarp();
+                next_slot();
+                ++pv_no;
+                if (it + 2 < T) scores(it + 3 == T);
+            }
+            w.next(T);
+        }
+        // every instruction issued has completed once this wait is over (q_empty is not used any more)
+        if (leader) tc_commit(q_empty);
+        __syncwarp();
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(q_empty, (uint32_t)(q_frees & 1))) {
+            if (globaltimer() - t0 > p.wait_ns) break;
+        }
+        __syncwarp();
+    } else if (warp < 4 * MT) {
+        // ------------------------------------------------------------ softmax: a row per thread
+        const int m = warp / 4, r = threadIdx.x;                 // row of the plane's tile
+        const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+        const uint32_t o_t = tmem + S::O_COL + m * DP + lanes;
+        int64_t k_no = 0;
+        bool first_seg = true, ok = true;
+        int tile_no = 0;
+        for (Walk w = start; ok && w.u < w.end;) {
+            const TreeRow row = w.row;
+            const int32_t T = w.tiles(), new0 = row.len - row.n, h = w.h, t0 = w.t;
+            const bool mine = r < row.count, some = (r & ~31) < row.count;
+            const uint32_t rr = (uint32_t)((int64_t)plane * R + r);
+            const int32_t i = mine ? (int32_t)sbt_div(p.group, rr) : 0, g = mine ? (int32_t)(rr - i * p.group.d) : 0;
+            const int64_t q_row = row.q0 + i;
+            float ref = -CUDART_INF_F, l = 0.f;
+            // bit j: this row sees position j of the tile (if it is on a page)
+            auto sees = [&](int32_t pos0) -> uint64_t {
+                const int64_t j0 = (int64_t)pos0 - new0;         // the new token at the tile's first position
+                uint64_t bits = 0;
+                if (p.mask) {
+                    const uint32_t* const a = p.mask + q_row * p.ld_mask;
+                    const int64_t w0 = j0 >> 5;
+                    auto word = [&](int64_t x) -> uint64_t { return mine && x >= 0 && x < p.ld_mask ? sbt_ld(a + x) : 0u; };
+                    const int sh = (int)(j0 & 31);
+                    bits = (word(w0) | word(w0 + 1) << 32) >> sh;
+                    if (sh) bits |= word(w0 + 2) << (64 - sh);
+                } else if (i >= j0) {
+                    bits = i - j0 >= 63 ? ~0ull : (2ull << (i - j0)) - 1;
+                }
+                if (j0 < 0) bits = j0 <= -64 ? ~0ull : bits | ((1ull << -j0) - 1);
+                const int64_t left = row.n - j0;                 // positions up to the sequence's end
+                if (left < 64) bits &= left <= 0 ? 0 : (1ull << left) - 1;
+                return bits;
+            };
+            for (int32_t it = 0; it < T; ++it, ++k_no) {
+                const int buf = (int)(k_no & 1);
+                if (!mbar_wait_bounded(s_full(m, buf), (uint32_t)(k_no >> 1) & 1, p.wait_ns, abort_flag, p.status, kCodeTreeSoft))
+                    ok = false;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t on_page = s_bits[tile_no++ & (kBits - 1)];
+                if (some) {
+                    const uint32_t s_t = tmem + (m * 2 + buf) * kTok + lanes;
+                    uint32_t x[2][32];
+                    tmem_ld_32x32b_x32(s_t, x[0]);
+                    tmem_ld_32x32b_x32(s_t + 32, x[1]);
+                    tmem_ld_wait();
+                    const int32_t pos0 = (t0 + it) * kTok;
+                    uint64_t vis = ~0ull;
+                    const bool partial = on_page != ~0ull || pos0 + kTok > new0;
+                    if (partial) vis = on_page & sees(pos0);
+                    if (p.negate)
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) x[j / 32][j % 32] ^= 0x80000000u;
+                    if (partial)
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (!(vis >> j & 1)) x[j / 32][j % 32] = 0xff800000u;
+                    float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+                    for (int j = 0; j < 64; j += 2)
+                        top[j / 2 & 3] = max3(top[j / 2 & 3], __uint_as_float(x[j / 32][j % 32]), __uint_as_float(x[j / 32][j % 32 + 1]));
+                    float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    if (most != -CUDART_INF_F) most *= p.scale;
+                    const bool take = most > ref + S::SLACK;     // ref = -inf: as soon as anything is seen
+                    if (__any_sync(0xffffffffu, take)) {
+                        const float f = take ? sbt_attn::exp2_fast(ref - most) : 1.f;
+                        if (take) ref = most;
+                        l *= f;
+                        if (it > 0) {
+                            if (!mbar_wait_bounded(pv_done(m, buf ^ 1), (uint32_t)((k_no - 1) >> 1) & 1, p.wait_ns, abort_flag,
+                                                   p.status, kCodeTreeSoft))
+                                ok = false;
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int d = 0; d < DP; d += 32) {
+                                uint32_t o[32];
+                                tmem_ld_32x32b_x32(o_t + d, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_st_x32(o_t + d, o);
+                            }
+                        }
+                    }
+                    const float base = ref == -CUDART_INF_F ? 0.f : S::SHIFT - ref;
+                    float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+                    uint32_t hi[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float2 y = fma2(make_float2(__uint_as_float(x[j / 16][2 * j % 32]), __uint_as_float(x[j / 16][2 * j % 32 + 1])),
+                                              make_float2(p.scale, p.scale), make_float2(base, base));
+                        float2 e = make_float2(sbt_attn::exp2_fast(y.x), sbt_attn::exp2_fast(y.y));
+                        if (partial) {  // a scale of zero makes NaN of a masked score
+                            e.x = vis >> (2 * j) & 1 ? e.x : 0.f;
+                            e.y = vis >> (2 * j + 1) & 1 ? e.y : 0.f;
+                        }
+                        sum[j & 1] = add2(sum[j & 1], e);
+                        hi[j] = pack2<KIND>(e.x, e.y);
+                        const float2 v = unpack2<KIND>(hi[j] ^ 0x80008000u);
+                        const float2 lo = add2(e, v);
+                        x[j / 16][j % 16] = pack2<KIND>(lo.x, lo.y);  // in the place of scores that are used up
+                    }
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    tmem_st_x32(s_t, hi);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) hi[j] = x[j / 16][j % 16];
+                    tmem_st_x32(s_t + 32, hi);
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                mbar_arrive(p_ready(m, buf));
+            }
+            if (!ok) break;
+            // ---- the segment's state, once the last product is done
+            if (!mbar_wait_bounded(pv_done(m, (int)(k_no - 1) & 1), (uint32_t)((k_no - 1) >> 1) & 1, p.wait_ns, abort_flag,
+                                   p.status, kCodeTreeSoft))
+                ok = false;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const bool ends = t0 + T == row.tiles, cut = t0 != 0, whole = ends && !cut;
+            const int32_t qh = h * (int32_t)p.group.d + g;
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (first_seg ? 0 : 1);
+            const float m_out = ref == -CUDART_INF_F ? ref : ref - S::SHIFT, inv = sbt_attn::inverse(l);
+            if (some) {
+                if (mine && whole && p.lse) p.lse[q_row * p.q_heads + qh] = sbt_attn::log_sum(m_out, l);
+                if (mine && !whole) p.part_ml[slot * R + r] = make_float2(m_out, l);
+                const bool poison = *s_special != 0;
+#pragma unroll 1
+                for (int d = 0; d < DP; d += 32) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    tmem_ld_32x32b_x32(o_t + d, o);
+                    tmem_ld_wait();
+                    if (!mine) continue;
+                    if (whole)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv);
+                    if (poison) {
+                        // what was taken out of the new positions' values goes to the rows that see it
+                        for (int32_t pos = max(max(new0, 0), t0 * kTok); pos < min((t0 + T) * kTok, row.len); ++pos) {
+                            if (!(sees(pos) & 1)) continue;
+                            const uint32_t pg = sbt_div(p.page_size, (uint32_t)pos);
+                            const int32_t page = sbt_ld(p.table + (int64_t)row.seq * p.ld_table + pg);
+                            if (page < 0 || page >= p.n_pages) continue;
+                            const uint16_t* const v = reinterpret_cast<const uint16_t*>(p.v) + page * p.ld_page +
+                                (int64_t)(pos - (int32_t)(pg * p.page_size.d)) * p.ld_slot + h * p.ld_head;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (d + j < p.head_dim) {
+                                    const uint16_t e = sbt_ld(v + d + j);
+                                    if (special<KIND>(e)) o[j] = __float_as_uint(__uint_as_float(o[j]) + Num<KIND>::get(e));
+                                }
+                        }
+                    }
+                    if (!whole) {
+                        float4* const to = reinterpret_cast<float4*>(p.part_o + (slot * R + r) * DP + d);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            to[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                                __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+                    } else {
+                        uint16_t* const to = reinterpret_cast<uint16_t*>(p.out) + q_row * p.ld_out + qh * p.ld_oh + d;
+                        if (p.out_vec) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (d + 8 * j < p.head_dim) {
+                                    uint32_t y[4];
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+                                        y[k] = pack2<KIND>(__uint_as_float(o[8 * j + 2 * k]), __uint_as_float(o[8 * j + 2 * k + 1]));
+                                    reinterpret_cast<uint4*>(to)[j] = make_uint4(y[0], y[1], y[2], y[3]);
+                                }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (d + j < p.head_dim) to[j] = Num<KIND>::put(__uint_as_float(o[j]));
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            if (!cut && threadIdx.x == 0) {
+                TreeDesc e = {};
+                if (!whole) {
+                    e.valid = 1, e.b = row.b, e.h = h, e.plane = plane, e.first = c, e.first_slot = first_seg ? 0 : 1;
+                    e.last = line.warp_of(w.u - t0 + row.tiles - 1);
+                }
+                if (p.desc_by_line)
+                    p.desc[((int64_t)row.b * p.kv_heads + h) * p.planes + plane] = e;
+                else if (e.valid)
+                    p.desc[blockIdx.x] = e;
+            }
+            first_seg = false;
+            w.next(T);
+        }
+    }
+
+    // ---- rows of entries that hold no position they could see: zeros, and a log-sum-exp of minus infinity
+    for (int64_t b = c; b < p.batch; b += p.ranges) {
+        const TreeRow row = row_of(p, (int32_t)b, plane, R);
+        if (row.tiles) continue;
+        for (int64_t e = threadIdx.x; e < (int64_t)row.count * p.kv_heads; e += THREADS) {
+            const int32_t h = (int32_t)(e / row.count);
+            const uint32_t rr = (uint32_t)((int64_t)plane * R + e - (int64_t)h * row.count), i = sbt_div(p.group, rr);
+            const int32_t qh = h * (int32_t)p.group.d + (int32_t)(rr - i * p.group.d);
+            uint16_t* const to = reinterpret_cast<uint16_t*>(p.out) + (row.q0 + (int64_t)i) * p.ld_out + qh * p.ld_oh;
+            for (int d = 0; d < p.head_dim; ++d) to[d] = 0;
+            if (p.lse) p.lse[(row.q0 + (int64_t)i) * p.q_heads + qh] = -CUDART_INF_F;
+        }
+        if (p.desc_by_line)
+            for (int32_t h = threadIdx.x; h < p.kv_heads; h += THREADS)
+                p.desc[((int64_t)b * p.kv_heads + h) * p.planes + plane].valid = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag && p.desc_by_line && threadIdx.x == 0 && !idle)
+        for (Walk w = start; w.u < w.end; w.next(w.tiles()))  // what was not finished is not joined
+            if (w.t == 0) p.desc[((int64_t)w.row.b * p.kv_heads + w.h) * p.planes + plane].valid = 0;
+    if (warp == WARPS - 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, S::COLS);
+    }
+}
+
+// Adds the parts of cut lines in the order of the line: a block takes kJoin / (DP
+// / 4) rows of one of them, a thread four elements.
+template <int KIND, int DP, int MT>
+__global__ void __launch_bounds__(kJoin) k_tree_join(const TreeAttnParams p, int32_t pieces) {
+    constexpr int R = MT * kRows, LANES = DP / 4, PER = kJoin / LANES;
+    griddep_wait();
+    const TreeDesc e = p.desc[blockIdx.x / pieces];
+    if (!e.valid) return;
+    const TreeRow row = row_of(p, e.b, e.plane, R);
+    const int r = (blockIdx.x % pieces) * PER + threadIdx.x / LANES, d = threadIdx.x % LANES * 4;
+    if (threadIdx.x >= PER * LANES || r >= row.count) return;
+    auto slot = [&](int32_t i) -> int64_t {
+        return 2 * ((int64_t)(e.first + i) * p.planes + e.plane) + (i == 0 ? e.first_slot : 0);
+    };
+    const int32_t n = e.last - e.first + 1;
+    float top = -CUDART_INF_F;
+#pragma unroll 4
+    for (int32_t i = 0; i < n; ++i) top = fmaxf(top, sbt_ld(p.part_ml + slot(i) * R + r).x);
+    const float ts = top == -CUDART_INF_F ? 0.f : top;
+    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int32_t i = 0; i < n; ++i) {
+        const float2 ml = sbt_ld(p.part_ml + slot(i) * R + r);
+        const float4 x = sbt_ld(reinterpret_cast<const float4*>(p.part_o + (slot(i) * R + r) * DP + d));
+        const float a = sbt_attn::exp2_fast(ml.x - ts);
+        l += ml.y * a;
+        o[0] += x.x * a, o[1] += x.y * a, o[2] += x.z * a, o[3] += x.w * a;
+    }
+    const uint32_t rr = (uint32_t)((int64_t)e.plane * R + r), i = sbt_div(p.group, rr);
+    const int32_t qh = e.h * (int32_t)p.group.d + (int32_t)(rr - i * p.group.d);
+    const int64_t q_row = row.q0 + (int64_t)i;
+    const float inv = sbt_attn::inverse(l);
+    uint16_t* const to = reinterpret_cast<uint16_t*>(p.out) + q_row * p.ld_out + qh * p.ld_oh;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (d + j < p.head_dim) to[d + j] = Num<KIND>::put(o[j] * inv);
+    if (d == 0 && p.lse) p.lse[q_row * p.q_heads + qh] = sbt_attn::log_sum(top, l);
+}
+
+// Blocks that the workspace has room for: two an SM of 128 rows, or one of 256.
+inline int64_t part_blocks(const sbt_context* ctx, int mt) { return (int64_t)ctx->sm_count * (mt == 1 ? 2 : 1); }
+
+template <int KIND, int DP, int MT>
+sbt_status enqueue(sbt_context* ctx, TreeAttnParams& p, void* workspace, cudaStream_t stream) {
+    typedef TreeShape<KIND, DP, MT> S;
+    const int resident = std::min<int64_t>(sbt_resident_blocks<k_tree_attention<KIND, DP, MT>>(ctx, S::THREADS, S::SMEM),
+                                           part_blocks(ctx, MT));
+    p.planes = (int32_t)sbt_cdiv((int64_t)p.max_new * p.group.d, S::R);
+    p.ranges = std::max(1, resident / p.planes);
+    const int64_t blocks = (int64_t)p.ranges * p.planes, lines = (int64_t)p.batch * p.kv_heads * p.planes;
+    p.desc_by_line = lines <= blocks;
+    p.desc = (TreeDesc*)workspace;
+    p.part_ml = (float2*)((char*)workspace + sbt_cdiv(blocks * sizeof(TreeDesc), 256) * 256);
+    p.part_o = (float*)(p.part_ml + 2 * blocks * S::R);
+    sbt_status st = sbt_cuda_check(sbt_launch_dependent(k_tree_attention<KIND, DP, MT>, dim3((unsigned)blocks),
+                                                        dim3(S::THREADS), S::SMEM, stream, p),
+                                   "paged_tree_attention launch");
+    if (st || (st = sbt_after_launch(ctx, "paged_tree_attention"))) return st;
+    if (p.ranges == 1) return SBT_OK;  // no line is cut
+    const int64_t n_desc = p.desc_by_line ? lines : blocks;
+    const int32_t pieces = (int32_t)sbt_cdiv(std::min<int64_t>(S::R, (int64_t)p.max_new * p.group.d), kJoin / (DP / 4));
+    st = sbt_cuda_check(sbt_launch_dependent(k_tree_join<KIND, DP, MT>, dim3((unsigned)(n_desc * pieces)), dim3(kJoin), 0,
+                                             stream, p, pieces),
+                        "paged_tree_attention join launch");
+    if (st) return st;
+    return sbt_after_launch(ctx, "paged_tree_attention join");
+}
+
+// One translation unit each: the head sizes to 128 and those past it.
+template <int KIND> sbt_status narrow(sbt_context* ctx, TreeAttnParams& p, bool two, void* workspace, cudaStream_t stream);
+template <int KIND> sbt_status wide(sbt_context* ctx, TreeAttnParams& p, void* workspace, cudaStream_t stream);
+
+}  // namespace sbt_tree
