@@ -71,7 +71,7 @@ struct TreeAttnParams {
     int32_t rows, batch, max_new, q_heads, kv_heads, n_seq, head_dim, max_len;
     int32_t planes;                            // tiles of MT * 128 rows that an entry may need
     int32_t ranges;                            // blocks per plane
-    int32_t copy_q, copy_kv, out_vec;          // bytes of one copy into shared memory; out as 16-byte vectors
+    int32_t copy_kv, q_vec, out_vec;           // bytes of a copy by lanes; q and out as 16-byte vectors
     int32_t desc_by_line;                      // descriptors by line (there are no more lines than blocks), else by block
     sbt_fastdiv group, page_size;
     float scale;                               // |scale| log2 e
@@ -82,6 +82,12 @@ struct TreeAttnParams {
     TreeDesc* desc;
     float2* part_ml;                           // [2 blocks][MT * 128]
     float* part_o;                             // [2 blocks][MT * 128][DP]
+};
+
+// Keys and values as tensors of pages, heads, slots and elements.
+struct TreeMaps {
+    CUtensorMap k, v;
+    bool use;
 };
 
 // Entry b's rows of one plane: tokens are the rows q0 .. q0 + n - 1 of q, the last n of len positions.
@@ -220,9 +226,9 @@ __device__ __forceinline__ bool special(uint16_t x) {
     return (x & e) == e;
 }
 
-template <int KIND, int DP, int MT>
+template <int KIND, int DP, int MT, bool TMA>
 struct TreeShape {
-    static constexpr int WARPS = 4 * MT + kLoaders / 32 + 1, THREADS = 32 * WARPS;
+    static constexpr int WARPS = 4 * MT + (TMA ? 1 : kLoaders / 32) + 1, THREADS = 32 * WARPS;
     static constexpr int BLOCKS = MT == 1 && DP <= 128 ? 2 : 1;
     static constexpr int R = MT * kRows;
     static constexpr uint32_t Q_TILE = kRows * DP * 2, SLOT = kTok * DP * 2;
@@ -235,43 +241,43 @@ struct TreeShape {
     static constexpr float SLACK = KIND == kF16 ? 6.f : 8.f;    // see the head of the file
     static constexpr float SHIFT = KIND == kF16 ? 9.f : 0.f;
     static_assert(SLOTS >= 4, "K two tiles ahead of V, and two more on their way");
-    static_assert(BARS * 8 + kBits * 8 + 16 + SLOTS * 4 <= 512, "barriers and notes fit their place");
+    static_assert(BARS * 8 + kBits * 8 + 16 <= 512, "barriers and notes fit their place");
 };
 
 enum : unsigned int { kCodeTreeLoad = 0x10000, kCodeTreeMma = 0x20000, kCodeTreeSoft = 0x40000 };
 
-template <int KIND, int DP, int MT>
-__global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KIND, DP, MT>::BLOCKS)
-    k_tree_attention(const TreeAttnParams p) {
-    typedef TreeShape<KIND, DP, MT> S;
+template <int KIND, int DP, int MT, bool TMA>
+__global__ void __launch_bounds__(TreeShape<KIND, DP, MT, TMA>::THREADS, TreeShape<KIND, DP, MT, TMA>::BLOCKS)
+    k_tree_attention(const TreeAttnParams p, const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map) {
+    typedef TreeShape<KIND, DP, MT, TMA> S;
     constexpr int WARPS = S::WARPS, THREADS = S::THREADS, R = S::R, NS = S::SLOTS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int64_t s_warp[WARPS];
     __shared__ int64_t s_first[THREADS];
-    __shared__ int64_t s_offsets[kLoaders / 32][2 * kTok];
+    __shared__ int64_t s_offsets[TMA ? 1 : kLoaders / 32][2 * kTok];
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* const q_s = smem;
     uint8_t* const ring = smem + MT * S::Q_TILE;
     uint64_t* const bars = reinterpret_cast<uint64_t*>(ring + NS * S::SLOT);
     uint64_t* const s_bits = bars + S::BARS;                              // [kBits] positions of a tile that are on a page
-    int32_t* const s_new = reinterpret_cast<int32_t*>(s_bits + kBits);    // [SLOTS] first new position of a V tile
-    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(s_new + NS);
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(s_bits + kBits);
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* const s_special = abort_flag + 1;                       // a V among the new positions held infinity or NaN
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (NS + s); };
-    const uint32_t q_full = bar0 + 8u * (2 * NS), q_empty = q_full + 8;
-    auto s_full = [&](int m, int buf) { return q_empty + 8u + 8u * (6 * m + buf); };
-    auto p_ready = [&](int m, int buf) { return q_empty + 8u + 8u * (6 * m + 2 + buf); };
+    const uint32_t q_full = bar0 + 8u * (2 * NS), all_done = q_full + 8;
+    auto s_full = [&](int m, int buf) { return all_done + 8u + 8u * (6 * m + buf); };
+    auto p_ready = [&](int m, int buf) { return all_done + 8u + 8u * (6 * m + 2 + buf); };
     // one for each of two tiles: a wait for tile k comes after tile k - 2 is done and before k + 2 can be, so that
     // the parity names the phase
-    auto pv_done = [&](int m, int buf) { return q_empty + 8u + 8u * (6 * m + 4 + buf); };
+    auto pv_done = [&](int m, int buf) { return all_done + 8u + 8u * (6 * m + 4 + buf); };
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x / 32), 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < NS; ++s) mbar_init(full(s), kLoaders), mbar_init(empty(s), 1);
-        mbar_init(q_full, kLoaders), mbar_init(q_empty, 1);
+        for (int s = 0; s < NS; ++s) mbar_init(full(s), TMA ? 1 : kLoaders), mbar_init(empty(s), 1);
+        mbar_init(q_full, R), mbar_init(all_done, 1);
         for (int m = 0; m < MT; ++m)
             for (int b = 0; b < 2; ++b) mbar_init(s_full(m, b), 1), mbar_init(p_ready(m, b), kRows), mbar_init(pv_done(m, b), 1);
         *abort_flag = 0;
@@ -282,7 +288,7 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
         tmem_alloc(smem_u32(tmem_slot), S::COLS);
         tmem_relinquish();
     }
-    if (p.head_dim < DP) {  // columns past the head size stay zero for the whole call
+    if (!TMA && p.head_dim < DP) {  // columns past the head size stay zero for the whole call
         uint4* const w = reinterpret_cast<uint4*>(smem);
         for (uint32_t i = threadIdx.x; i < (MT * S::Q_TILE + NS * S::SLOT) / 16; i += THREADS) w[i] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
@@ -348,21 +354,94 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
     }
 
     if (idle) {
-    } else if (warp >= 4 * MT && warp < 4 * MT + kLoaders / 32) {
-        // ------------------------------------------------------------ copies
+    } else if (TMA && warp == 4 * MT) {
+        // ------------------------------------------------------------ copies by the tensor copy engine
+        // A tile is a box of 64 elements and a page's positions (64 at most) for every 128 bytes of its rows; a lane
+        // starts one of them.  A page that is not there is a coordinate outside the tensor, which reads as zeros.
+        const int per_page = min((int)p.page_size.d, kTok), boxes = kTok / per_page * (DP / 64);
+        const int mine = lane / (DP / 64), x = lane % (DP / 64) * 64;  // page of the tile, first element
+        const uint32_t box_at = smem_u32(ring) + (x / 64) * kTok * 128 + mine * per_page * 128;
+        int slot = 0, tile_no = 0;
+        uint32_t phase = 1;  // the first pass finds the slots empty
+        bool ok = true;
+        int64_t items = 0;
+        for (Walk w = start; ok && w.u < w.end;) {
+            const TreeRow& row = w.row;
+            const int32_t T = w.tiles();
+            int32_t page[4], at[4];    // of four tiles, by their numbers modulo 4: pages are asked for two tiles ahead
+            auto look_up = [&](int32_t it, int32_t& page, int32_t& at) {
+                const int32_t pos = (w.t + it) * kTok + mine * per_page;
+                page = -1, at = 0;
+                if (lane < boxes && it < T && pos < row.len) {
+                    const uint32_t j = sbt_div(p.page_size, (uint32_t)pos);
+                    at = pos - (int32_t)(j * p.page_size.d);
+                    page = sbt_ld(p.table + (int64_t)row.seq * p.ld_table + j);
+                }
+            };
+            auto tile = [&](const CUtensorMap* map, int32_t page, int32_t at) {
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(empty(slot), phase, p.wait_ns, abort_flag, p.status, kCodeTreeLoad))) {
+                    ok = false;
+                    return;
+                }
+                // the test hook's first tile is neither announced nor started
+                const bool withheld = p.withhold && items == 0;
+                if (lane == 0 && !withheld) mbar_arrive_expect_tx(full(slot), S::SLOT);
+                __syncwarp();
+                if (lane < boxes && !withheld)
+                    tma_load_4d(box_at + slot * S::SLOT, map, x, at, w.h, page >= 0 && page < p.n_pages ? page : -1, full(slot));
+                ++items;
+                if (++slot == NS) slot = 0, phase ^= 1;
+            };
+            auto k_tile = [&](int32_t page, int32_t at) {
+                uint64_t bits = 0;
+                if (lane < boxes && x == 0 && page >= 0 && page < p.n_pages)
+                    bits = (per_page == kTok ? ~0ull : (1ull << per_page) - 1) << (mine * per_page);
+                const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)bits);
+                const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32));
+                if (lane == 0) s_bits[tile_no & (kBits - 1)] = lo | (uint64_t)hi << 32;
+                ++tile_no;
+                __syncwarp();
+                tile(&k_map, page, at);
+            };
+            // K runs two tiles ahead of V, as the products do
+#pragma unroll
+            for (int i = 0; i < 4; ++i) look_up(i, page[i], at[i]);
+            k_tile(page[0], at[0]);
+            if (ok && T > 1) k_tile(page[1], at[1]);
+            for (int32_t it0 = 0; ok && it0 < T; it0 += 4)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int32_t it = it0 + i;
+                    if (ok && it < T) {
+                        tile(&v_map, page[i], at[i]);
+                        look_up(it + 4, page[i], at[i]);
+                        if (ok && it + 2 < T) k_tile(page[(i + 2) & 3], at[(i + 2) & 3]);
+                    }
+                }
+            w.next(T);
+        }
+        // copies in flight land before the block leaves
+        for (int64_t i = 0; i < items && i < NS; ++i) {
+            if (slot == 0) slot = NS, phase ^= 1;
+            --slot;
+            const uint64_t t0 = globaltimer();
+            while (!(p.withhold && items <= NS && i == items - 1) && !mbar_try_wait(full(slot), phase ^ 1) && globaltimer() - t0 < p.wait_ns) {
+            }
+        }
+        __syncwarp();
+    } else if (!TMA && warp >= 4 * MT && warp < WARPS - 1) {
+        // ------------------------------------------------------------ copies by lanes
         const int tid = threadIdx.x - 4 * MT * 32;
         int item = 0, landed = 0;          // tiles begun, and signalled as landed
-        uint32_t scan = 0;                 // slots whose V holds new positions
         bool ok = true;
-        int q_uses = 0;
         int tile_no = 0;
-        const uint32_t ring_u32 = smem_u32(ring), q_u32 = smem_u32(q_s);
+        const uint32_t ring_u32 = smem_u32(ring);
         constexpr int LPR = DP <= 64 ? 8 : DP <= 128 ? 16 : 32, RPI = 32 / LPR;  // lanes of a row, 16 bytes each; rows at a time
         const int lw = tid >> 5, byte0 = (lane % LPR) * 16, r0 = lane / LPR, row_bytes = p.head_dim * 2;
         int64_t* const s_off = s_offsets[lw];  // of the rows of two tiles: byte offsets, -1 where there is none
-        // place of piece `w` (of BYTES) of row `r` in a tile of `rows` rows
-        auto place = [](uint32_t base, int rows, int r, int byte) {
-            return base + (uint32_t)(byte >> 7) * rows * 128u + r * 128u + ((((byte >> 4) & 7) ^ (r & 7)) << 4) + (byte & 15);
+        // place of a byte of row r
+        auto place = [](uint32_t base, int r, int byte) {
+            return base + (uint32_t)(byte >> 7) * kTok * 128u + r * 128u + ((((byte >> 4) & 7) ^ (r & 7)) << 4) + (byte & 15);
         };
         // This lane's rows of a tile are row0, row0 + STEP, ..; their places, less the rows' pitch, repeat.
         constexpr int STEP = RPI * (kLoaders / 32), N = (kTok + STEP - 1) / STEP;
@@ -370,7 +449,7 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
         const int row0 = lw * RPI + r0;
         uint32_t at_place[PERIOD];
 #pragma unroll
-        for (int i = 0; i < PERIOD; ++i) at_place[i] = place(0, kTok, row0 + i * STEP, byte0) - i * STEP * 128;
+        for (int i = 0; i < PERIOD; ++i) at_place[i] = place(0, row0 + i * STEP, byte0) - i * STEP * 128;
         // A whole tile in 16-byte pieces, every row of which is on a page: as few instructions as a copy can take, since
         // three warps start all copies of an SM.
         auto copy_tile = [&](uint32_t dst, const char* src, const int64_t* o) {
@@ -404,24 +483,26 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
                 default: sbt_attn::cp_wait<7>(); break;
             }
         };
-        // Copies the rows of a tile: at(r) is a row's address (NULL: zeros).
-        auto copy_rows = [&](uint32_t dst, uint8_t* dst_p, int rows, int bytes, auto at) {
+        // The same with rows that are not there (zeros) or pieces of less than 16 bytes.
+        auto copy_rows = [&](uint32_t dst, uint8_t* dst_p, const char* src, const int64_t* o) {
+            const int bytes = p.copy_kv;
+            auto at = [&](int r) { return o[r] < 0 ? nullptr : src + o[r]; };
             if (bytes == 16) {
                 if (byte0 < row_bytes)
-                    for (int r = row0; r < rows; r += STEP) {
+                    for (int r = row0; r < kTok; r += STEP) {
                         const char* const a = at(r);
-                        sbt_attn::cp_async16(place(dst, rows, r, byte0), a ? a + byte0 : p.q, a ? 16 : 0);
+                        sbt_attn::cp_async16(place(dst, r, byte0), a ? a + byte0 : p.q, a ? 16 : 0);
                     }
             } else {
-                for (int r = lw; r < rows; r += kLoaders / 32) {
+                for (int r = lw; r < kTok; r += kLoaders / 32) {
                     const char* const a = at(r);
                     for (int byte = lane * bytes; byte < row_bytes; byte += 32 * bytes) {
                         if (bytes == 8)
-                            sbt_attn::cp_async8(place(dst, rows, r, byte), a ? a + byte : p.q, a ? 8 : 0);
+                            sbt_attn::cp_async8(place(dst, r, byte), a ? a + byte : p.q, a ? 8 : 0);
                         else if (bytes == 4)
-                            sbt_attn::cp_async4(place(dst, rows, r, byte), a ? a + byte : p.q, a ? 4 : 0);
+                            sbt_attn::cp_async4(place(dst, r, byte), a ? a + byte : p.q, a ? 4 : 0);
                         else
-                            *reinterpret_cast<uint16_t*>(dst_p + (place(0, rows, r, byte))) =
+                            *reinterpret_cast<uint16_t*>(dst_p + (place(0, r, byte))) =
                                 a ? sbt_ld(reinterpret_cast<const uint16_t*>(a + byte)) : (uint16_t)0;
                     }
                 }
@@ -431,26 +512,6 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
         auto signal = [&]() {
             wait_landed(item - landed - 1);
             const int s = landed % NS;
-            if (scan >> s & 1) {
-                // this thread's own pieces of the rows of new positions: infinities and NaN become zero
-                scan &= ~(1u << s);
-                const int from = s_new[s];
-                uint8_t* const base = ring + s * S::SLOT;
-                auto clean = [&](int r, int byte, int bytes) {
-                    if (byte >= row_bytes) return;
-                    uint16_t* const x = reinterpret_cast<uint16_t*>(base + place(0, kTok, r, byte));
-                    for (int i = 0; i < bytes / 2; ++i)
-                        if (special<KIND>(x[i])) x[i] = 0, *s_special = 1;
-                };
-                if (p.copy_kv == 16) {
-                    for (int r = row0; r < kTok; r += STEP)
-                        if (r >= from) clean(r, byte0, 16);
-                } else {
-                    for (int r = lw; r < kTok; r += kLoaders / 32)
-                        for (int byte = lane * p.copy_kv; r >= from && byte < row_bytes; byte += 32 * p.copy_kv)
-                            clean(r, byte, p.copy_kv);
-                }
-            }
             fence_proxy_async_smem();
             if (!(p.withhold && landed == 0)) mbar_arrive(full(s));
             ++landed;
@@ -474,7 +535,7 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
 
         for (Walk w = start; ok && w.u < w.end;) {
             const TreeRow& row = w.row;
-            const int32_t T = w.tiles(), new0 = row.len - row.n;
+            const int32_t T = w.tiles();
             // this lane's two positions of a tile and their pages, -1 where there is none
             int32_t at[2], page[2];
             auto look_up = [&](int32_t it) {
@@ -491,22 +552,14 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
             };
             bool all[2] = {false, false};  // of two tiles: every row is on a page
             // tile it of K or V
-            auto tile = [&](const char* src, int32_t it, bool is_v) {
+            auto tile = [&](const char* src, int32_t it) {
                 const int s = slot_of();
                 if (!ok) return;
-                if (is_v && (w.t + it + 1) * kTok > new0) {
-                    scan |= 1u << s;
-                    if (lane == 0) s_new[s] = max(0, new0 - (w.t + it) * kTok);
-                    __syncwarp();
-                }
                 const int64_t* const o = s_off + (it & 1) * kTok;
                 if (all[it & 1] && p.copy_kv == 16)
                     copy_tile(ring_u32 + s * S::SLOT, src, o);
                 else
-                    copy_rows(ring_u32 + s * S::SLOT, ring + s * S::SLOT, kTok, p.copy_kv, [&](int r) {
-                    const int64_t x = o[r];
-                    return x < 0 ? nullptr : src + x;
-                });
+                    copy_rows(ring_u32 + s * S::SLOT, ring + s * S::SLOT, src, o);
                 sbt_attn::cp_commit();
                 ++item;
             };
@@ -524,38 +577,14 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
                 ++tile_no;
                 __syncwarp();
                 look_up(it + 1);
-                tile(p.k, it, false);
+                tile(p.k, it);
             };
             look_up(0);
-            // queries, once nothing reads the last segment's
-            if (q_uses > 0) {
-                while (landed < item) signal();
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded(q_empty, (q_uses - 1) & 1, p.wait_ns, abort_flag, p.status,
-                                                               kCodeTreeLoad))) {
-                    ok = false;
-                    break;
-                }
-            }
-            const int64_t first = (int64_t)plane * R;
-            for (int m = 0; m < MT; ++m)
-                copy_rows(q_u32 + m * S::Q_TILE, q_s + m * S::Q_TILE, kRows, p.copy_q, [&](int r) -> const char* {
-                    r += m * kRows;
-                    if (r >= row.count) return nullptr;
-                    const uint32_t i = sbt_div(p.group, (uint32_t)(first + r));
-                    const int32_t g = (int32_t)(first + r - (int64_t)i * p.group.d);
-                    return p.q + ((row.q0 + (int64_t)i) * p.ld_q + (int64_t)(w.h * (int32_t)p.group.d + g) * p.ld_qh) * 2;
-                });
-            sbt_attn::cp_commit();
             // K runs two tiles ahead of V, as the products do
             k_tile(0);
             if (ok && T > 1) k_tile(1);
-            if (!ok) break;
-            wait_landed(T > 1 ? 2 : 1);
-            fence_proxy_async_smem();
-            mbar_arrive(q_full);
-            ++q_uses;
             for (int32_t it = 0; ok && it < T; ++it) {
-                tile(p.v, it, true);
+                tile(p.v, it);
                 __syncwarp();  // its offsets make room for those of two tiles on
                 if (ok && it + 2 < T) k_tile(it + 2);
             }
@@ -574,7 +603,7 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
         const uint32_t k_lo = (uint32_t)k_desc, k_hi = (uint32_t)(k_desc >> 32);
         const uint32_t v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32);
         const uint32_t ring_a = smem_u32(ring) >> 4, q_a = k_lo + (smem_u32(q_s) >> 4);
-        int q_uses = 0, q_frees = 0, slot = 0;
+        int q_uses = 0, slot = 0;
         uint32_t full_phase = 0;
         int64_t k_no = 0, pv_no = 0;   // tiles multiplied with Q, and with P
         bool ok = true;
@@ -586,14 +615,13 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
         auto next_slot = [&]() {
             if (++slot == NS) slot = 0, full_phase ^= 1;
         };
-        auto scores = [&](bool last) {
+        auto scores = [&]() {
             const int buf = (int)(k_no & 1);
             if (!wait(full(slot), full_phase)) return;
             const uint32_t b = k_lo + ring_a + slot * (S::SLOT >> 4);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                // this S still holds the P of two tiles ago until its product is done
-                if (k_no >= 2 && !wait(pv_done(m, buf), (uint32_t)((k_no - 2) >> 1) & 1)) return;
+                // this S held the P of two tiles ago: its product was issued before, and one thread's run in order
                 const uint32_t d = tmem + (m * 2 + buf) * kTok;
                 if (leader) {
 #pragma unroll
@@ -609,20 +637,16 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
                 }
                 __syncwarp();
             }
-            if (leader) {
-                tc_commit(empty(slot));
-                if (last) tc_commit(q_empty);
-            }
+            if (leader) tc_commit(empty(slot));
             __syncwarp();
-            if (last) ++q_frees;
             next_slot();
             ++k_no;
         };
         for (Walk w = start; ok && w.u < w.end;) {
             const int32_t T = w.tiles();
             if (!wait(q_full, q_uses++ & 1)) break;
-            scores(T == 1);
-            if (ok && T > 1) scores(T == 2);
+            scores();
+            if (ok && T > 1) scores();
             for (int32_t it = 0; ok && it < T; ++it) {
                 const int buf = (int)(pv_no & 1);
                 if (!wait(full(slot), full_phase)) break;
@@ -644,15 +668,15 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
                 __syncwarp();
                 next_slot();
                 ++pv_no;
-                if (it + 2 < T) scores(it + 3 == T);
+                if (it + 2 < T) scores();
             }
             w.next(T);
         }
-        // every instruction issued has completed once this wait is over (q_empty is not used any more)
-        if (leader) tc_commit(q_empty);
+        // every instruction issued has completed once this wait is over
+        if (leader) tc_commit(all_done);
         __syncwarp();
         const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(q_empty, (uint32_t)(q_frees & 1))) {
+        while (!mbar_try_wait(all_done, 0)) {
             if (globaltimer() - t0 > p.wait_ns) break;
         }
         __syncwarp();
@@ -663,7 +687,8 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
         const uint32_t o_t = tmem + S::O_COL + m * DP + lanes;
         int64_t k_no = 0;
         bool first_seg = true, ok = true;
-        int tile_no = 0;
+        int tile_no = 0, v_slot = 0;
+        uint32_t v_phase = 0;
         for (Walk w = start; ok && w.u < w.end;) {
             const TreeRow row = w.row;
             const int32_t T = w.tiles(), new0 = row.len - row.n, h = w.h, t0 = w.t;
@@ -672,6 +697,30 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
             const int32_t i = mine ? (int32_t)sbt_div(p.group, rr) : 0, g = mine ? (int32_t)(rr - i * p.group.d) : 0;
             const int64_t q_row = row.q0 + i;
             float ref = -CUDART_INF_F, l = 0.f;
+            // ---- this row's query (the last segment's is not read any more); zeros in rows that are not there
+            {
+                const char* const a = p.q + (q_row * p.ld_q + (int64_t)(h * (int32_t)p.group.d + g) * p.ld_qh) * 2;
+                uint8_t* const to = q_s + m * S::Q_TILE + (r & 127) * 128;
+                if (p.q_vec) {
+#pragma unroll
+                    for (int e0 = 0; e0 < DP / 8; e0 += 8) {
+                        uint4 v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            v[e] = mine && (e0 + e) * 8 < p.head_dim ? sbt_ld(reinterpret_cast<const uint4*>(a) + e0 + e)
+                                                                     : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<uint4*>(to + (e0 / 8) * kRows * 128 + ((e ^ (r & 7)) << 4)) = v[e];
+                    }
+                } else {
+                    for (int d = 0; d < DP; ++d)
+                        *reinterpret_cast<uint16_t*>(to + (d >> 6) * kRows * 128 + (((d >> 3 & 7) ^ (r & 7)) << 4) + (d & 7) * 2) =
+                            mine && d < p.head_dim ? sbt_ld(reinterpret_cast<const uint16_t*>(a) + d) : (uint16_t)0;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(q_full);
+            }
             // bit j: this row sees position j of the tile (if it is on a page)
             auto sees = [&](int32_t pos0) -> uint64_t {
                 const int64_t j0 = (int64_t)pos0 - new0;         // the new token at the tile's first position
@@ -691,6 +740,9 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
                 if (left < 64) bits &= left <= 0 ? 0 : (1ull << left) - 1;
                 return bits;
             };
+            // the ring's slots go to K K V K V .. K V V
+            v_slot += T > 1 ? 2 : 1;
+            if (v_slot >= NS) v_slot -= NS, v_phase ^= 1;
             for (int32_t it = 0; it < T; ++it, ++k_no) {
                 const int buf = (int)(k_no & 1);
                 if (!mbar_wait_bounded(s_full(m, buf), (uint32_t)(k_no >> 1) & 1, p.wait_ns, abort_flag, p.status, kCodeTreeSoft))
@@ -770,6 +822,38 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT>::THREADS, TreeShape<KI
                     tmem_st_x32(s_t + 32, hi);
                     tmem_st_wait();
                 }
+                if ((t0 + it + 1) * kTok > new0) {
+                    // the tile holds new positions, or ends past the last: infinities and NaN of the former and all
+                    // of what follows become zero in V
+                    const int s = v_slot;
+                    if (!mbar_wait_bounded(full(s), v_phase, p.wait_ns, abort_flag, p.status, kCodeTreeSoft)) ok = false;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const int32_t pos = (t0 + it) * kTok + (r & 127) / 2;
+                    if (pos >= new0) {
+                        uint8_t* const x = ring + s * S::SLOT + (r & 127) / 2 * 128;
+                        const uint32_t e = KIND == kBF16 ? 0x7F807F80u : 0x7C007C00u;
+                        for (int c = (r & 1) * (DP / 16); c < ((r & 1) + 1) * (DP / 16); ++c) {
+                            uint4* const at = reinterpret_cast<uint4*>(x + (c >> 3) * kTok * 128 + (((c & 7) ^ ((r & 127) / 2 & 7)) << 4));
+                            uint4 v = *at;
+                            uint32_t* const word = reinterpret_cast<uint32_t*>(&v);
+                            bool found = false;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t keep = pos >= row.len ? 0u : __vcmpne2(word[k] & e, e);
+                                found |= (word[k] & ~keep) != 0;
+                                word[k] &= keep;
+                            }
+                            if (found) {
+                                if (pos < row.len) *s_special = 1;
+                                *at = v;
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                v_slot += it + 2 < T ? 2 : 1;  // K of two tiles on follows in the ring
+                if (v_slot >= NS) v_slot -= NS, v_phase ^= 1;
                 tc_fence_before();
                 mbar_arrive(p_ready(m, buf));
             }
@@ -928,10 +1012,10 @@ __global__ void __launch_bounds__(kJoin) k_tree_join(const TreeAttnParams p, int
 // Blocks that the workspace has room for: two an SM of 128 rows, or one of 256.
 inline int64_t part_blocks(const sbt_context* ctx, int mt) { return (int64_t)ctx->sm_count * (mt == 1 ? 2 : 1); }
 
-template <int KIND, int DP, int MT>
-sbt_status enqueue(sbt_context* ctx, TreeAttnParams& p, void* workspace, cudaStream_t stream) {
-    typedef TreeShape<KIND, DP, MT> S;
-    const int resident = std::min<int64_t>(sbt_resident_blocks<k_tree_attention<KIND, DP, MT>>(ctx, S::THREADS, S::SMEM),
+template <int KIND, int DP, int MT, bool TMA>
+sbt_status enqueue(sbt_context* ctx, TreeAttnParams& p, const TreeMaps& maps, void* workspace, cudaStream_t stream) {
+    typedef TreeShape<KIND, DP, MT, TMA> S;
+    const int resident = std::min<int64_t>(sbt_resident_blocks<k_tree_attention<KIND, DP, MT, TMA>>(ctx, S::THREADS, S::SMEM),
                                            part_blocks(ctx, MT));
     p.planes = (int32_t)sbt_cdiv((int64_t)p.max_new * p.group.d, S::R);
     p.ranges = std::max(1, resident / p.planes);
@@ -940,8 +1024,8 @@ sbt_status enqueue(sbt_context* ctx, TreeAttnParams& p, void* workspace, cudaStr
     p.desc = (TreeDesc*)workspace;
     p.part_ml = (float2*)((char*)workspace + sbt_cdiv(blocks * sizeof(TreeDesc), 256) * 256);
     p.part_o = (float*)(p.part_ml + 2 * blocks * S::R);
-    sbt_status st = sbt_cuda_check(sbt_launch_dependent(k_tree_attention<KIND, DP, MT>, dim3((unsigned)blocks),
-                                                        dim3(S::THREADS), S::SMEM, stream, p),
+    sbt_status st = sbt_cuda_check(sbt_launch_dependent(k_tree_attention<KIND, DP, MT, TMA>, dim3((unsigned)blocks),
+                                                        dim3(S::THREADS), S::SMEM, stream, p, maps.k, maps.v),
                                    "paged_tree_attention launch");
     if (st || (st = sbt_after_launch(ctx, "paged_tree_attention"))) return st;
     if (p.ranges == 1) return SBT_OK;  // no line is cut
@@ -954,8 +1038,14 @@ sbt_status enqueue(sbt_context* ctx, TreeAttnParams& p, void* workspace, cudaStr
     return sbt_after_launch(ctx, "paged_tree_attention join");
 }
 
+template <int KIND, int DP, int MT>
+sbt_status enqueue(sbt_context* ctx, TreeAttnParams& p, const TreeMaps& maps, void* workspace, cudaStream_t stream) {
+    return maps.use ? enqueue<KIND, DP, MT, true>(ctx, p, maps, workspace, stream)
+                    : enqueue<KIND, DP, MT, false>(ctx, p, maps, workspace, stream);
+}
+
 // One translation unit each: the head sizes to 128 and those past it.
-template <int KIND> sbt_status narrow(sbt_context* ctx, TreeAttnParams& p, bool two, void* workspace, cudaStream_t stream);
-template <int KIND> sbt_status wide(sbt_context* ctx, TreeAttnParams& p, void* workspace, cudaStream_t stream);
+template <int KIND> sbt_status narrow(sbt_context*, TreeAttnParams&, const TreeMaps&, bool two, void* workspace, cudaStream_t);
+template <int KIND> sbt_status wide(sbt_context*, TreeAttnParams&, const TreeMaps&, void* workspace, cudaStream_t);
 
 }  // namespace sbt_tree

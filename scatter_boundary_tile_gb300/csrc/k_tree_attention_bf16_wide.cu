@@ -4,8 +4,8 @@
 namespace sbt_tree {
 
 template <>
-sbt_status wide<kBF16>(sbt_context* ctx, TreeAttnParams& p, void* ws, cudaStream_t stream) {
-    return p.head_dim <= 192 ? enqueue<kBF16, 192, 1>(ctx, p, ws, stream) : enqueue<kBF16, 256, 1>(ctx, p, ws, stream);
+sbt_status wide<kBF16>(sbt_context* ctx, TreeAttnParams& p, const TreeMaps& maps, void* ws, cudaStream_t stream) {
+    return p.head_dim <= 192 ? enqueue<kBF16, 192, 1>(ctx, p, maps, ws, stream) : enqueue<kBF16, 256, 1>(ctx, p, maps, ws, stream);
 }
 
 }  // namespace sbt_tree
