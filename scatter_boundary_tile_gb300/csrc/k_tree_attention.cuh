@@ -165,7 +165,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
         : "memory");
 }
 
-// 32 lanes x 32 consecutive 32-bit columns, from thread i of the warp to lane (base lane + i).
+// 32 lanes x 8 (or 32) consecutive 32-bit columns, from thread i of the warp to lane (base lane + i).
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -229,6 +234,7 @@ __device__ __forceinline__ bool special(uint16_t x) {
 template <int KIND, int DP, int MT, bool TMA>
 struct TreeShape {
     static constexpr int WARPS = 4 * MT + (TMA ? 1 : kLoaders / 32) + 1, THREADS = 32 * WARPS;
+    // (registers are bounded for whole warps on each of the SM's four partitions)
     static constexpr int BLOCKS = MT == 1 && DP <= 128 ? 2 : 1;
     static constexpr int R = MT * kRows;
     static constexpr uint32_t Q_TILE = kRows * DP * 2, SLOT = kTok * DP * 2;
@@ -247,7 +253,7 @@ struct TreeShape {
 enum : unsigned int { kCodeTreeLoad = 0x10000, kCodeTreeMma = 0x20000, kCodeTreeSoft = 0x40000 };
 
 template <int KIND, int DP, int MT, bool TMA>
-__global__ void __launch_bounds__(TreeShape<KIND, DP, MT, TMA>::THREADS, TreeShape<KIND, DP, MT, TMA>::BLOCKS)
+__global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 * 128, TreeShape<KIND, DP, MT, TMA>::BLOCKS)
     k_tree_attention(const TreeAttnParams p, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map) {
     typedef TreeShape<KIND, DP, MT, TMA> S;
@@ -595,7 +601,11 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT, TMA>::THREADS, TreeSha
     } else if (warp == WARPS - 1) {
         // ------------------------------------------------------------ matrix instructions
         // The whole warp walks and waits, so that what the instructions take is the same for all lanes; one lane issues.
-        const bool leader = lane == 0;
+        auto elected = []() {
+            uint32_t yes;
+            asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+            return yes != 0;
+        };
         const uint32_t type = KIND == kBF16 ? (1u << 7) | (1u << 10) : 0u;
         const uint32_t idesc_s = (1u << 4) | type | ((kTok >> 3) << 17) | ((kRows >> 4) << 24);
         const uint32_t idesc_o = (1u << 4) | type | ((DP >> 3) << 17) | ((kRows >> 4) << 24) | kIdescBMnMajor;
@@ -623,7 +633,7 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT, TMA>::THREADS, TreeSha
             for (int m = 0; m < MT; ++m) {
                 // this S held the P of two tiles ago: its product was issued before, and one thread's run in order
                 const uint32_t d = tmem + (m * 2 + buf) * kTok;
-                if (leader) {
+                if (elected()) {
 #pragma unroll
                     for (int j = 0; j < DP / 16; ++j) {
                         const uint32_t qj = (m * S::Q_TILE + (j / 4) * kRows * 128 + (j % 4) * 32) >> 4;
@@ -637,7 +647,7 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT, TMA>::THREADS, TreeSha
                 }
                 __syncwarp();
             }
-            if (leader) tc_commit(empty(slot));
+            if (elected()) tc_commit(empty(slot));
             __syncwarp();
             next_slot();
             ++k_no;
@@ -655,7 +665,7 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT, TMA>::THREADS, TreeSha
                 for (int m = 0; m < MT; ++m) {
                     if (!wait(p_ready(m, buf), (uint32_t)(pv_no >> 1) & 1)) break;
                     const uint32_t a = tmem + (m * 2 + buf) * kTok, d = tmem + S::O_COL + m * DP;
-                    if (leader) {
+                    if (elected()) {
 #pragma unroll
                         for (int j = 0; j < 2 * kTok / 16; ++j)  // the first numbers, then the second ones
                             mma_ts(d, a + j * 8, b + ((j % 4) * 2048 >> 4), v_hi, idesc_o, j > 0 ? 1u : it > 0);
@@ -664,7 +674,7 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT, TMA>::THREADS, TreeSha
                     __syncwarp();
                 }
                 if (!ok) break;
-                if (leader) tc_commit(empty(slot));
+                if (elected()) tc_commit(empty(slot));
                 __syncwarp();
                 next_slot();
                 ++pv_no;
@@ -673,7 +683,7 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT, TMA>::THREADS, TreeSha
             w.next(T);
         }
         // every instruction issued has completed once this wait is over
-        if (leader) tc_commit(all_done);
+        if (elected()) tc_commit(all_done);
         __syncwarp();
         const uint64_t t0 = globaltimer();
         while (!mbar_try_wait(all_done, 0)) {
@@ -799,27 +809,28 @@ __global__ void __launch_bounds__(TreeShape<KIND, DP, MT, TMA>::THREADS, TreeSha
                     }
                     const float base = ref == -CUDART_INF_F ? 0.f : S::SHIFT - ref;
                     float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-                    uint32_t hi[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float2 y = fma2(make_float2(__uint_as_float(x[j / 16][2 * j % 32]), __uint_as_float(x[j / 16][2 * j % 32 + 1])),
-                                              make_float2(p.scale, p.scale), make_float2(base, base));
-                        float2 e = make_float2(sbt_attn::exp2_fast(y.x), sbt_attn::exp2_fast(y.y));
-                        if (partial) {  // a scale of zero makes NaN of a masked score
-                            e.x = vis >> (2 * j) & 1 ? e.x : 0.f;
-                            e.y = vis >> (2 * j + 1) & 1 ? e.y : 0.f;
+                    for (int c = 0; c < 4; ++c) {  // 16 scores at a time: their registers are free for what comes after
+                        uint32_t hi[8], lo[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int k = c * 16 + 2 * j;
+                            const float2 y = fma2(make_float2(__uint_as_float(x[k / 32][k % 32]), __uint_as_float(x[k / 32][k % 32 + 1])),
+                                                  make_float2(p.scale, p.scale), make_float2(base, base));
+                            float2 e = make_float2(sbt_attn::exp2_fast(y.x), sbt_attn::exp2_fast(y.y));
+                            if (partial) {  // a scale of zero makes NaN of a masked score
+                                e.x = vis >> k & 1 ? e.x : 0.f;
+                                e.y = vis >> (k + 1) & 1 ? e.y : 0.f;
+                            }
+                            sum[j & 1] = add2(sum[j & 1], e);
+                            hi[j] = pack2<KIND>(e.x, e.y);
+                            const float2 d = add2(e, unpack2<KIND>(hi[j] ^ 0x80008000u));
+                            lo[j] = pack2<KIND>(d.x, d.y);
                         }
-                        sum[j & 1] = add2(sum[j & 1], e);
-                        hi[j] = pack2<KIND>(e.x, e.y);
-                        const float2 v = unpack2<KIND>(hi[j] ^ 0x80008000u);
-                        const float2 lo = add2(e, v);
-                        x[j / 16][j % 16] = pack2<KIND>(lo.x, lo.y);  // in the place of scores that are used up
+                        tmem_st_x8(s_t + c * 8, hi);
+                        tmem_st_x8(s_t + 32 + c * 8, lo);
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    tmem_st_x32(s_t, hi);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) hi[j] = x[j / 16][j % 16];
-                    tmem_st_x32(s_t + 32, hi);
                     tmem_st_wait();
                 }
                 if ((t0 + it + 1) * kTok > new0) {
