@@ -81,7 +81,7 @@ struct TreeAttnParams {
     int32_t withhold;                          // test hook: no block signals its first tile
     TreeDesc* desc;
     float2* part_ml;                           // [2 blocks][MT * 128]
-    float* part_o;                             // [2 blocks][MT * 128][DP]
+    float4* part_o;                            // [2 blocks][DP / 4][MT * 128]
 };
 
 // Keys and values as tensors of pages, heads, slots and elements.
@@ -233,7 +233,7 @@ __device__ __forceinline__ bool special(uint16_t x) {
 
 template <int KIND, int DP, int MT, bool TMA>
 struct TreeShape {
-    static constexpr int WARPS = 4 * MT + (TMA ? 1 : kLoaders / 32) + 1, THREADS = 32 * WARPS;
+    static constexpr int WARPS = 4 * MT + (TMA ? 1 : kLoaders / 32) + MT, THREADS = 32 * WARPS;
     // (registers are bounded for whole warps on each of the SM's four partitions)
     static constexpr int BLOCKS = MT == 1 && DP <= 128 ? 2 : 1;
     static constexpr int R = MT * kRows;
@@ -243,7 +243,7 @@ struct TreeShape {
     static constexpr size_t SMEM = 1024 + 512 + MT * Q_TILE + SLOTS * SLOT;
     static constexpr uint32_t O_COL = MT * 2 * kTok;            // S (and P): [MT][2][64], then O: [MT][DP]
     static constexpr uint32_t COLS = O_COL + MT * DP <= 256 ? 256 : 512;
-    static constexpr int BARS = 2 * SLOTS + 2 + 6 * MT;
+    static constexpr int BARS = 2 * SLOTS + 8 * MT;
     static constexpr float SLACK = KIND == kF16 ? 6.f : 8.f;    // see the head of the file
     static constexpr float SHIFT = KIND == kF16 ? 9.f : 0.f;
     static_assert(SLOTS >= 4, "K two tiles ahead of V, and two more on their way");
@@ -273,19 +273,21 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (NS + s); };
-    const uint32_t q_full = bar0 + 8u * (2 * NS), all_done = q_full + 8;
-    auto s_full = [&](int m, int buf) { return all_done + 8u + 8u * (6 * m + buf); };
-    auto p_ready = [&](int m, int buf) { return all_done + 8u + 8u * (6 * m + 2 + buf); };
+    auto q_full = [&](int m) { return bar0 + 8u * (2 * NS + 8 * m); };
+    auto all_done = [&](int m) { return q_full(m) + 8u; };
+    auto s_full = [&](int m, int buf) { return q_full(m) + 8u * (2 + buf); };
+    auto p_ready = [&](int m, int buf) { return q_full(m) + 8u * (4 + buf); };
     // one for each of two tiles: a wait for tile k comes after tile k - 2 is done and before k + 2 can be, so that
     // the parity names the phase
-    auto pv_done = [&](int m, int buf) { return all_done + 8u + 8u * (6 * m + 4 + buf); };
+    auto pv_done = [&](int m, int buf) { return q_full(m) + 8u * (6 + buf); };
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x / 32), 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < NS; ++s) mbar_init(full(s), TMA ? 1 : kLoaders), mbar_init(empty(s), 1);
-        mbar_init(q_full, R), mbar_init(all_done, 1);
-        for (int m = 0; m < MT; ++m)
+        for (int s = 0; s < NS; ++s) mbar_init(full(s), TMA ? 1 : kLoaders), mbar_init(empty(s), MT);
+        for (int m = 0; m < MT; ++m) {
+            mbar_init(q_full(m), kRows), mbar_init(all_done(m), 1);
             for (int b = 0; b < 2; ++b) mbar_init(s_full(m, b), 1), mbar_init(p_ready(m, b), kRows), mbar_init(pv_done(m, b), 1);
+        }
         *abort_flag = 0;
         *s_special = 0;
         fence_mbar_init();
@@ -311,9 +313,13 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
         const int32_t n = row_of(p, b, plane, R).tiles;
         return n ? (int64_t)(n + kLineCost) * p.kv_heads : 0;
     };
-    int64_t total = 0;
-    for (uint32_t b = threadIdx.x; b < (uint32_t)p.batch; b += THREADS) total += places((int32_t)b);
-    {
+    const bool one_step = p.batch <= THREADS;  // every thread holds its own entry's places
+    int64_t total = 0, at = 0, mine_places = 0;
+    if (one_step) {
+        if ((int32_t)threadIdx.x < p.batch) mine_places = places(threadIdx.x);
+        at = sbt_attn::block_scan<WARPS>(mine_places, &total, s_warp);
+    } else {
+        for (uint32_t b = threadIdx.x; b < (uint32_t)p.batch; b += THREADS) total += places((int32_t)b);
         int64_t sum;
         sbt_attn::block_scan<WARPS>(total, &sum, s_warp);
         total = sum;
@@ -327,9 +333,11 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
     {
         int64_t before = 0;
         for (uint32_t b0 = 0; b0 < (uint32_t)p.batch && before <= u0; b0 += THREADS) {
-            const uint32_t b = b0 + threadIdx.x;
-            int64_t sum;
-            const int64_t at = before + sbt_attn::block_scan<WARPS>(b < (uint32_t)p.batch ? places((int32_t)b) : 0, &sum, s_warp);
+            int64_t sum = total;
+            if (!one_step) {
+                const uint32_t b = b0 + threadIdx.x;
+                at = before + sbt_attn::block_scan<WARPS>(b < (uint32_t)p.batch ? places((int32_t)b) : 0, &sum, s_warp);
+            }
             s_first[threadIdx.x] = at;
             __syncthreads();
             if (before <= u0 && u0 < before + sum) {
@@ -435,7 +443,7 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
             }
         }
         __syncwarp();
-    } else if (!TMA && warp >= 4 * MT && warp < WARPS - 1) {
+    } else if (!TMA && warp >= 4 * MT && warp < WARPS - MT) {
         // ------------------------------------------------------------ copies by lanes
         const int tid = threadIdx.x - 4 * MT * 32;
         int item = 0, landed = 0;          // tiles begun, and signalled as landed
@@ -598,8 +606,9 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
         }
         while (ok && landed < item) signal();
         sbt_attn::cp_wait<0>();
-    } else if (warp == WARPS - 1) {
-        // ------------------------------------------------------------ matrix instructions
+    } else if (warp >= WARPS - MT) {
+        // ------------------------------------------------------------ matrix instructions: a warp for each 128 rows
+        const int m = warp - (WARPS - MT);
         // The whole warp walks and waits, so that what the instructions take is the same for all lanes; one lane issues.
         auto elected = []() {
             uint32_t yes;
@@ -612,10 +621,10 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
         const uint64_t k_desc = smem_desc_sw128(0), v_desc = smem_desc_mn_sw128(0, kTok * 128);
         const uint32_t k_lo = (uint32_t)k_desc, k_hi = (uint32_t)(k_desc >> 32);
         const uint32_t v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32);
-        const uint32_t ring_a = smem_u32(ring) >> 4, q_a = k_lo + (smem_u32(q_s) >> 4);
+        const uint32_t ring_a = smem_u32(ring) >> 4, q_a = k_lo + ((smem_u32(q_s) + m * S::Q_TILE) >> 4);
         int q_uses = 0, slot = 0;
         uint32_t full_phase = 0;
-        int64_t k_no = 0, pv_no = 0;   // tiles multiplied with Q, and with P
+        int64_t k_no = 0;              // tiles multiplied with P
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, p.wait_ns, abort_flag, p.status, kCodeTreeMma));
@@ -625,68 +634,54 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
         auto next_slot = [&]() {
             if (++slot == NS) slot = 0, full_phase ^= 1;
         };
-        auto scores = [&]() {
-            const int buf = (int)(k_no & 1);
-            if (!wait(full(slot), full_phase)) return;
-            const uint32_t b = k_lo + ring_a + slot * (S::SLOT >> 4);
+        // S of tile k into buffer k & 1, from the K in `slot`.  The buffer held the P of two tiles ago: that product was
+        // issued before, and one thread's instructions run in order.
+        auto scores = [&](int64_t k) {
+            const uint32_t b = k_lo + ring_a + slot * (S::SLOT >> 4), d = tmem + (m * 2 + (int)(k & 1)) * kTok;
+            if (elected()) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                // this S held the P of two tiles ago: its product was issued before, and one thread's run in order
-                const uint32_t d = tmem + (m * 2 + buf) * kTok;
-                if (elected()) {
-#pragma unroll
-                    for (int j = 0; j < DP / 16; ++j) {
-                        const uint32_t qj = (m * S::Q_TILE + (j / 4) * kRows * 128 + (j % 4) * 32) >> 4;
-                        const uint32_t kj = ((j / 4) * kTok * 128 + (j % 4) * 32) >> 4;
-                        if (j == 0)
-                            mma_ss<false>(d, q_a + qj, b + kj, k_hi, idesc_s);
-                        else
-                            mma_ss<true>(d, q_a + qj, b + kj, k_hi, idesc_s);
-                    }
-                    tc_commit(s_full(m, buf));
+                for (int j = 0; j < DP / 16; ++j) {
+                    const uint32_t qj = ((j / 4) * kRows * 128 + (j % 4) * 32) >> 4;
+                    const uint32_t kj = ((j / 4) * kTok * 128 + (j % 4) * 32) >> 4;
+                    if (j == 0)
+                        mma_ss<false>(d, q_a + qj, b + kj, k_hi, idesc_s);
+                    else
+                        mma_ss<true>(d, q_a + qj, b + kj, k_hi, idesc_s);
                 }
-                __syncwarp();
+                tc_commit(s_full(m, (int)(k & 1)));
+                tc_commit(empty(slot));
             }
-            if (elected()) tc_commit(empty(slot));
             __syncwarp();
             next_slot();
-            ++k_no;
         };
         for (Walk w = start; ok && w.u < w.end;) {
             const int32_t T = w.tiles();
-            if (!wait(q_full, q_uses++ & 1)) break;
-            scores();
-            if (ok && T > 1) scores();
-            for (int32_t it = 0; ok && it < T; ++it) {
-                const int buf = (int)(pv_no & 1);
+            if (!wait(q_full(m), q_uses++ & 1)) break;
+            for (int i = 0; i < min(T, 2) && wait(full(slot), full_phase); ++i) scores(k_no + i);
+            for (int32_t it = 0; ok && it < T; ++it, ++k_no) {
+                const int buf = (int)(k_no & 1);
                 if (!wait(full(slot), full_phase)) break;
+                if (!wait(p_ready(m, buf), (uint32_t)(k_no >> 1) & 1)) break;
+                const uint32_t a = tmem + (m * 2 + buf) * kTok, d = tmem + S::O_COL + m * DP;
                 const uint32_t b = v_lo + ring_a + slot * (S::SLOT >> 4);
+                if (elected()) {
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    if (!wait(p_ready(m, buf), (uint32_t)(pv_no >> 1) & 1)) break;
-                    const uint32_t a = tmem + (m * 2 + buf) * kTok, d = tmem + S::O_COL + m * DP;
-                    if (elected()) {
-#pragma unroll
-                        for (int j = 0; j < 2 * kTok / 16; ++j)  // the first numbers, then the second ones
-                            mma_ts(d, a + j * 8, b + ((j % 4) * 2048 >> 4), v_hi, idesc_o, j > 0 ? 1u : it > 0);
-                        tc_commit(pv_done(m, buf));
-                    }
-                    __syncwarp();
+                    for (int j = 0; j < 2 * kTok / 16; ++j)  // the first numbers, then the second ones
+                        mma_ts(d, a + j * 8, b + ((j % 4) * 2048 >> 4), v_hi, idesc_o, j > 0 ? 1u : it > 0);
+                    tc_commit(pv_done(m, buf));
+                    tc_commit(empty(slot));
                 }
-                if (!ok) break;
-                if (elected()) tc_commit(empty(slot));
                 __syncwarp();
                 next_slot();
-                ++pv_no;
-                if (it + 2 < T) scores();
+                if (it + 2 < T && wait(full(slot), full_phase)) scores(k_no + 2);
             }
             w.next(T);
         }
         // every instruction issued has completed once this wait is over
-        if (elected()) tc_commit(all_done);
+        if (elected()) tc_commit(all_done(m));
         __syncwarp();
         const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(all_done, 0)) {
+        while (!mbar_try_wait(all_done(m), 0)) {
             if (globaltimer() - t0 > p.wait_ns) break;
         }
         __syncwarp();
@@ -729,7 +724,7 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
                             mine && d < p.head_dim ? sbt_ld(reinterpret_cast<const uint16_t*>(a) + d) : (uint16_t)0;
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(q_full);
+                mbar_arrive(q_full(m));
             }
             // bit j: this row sees position j of the tile (if it is on a page)
             auto sees = [&](int32_t pos0) -> uint64_t {
@@ -912,10 +907,10 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
                         }
                     }
                     if (!whole) {
-                        float4* const to = reinterpret_cast<float4*>(p.part_o + (slot * R + r) * DP + d);
+                        float4* const to = p.part_o + (slot * (DP / 4) + d / 4) * R + r;
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            to[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                            to[j * R] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
                                                 __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
                     } else {
                         uint16_t* const to = reinterpret_cast<uint16_t*>(p.out) + q_row * p.ld_out + qh * p.ld_oh + d;
@@ -981,43 +976,59 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
     }
 }
 
-// Adds the parts of cut lines in the order of the line: a block takes kJoin / (DP
-// / 4) rows of one of them, a thread four elements.
+// Adds the parts of cut lines in the order of the line.  A block takes 32 rows, a lane each, of one of them, and its
+// eight warps 8 / groups vectors of four elements, whose parts `groups` warps share out and join in shared memory.
 template <int KIND, int DP, int MT>
-__global__ void __launch_bounds__(kJoin) k_tree_join(const TreeAttnParams p, int32_t pieces) {
-    constexpr int R = MT * kRows, LANES = DP / 4, PER = kJoin / LANES;
+__global__ void __launch_bounds__(kJoin) k_tree_join(const TreeAttnParams p, int32_t pieces, int32_t groups) {
+    constexpr int R = MT * kRows;
+    __shared__ float4 s_o[kJoin];
+    __shared__ float s_l[kJoin];
     griddep_wait();
     const TreeDesc e = p.desc[blockIdx.x / pieces];
     if (!e.valid) return;
     const TreeRow row = row_of(p, e.b, e.plane, R);
-    const int r = (blockIdx.x % pieces) * PER + threadIdx.x / LANES, d = threadIdx.x % LANES * 4;
-    if (threadIdx.x >= PER * LANES || r >= row.count) return;
-    auto slot = [&](int32_t i) -> int64_t {
-        return 2 * ((int64_t)(e.first + i) * p.planes + e.plane) + (i == 0 ? e.first_slot : 0);
-    };
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quads = kJoin / 32 / groups, rest = blockIdx.x % pieces;
+    const int r0 = rest / (DP / 4 / quads) * 32, quad = rest % (DP / 4 / quads) * quads + warp / groups, group = warp % groups;
+    if (r0 >= row.count) return;
+    const int r = min(r0 + lane, row.count - 1);
+    const int64_t step = 2ll * p.planes;                      // slots between a line's parts
+    const int64_t slot0 = 2 * ((int64_t)e.first * p.planes + e.plane);
+    auto slot = [&](int32_t i) -> int64_t { return slot0 + i * step + (i == 0 ? e.first_slot : 0); };
     const int32_t n = e.last - e.first + 1;
     float top = -CUDART_INF_F;
-#pragma unroll 4
+#pragma unroll 8
     for (int32_t i = 0; i < n; ++i) top = fmaxf(top, sbt_ld(p.part_ml + slot(i) * R + r).x);
     const float ts = top == -CUDART_INF_F ? 0.f : top;
     float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int32_t i = 0; i < n; ++i) {
+    for (int32_t i = group; i < n; i += groups) {
         const float2 ml = sbt_ld(p.part_ml + slot(i) * R + r);
-        const float4 x = sbt_ld(reinterpret_cast<const float4*>(p.part_o + (slot(i) * R + r) * DP + d));
+        const float4 x = sbt_ld(p.part_o + (slot(i) * (DP / 4) + quad) * R + r);
         const float a = sbt_attn::exp2_fast(ml.x - ts);
         l += ml.y * a;
         o[0] += x.x * a, o[1] += x.y * a, o[2] += x.z * a, o[3] += x.w * a;
     }
+    if (groups > 1) {
+        s_o[threadIdx.x] = make_float4(o[0], o[1], o[2], o[3]);
+        s_l[threadIdx.x] = l;
+        __syncthreads();
+        if (group) return;
+        for (int i = 1; i < groups; ++i) {
+            const float4 x = s_o[threadIdx.x + 32 * i];
+            l += s_l[threadIdx.x + 32 * i];
+            o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w;
+        }
+    }
+    if (r0 + lane >= row.count) return;
     const uint32_t rr = (uint32_t)((int64_t)e.plane * R + r), i = sbt_div(p.group, rr);
     const int32_t qh = e.h * (int32_t)p.group.d + (int32_t)(rr - i * p.group.d);
     const int64_t q_row = row.q0 + (int64_t)i;
     const float inv = sbt_attn::inverse(l);
-    uint16_t* const to = reinterpret_cast<uint16_t*>(p.out) + q_row * p.ld_out + qh * p.ld_oh;
+    uint16_t* const to = reinterpret_cast<uint16_t*>(p.out) + q_row * p.ld_out + qh * p.ld_oh + quad * 4;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        if (d + j < p.head_dim) to[d + j] = Num<KIND>::put(o[j] * inv);
-    if (d == 0 && p.lse) p.lse[q_row * p.q_heads + qh] = sbt_attn::log_sum(top, l);
+        if (quad * 4 + j < p.head_dim) to[j] = Num<KIND>::put(o[j] * inv);
+    if (quad == 0 && p.lse) p.lse[q_row * p.q_heads + qh] = sbt_attn::log_sum(top, l);
 }
 
 // Blocks that the workspace has room for: two an SM of 128 rows, or one of 256.
@@ -1026,24 +1037,28 @@ inline int64_t part_blocks(const sbt_context* ctx, int mt) { return (int64_t)ctx
 template <int KIND, int DP, int MT, bool TMA>
 sbt_status enqueue(sbt_context* ctx, TreeAttnParams& p, const TreeMaps& maps, void* workspace, cudaStream_t stream) {
     typedef TreeShape<KIND, DP, MT, TMA> S;
-    const int resident = std::min<int64_t>(sbt_resident_blocks<k_tree_attention<KIND, DP, MT, TMA>>(ctx, S::THREADS, S::SMEM),
-                                           part_blocks(ctx, MT));
+    // (the runtime's count of resident blocks is one for any kernel that allocates TMEM)
+    sbt_resident_blocks<k_tree_attention<KIND, DP, MT, TMA>>(ctx, S::THREADS, S::SMEM);
+    const int resident = ctx->sm_count * S::BLOCKS;
     p.planes = (int32_t)sbt_cdiv((int64_t)p.max_new * p.group.d, S::R);
     p.ranges = std::max(1, resident / p.planes);
     const int64_t blocks = (int64_t)p.ranges * p.planes, lines = (int64_t)p.batch * p.kv_heads * p.planes;
     p.desc_by_line = lines <= blocks;
     p.desc = (TreeDesc*)workspace;
     p.part_ml = (float2*)((char*)workspace + sbt_cdiv(blocks * sizeof(TreeDesc), 256) * 256);
-    p.part_o = (float*)(p.part_ml + 2 * blocks * S::R);
+    p.part_o = (float4*)(p.part_ml + 2 * blocks * S::R);
     sbt_status st = sbt_cuda_check(sbt_launch_dependent(k_tree_attention<KIND, DP, MT, TMA>, dim3((unsigned)blocks),
                                                         dim3(S::THREADS), S::SMEM, stream, p, maps.k, maps.v),
                                    "paged_tree_attention launch");
     if (st || (st = sbt_after_launch(ctx, "paged_tree_attention"))) return st;
     if (p.ranges == 1) return SBT_OK;  // no line is cut
     const int64_t n_desc = p.desc_by_line ? lines : blocks;
-    const int32_t pieces = (int32_t)sbt_cdiv(std::min<int64_t>(S::R, (int64_t)p.max_new * p.group.d), kJoin / (DP / 4));
+    // Few lines are cut into many parts: four warps share a vector's; many lines into two or three.
+    const int64_t row_groups = sbt_cdiv(std::min<int64_t>(S::R, (int64_t)p.max_new * p.group.d), 32);
+    const int32_t groups = n_desc * row_groups * (DP / 32) < 4 * ctx->sm_count ? 4 : 1;
+    const int32_t pieces = (int32_t)(row_groups * (DP / 4) / (kJoin / 32 / groups));
     st = sbt_cuda_check(sbt_launch_dependent(k_tree_join<KIND, DP, MT>, dim3((unsigned)(n_desc * pieces)), dim3(kJoin), 0,
-                                             stream, p, pieces),
+                                             stream, p, pieces, groups),
                         "paged_tree_attention join launch");
     if (st) return st;
     return sbt_after_launch(ctx, "paged_tree_attention join");
