@@ -46,10 +46,8 @@ size_t sbt_tree_attention_workspace_bytes(const sbt_context* ctx, int32_t max_ne
     const int dp = padded(head_dim);
     const int64_t rows = (int64_t)max_new * (q_heads / kv_heads);
     const int mt = two_tiles(rows, dp) ? 2 : 1;
-    // at most this many blocks with cut lines; more planes than that have a block each and cut nothing
-    const int64_t R = (int64_t)mt * kRows, blocks = std::max(part_blocks(ctx, mt), sbt_cdiv(rows, R));
-    const int64_t parts = part_blocks(ctx, mt);
-    return (size_t)(sbt_cdiv(blocks * sizeof(TreeDesc), 256) * 256 + 2 * parts * R * (sizeof(float2) + dp * sizeof(float)));
+    const int64_t R = (int64_t)mt * kRows, blocks = part_blocks(ctx, mt);
+    return (size_t)(sbt_cdiv(blocks * sizeof(TreeDesc), 256) * 256 + 2 * blocks * R * (sizeof(float2) + dp * sizeof(float)));
 }
 
 sbt_status sbt_launch_tree_attention(sbt_context* ctx, sbt_dtype dtype, const SbtHeadRows& q, int32_t rows,
@@ -70,7 +68,8 @@ sbt_status sbt_launch_tree_attention(sbt_context* ctx, sbt_dtype dtype, const Sb
     p.max_len = (int32_t)std::min<int64_t>((int64_t)map->max_pages * map->page_size, INT32_MAX - 1023);
     p.group = sbt_make_fastdiv((uint32_t)(q_heads / cache->heads));
     p.page_size = sbt_make_fastdiv((uint32_t)map->page_size);
-    p.scale = fabsf(scale) * 1.4426950408889634f, p.negate = scale < 0.f;
+    // (a scale of zero would make NaN of a masked score of minus infinity; 2^-126 of any finite one is as good as zero)
+    p.scale = std::max(fabsf(scale) * 1.4426950408889634f, 0x1p-126f), p.negate = scale < 0.f ? 0x80008000u : 0u;
     p.q_vec = piece(q.p, q.ld, q.ldh, 0, p.head_dim) == 16;
     p.copy_kv = std::min(piece(p.k, p.ld_page, p.ld_slot, p.ld_head, p.head_dim), piece(p.v, 0, 0, 0, p.head_dim));
     p.out_vec = piece(out.p, out.ld, out.ldh, 0, p.head_dim) == 16;

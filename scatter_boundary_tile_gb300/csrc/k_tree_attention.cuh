@@ -69,13 +69,12 @@ struct TreeAttnParams {
     int64_t ld_page, ld_slot, ld_head;         // elements
     int64_t ld_table, n_pages, ld_mask;
     int32_t rows, batch, max_new, q_heads, kv_heads, n_seq, head_dim, max_len;
-    int32_t planes;                            // tiles of MT * 128 rows that an entry may need
-    int32_t ranges;                            // blocks per plane
+    int32_t planes;                            // MT * 128 rows each that an entry may need
     int32_t copy_kv, q_vec, out_vec;           // bytes of a copy by lanes; q and out as 16-byte vectors
     int32_t desc_by_line;                      // descriptors by line (there are no more lines than blocks), else by block
     sbt_fastdiv group, page_size;
-    float scale;                               // |scale| log2 e
-    int32_t negate;
+    float scale;                               // |scale| log2 e, not zero
+    uint32_t negate;                           // sign bits of two numbers where the scale is negative: on the queries
     unsigned int* status;
     uint64_t wait_ns;
     int32_t withhold;                          // test hook: no block signals its first tile
@@ -90,42 +89,77 @@ struct TreeMaps {
     bool use;
 };
 
-// Entry b's rows of one plane: tokens are the rows q0 .. q0 + n - 1 of q, the last n of len positions.
+// Entry b (its tokens are the rows q0 .. q0 + n - 1 of q, the last n of len positions; n = 0: none, or left out) and
+// one plane of its rows.
 struct TreeRow {
-    int32_t b, q0, n, len, seq, tiles;
-    int32_t count;                             // query rows of the plane
+    int32_t b, q0, n, len, seq;
+    int32_t plane, count, tiles;               // query rows, and tiles they see
 };
 
-__device__ __forceinline__ TreeRow row_of(const TreeAttnParams& p, int32_t b, int32_t plane, int32_t plane_rows) {
-    TreeRow r = {b, 0, 0, 0, -1, 0, 0};
-    const int32_t c0 = sbt_ld(p.cu + b), c1 = sbt_ld(p.cu + b + 1);
-    const int64_t n = (int64_t)c1 - c0;
-    if (c0 < 0 || c1 > p.rows || n <= 0 || n > p.max_new) return r;
-    const int64_t all = n * p.group.d, first = (int64_t)plane * plane_rows;
-    if (first >= all) return r;
-    r.q0 = c0, r.n = (int32_t)n;
-    r.count = (int32_t)min((int64_t)plane_rows, all - first);
-    const int32_t s = p.seq ? sbt_ld(p.seq + b) : b;
-    if (s < 0 || s >= p.n_seq) return r;
-    r.seq = s;
-    r.len = min(max(sbt_ld(p.lens + s), 0), p.max_len);
+__device__ __forceinline__ void set_plane(const TreeAttnParams& p, TreeRow& r, int32_t plane, int32_t R) {
+    const int64_t all = r.n * (int64_t)p.group.d, first = (int64_t)plane * R;
+    r.plane = plane;
+    r.count = (int32_t)max((int64_t)0, min((int64_t)R, all - first));
+    r.tiles = 0;
+    if (r.count == 0 || r.seq < 0) return;
     // without a mask no row of the plane sees past its last token
     const int32_t last = (int32_t)sbt_div(p.group, (uint32_t)(first + r.count - 1));
     const int32_t hi = p.mask ? r.len : r.len - r.n + last + 1;
     r.tiles = hi > 0 ? (hi + kTok - 1) / kTok : 0;
+}
+
+__device__ __forceinline__ TreeRow row_of(const TreeAttnParams& p, int32_t b, int32_t R) {
+    TreeRow r = {b, 0, 0, 0, -1, 0, 0, 0};
+    const int32_t c0 = sbt_ld(p.cu + b), c1 = sbt_ld(p.cu + b + 1), s = p.seq ? sbt_ld(p.seq + b) : b;
+    const bool held = s >= 0 && s < p.n_seq;
+    const int32_t len = held ? sbt_ld(p.lens + s) : 0;         // on its way beside cu
+    const int64_t n = (int64_t)c1 - c0;
+    if (c0 < 0 || c1 > p.rows || n <= 0 || n > p.max_new) return r;
+    r.q0 = c0, r.n = (int32_t)n;
+    if (held) r.seq = s, r.len = min(max(len, 0), p.max_len);
+    set_plane(p, r, 0, R);
     return r;
+}
+
+// Planes that an entry's rows fill.
+__device__ __forceinline__ int32_t planes_of(const TreeAttnParams& p, const TreeRow& r, int32_t R) {
+    return (int32_t)((r.n * (int64_t)p.group.d + R - 1) / R);
+}
+
+// Places of one head's lines, a line for every plane that sees anything.
+__device__ __forceinline__ int64_t head_places(const TreeAttnParams& p, TreeRow r, int32_t R) {
+    int64_t sum = 0;
+    for (int32_t i = 0; i < planes_of(p, r, R); ++i) {
+        set_plane(p, r, i, R);
+        if (r.tiles) sum += r.tiles + kLineCost;
+    }
+    return sum;
 }
 
 // The lines of a range, one after another; every role walks it by itself.
 struct Walk {
     const TreeAttnParams& p;
-    int32_t plane, plane_rows;
+    int32_t R;
     TreeRow row;
     int32_t h, t;          // key-value head; first tile of the segment
     int64_t u, end;        // its place; the range's end
 
     // The tiles of the segment at hand.
     __device__ __forceinline__ int32_t tiles() const { return (int32_t)min((int64_t)(row.tiles - t), end - u); }
+    // The first line from here on (plane, head, entry) that sees anything.
+    __device__ __forceinline__ void find() {
+        while (true) {
+            for (const int32_t n = planes_of(p, row, R); row.plane < n; set_plane(p, row, row.plane + 1, R))
+                if (row.tiles) return;
+            if (row.seq >= 0 && row.n && ++h < p.kv_heads) {
+                set_plane(p, row, 0, R);
+                continue;
+            }
+            h = 0;
+            if (row.b + 1 >= p.batch) return;
+            row = row_of(p, row.b + 1, R);
+        }
+    }
     __device__ __forceinline__ void next(int32_t done) {
         u += done;
         t += done;
@@ -133,12 +167,8 @@ struct Walk {
         u += kLineCost;
         t = 0;
         if (u >= end) return;
-        if (++h < p.kv_heads) return;
-        h = 0;
-        for (int32_t b = row.b + 1; b < p.batch; ++b) {
-            row = row_of(p, b, plane, plane_rows);
-            if (row.tiles) break;
-        }
+        set_plane(p, row, row.plane + 1, R);
+        find();
     }
 };
 
@@ -237,6 +267,7 @@ struct TreeShape {
     // (registers are bounded for whole warps on each of the SM's four partitions)
     static constexpr int BLOCKS = MT == 1 && DP <= 128 ? 2 : 1;
     static constexpr int R = MT * kRows;
+    static constexpr int TERMS = MT == 1 ? 2 : 1;               // 16-bit numbers of a probability
     static constexpr uint32_t Q_TILE = kRows * DP * 2, SLOT = kTok * DP * 2;
     static constexpr uint32_t MOST = (BLOCKS == 2 ? 113 : 227) * 1024 - 8192 - 1536 - MT * Q_TILE;
     static constexpr int SLOTS = MOST / SLOT < 8 ? MOST / SLOT : 8;
@@ -261,6 +292,7 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
     extern __shared__ uint8_t smem_raw[];
     __shared__ int64_t s_warp[WARPS];
     __shared__ int64_t s_first[THREADS];
+    __shared__ TreeRow s_row;
     __shared__ int64_t s_offsets[TMA ? 1 : kLoaders / 32][2 * kTok];
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* const q_s = smem;
@@ -307,24 +339,22 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
     const uint32_t tmem = *tmem_slot;
     griddep_wait();
 
-    // ---- the line of this plane, and this block's range of it
-    const int32_t plane = blockIdx.x % p.planes, c = blockIdx.x / p.planes;
-    auto places = [&](int32_t b) {
-        const int32_t n = row_of(p, b, plane, R).tiles;
-        return n ? (int64_t)(n + kLineCost) * p.kv_heads : 0;
-    };
+    // ---- the line, and this block's range of it
+    const int32_t c = blockIdx.x;
+    auto places = [&](int32_t b, TreeRow& r) { return head_places(p, r = row_of(p, b, R), R) * p.kv_heads; };
     const bool one_step = p.batch <= THREADS;  // every thread holds its own entry's places
     int64_t total = 0, at = 0, mine_places = 0;
+    TreeRow my_row;
     if (one_step) {
-        if ((int32_t)threadIdx.x < p.batch) mine_places = places(threadIdx.x);
+        if ((int32_t)threadIdx.x < p.batch) mine_places = places(threadIdx.x, my_row);
         at = sbt_attn::block_scan<WARPS>(mine_places, &total, s_warp);
     } else {
-        for (uint32_t b = threadIdx.x; b < (uint32_t)p.batch; b += THREADS) total += places((int32_t)b);
+        for (uint32_t b = threadIdx.x; b < (uint32_t)p.batch; b += THREADS) total += places((int32_t)b, my_row);
         int64_t sum;
         sbt_attn::block_scan<WARPS>(total, &sum, s_warp);
         total = sum;
     }
-    const int64_t G = min(total, (int64_t)p.ranges);
+    const int64_t G = min(total, (int64_t)gridDim.x);
     bool idle = c >= G;
     const Line line(total, G > 0 ? G : 1);
     const int64_t u0 = idle ? total : line.start(c), u1 = idle ? total : line.start(c + 1);
@@ -336,7 +366,7 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
             int64_t sum = total;
             if (!one_step) {
                 const uint32_t b = b0 + threadIdx.x;
-                at = before + sbt_attn::block_scan<WARPS>(b < (uint32_t)p.batch ? places((int32_t)b) : 0, &sum, s_warp);
+                at = before + sbt_attn::block_scan<WARPS>(b < (uint32_t)p.batch ? places((int32_t)b, my_row) : 0, &sum, s_warp);
             }
             s_first[threadIdx.x] = at;
             __syncthreads();
@@ -356,12 +386,20 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
     }
     if (!p.desc_by_line && threadIdx.x == 0) p.desc[blockIdx.x].valid = 0;
 
-    Walk start = {p, plane, R, {}, 0, 0, 0, u1};
+    if (one_step && !idle && (int32_t)threadIdx.x == b_first) s_row = my_row;
+    __syncthreads();
+    Walk start = {p, R, {}, 0, 0, 0, u1};
     if (!idle) {
-        start.row = row_of(p, b_first, plane, R);
-        const int64_t width = start.row.tiles + kLineCost;
+        start.row = one_step ? s_row : row_of(p, b_first, R);
+        set_plane(p, start.row, 0, R);
+        const int64_t width = head_places(p, start.row, R);
         start.h = (int32_t)sbt_attn::divide(u0 - u_first, width);
-        const int64_t line_u = u_first + start.h * width + kLineCost;
+        int64_t line_u = u_first + start.h * width;              // of the line that holds u0
+        while (start.row.tiles == 0 || u0 >= line_u + start.row.tiles + kLineCost) {
+            if (start.row.tiles) line_u += start.row.tiles + kLineCost;
+            set_plane(p, start.row, start.row.plane + 1, R);
+        }
+        line_u += kLineCost;
         start.u = u0 > line_u ? u0 : line_u;
         start.t = (int32_t)(start.u - line_u);
         idle = start.u >= u1;  // nothing but a line's empty places
@@ -660,20 +698,22 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
             for (int i = 0; i < min(T, 2) && wait(full(slot), full_phase); ++i) scores(k_no + i);
             for (int32_t it = 0; ok && it < T; ++it, ++k_no) {
                 const int buf = (int)(k_no & 1);
+                // V, and the K of two tiles on, which follows it in the ring; then P, which both wait for
                 if (!wait(full(slot), full_phase)) break;
+                if (it + 2 < T && !wait(full(slot + 1 == NS ? 0 : slot + 1), slot + 1 == NS ? full_phase ^ 1 : full_phase)) break;
                 if (!wait(p_ready(m, buf), (uint32_t)(k_no >> 1) & 1)) break;
                 const uint32_t a = tmem + (m * 2 + buf) * kTok, d = tmem + S::O_COL + m * DP;
                 const uint32_t b = v_lo + ring_a + slot * (S::SLOT >> 4);
                 if (elected()) {
 #pragma unroll
-                    for (int j = 0; j < 2 * kTok / 16; ++j)  // the first numbers, then the second ones
+                    for (int j = 0; j < S::TERMS * kTok / 16; ++j)  // the first numbers, then the second ones
                         mma_ts(d, a + j * 8, b + ((j % 4) * 2048 >> 4), v_hi, idesc_o, j > 0 ? 1u : it > 0);
                     tc_commit(pv_done(m, buf));
                     tc_commit(empty(slot));
                 }
                 __syncwarp();
                 next_slot();
-                if (it + 2 < T && wait(full(slot), full_phase)) scores(k_no + 2);
+                if (it + 2 < T) scores(k_no + 2);
             }
             w.next(T);
         }
@@ -698,7 +738,7 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
             const TreeRow row = w.row;
             const int32_t T = w.tiles(), new0 = row.len - row.n, h = w.h, t0 = w.t;
             const bool mine = r < row.count, some = (r & ~31) < row.count;
-            const uint32_t rr = (uint32_t)((int64_t)plane * R + r);
+            const uint32_t rr = (uint32_t)((int64_t)row.plane * R + r);
             const int32_t i = mine ? (int32_t)sbt_div(p.group, rr) : 0, g = mine ? (int32_t)(rr - i * p.group.d) : 0;
             const int64_t q_row = row.q0 + i;
             float ref = -CUDART_INF_F, l = 0.f;
@@ -707,21 +747,25 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
                 const char* const a = p.q + (q_row * p.ld_q + (int64_t)(h * (int32_t)p.group.d + g) * p.ld_qh) * 2;
                 uint8_t* const to = q_s + m * S::Q_TILE + (r & 127) * 128;
                 if (p.q_vec) {
+                    constexpr int BATCH = DP / 8 % 16 == 0 ? 16 : 8;  // all loads of a row of 128 elements are on their way at once
 #pragma unroll
-                    for (int e0 = 0; e0 < DP / 8; e0 += 8) {
-                        uint4 v[8];
+                    for (int e0 = 0; e0 < DP / 8; e0 += BATCH) {
+                        uint4 v[BATCH];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
+                        for (int e = 0; e < BATCH; ++e)
                             v[e] = mine && (e0 + e) * 8 < p.head_dim ? sbt_ld(reinterpret_cast<const uint4*>(a) + e0 + e)
                                                                      : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<uint4*>(to + (e0 / 8) * kRows * 128 + ((e ^ (r & 7)) << 4)) = v[e];
+                        for (int e = 0; e < BATCH; ++e)
+                            v[e].x ^= p.negate, v[e].y ^= p.negate, v[e].z ^= p.negate, v[e].w ^= p.negate;
+#pragma unroll
+                        for (int e = 0; e < BATCH; ++e)
+                            *reinterpret_cast<uint4*>(to + ((e0 + e) / 8) * kRows * 128 + (((e & 7) ^ (r & 7)) << 4)) = v[e];
                     }
                 } else {
                     for (int d = 0; d < DP; ++d)
                         *reinterpret_cast<uint16_t*>(to + (d >> 6) * kRows * 128 + (((d >> 3 & 7) ^ (r & 7)) << 4) + (d & 7) * 2) =
-                            mine && d < p.head_dim ? sbt_ld(reinterpret_cast<const uint16_t*>(a) + d) : (uint16_t)0;
+                            (mine && d < p.head_dim ? sbt_ld(reinterpret_cast<const uint16_t*>(a) + d) : (uint16_t)0) ^ (uint16_t)p.negate;
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(q_full(m));
@@ -763,16 +807,13 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
                     tmem_ld_32x32b_x32(s_t + 32, x[1]);
                     tmem_ld_wait();
                     const int32_t pos0 = (t0 + it) * kTok;
-                    uint64_t vis = ~0ull;
-                    const bool partial = on_page != ~0ull || pos0 + kTok > new0;
-                    if (partial) vis = on_page & sees(pos0);
-                    if (p.negate)
-#pragma unroll
-                        for (int j = 0; j < 64; ++j) x[j / 32][j % 32] ^= 0x80000000u;
-                    if (partial)
+                    if (on_page != ~0ull || pos0 + kTok > new0) {
+                        const uint64_t vis = on_page & sees(pos0);
+                        const uint32_t seen[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
 #pragma unroll
                         for (int j = 0; j < 64; ++j)
-                            if (!(vis >> j & 1)) x[j / 32][j % 32] = 0xff800000u;
+                            if (!(seen[j / 32] >> j % 32 & 1)) x[j / 32][j % 32] = 0xff800000u;
+                    }
                     float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
                     for (int j = 0; j < 64; j += 2)
@@ -812,18 +853,16 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
                             const int k = c * 16 + 2 * j;
                             const float2 y = fma2(make_float2(__uint_as_float(x[k / 32][k % 32]), __uint_as_float(x[k / 32][k % 32 + 1])),
                                                   make_float2(p.scale, p.scale), make_float2(base, base));
-                            float2 e = make_float2(sbt_attn::exp2_fast(y.x), sbt_attn::exp2_fast(y.y));
-                            if (partial) {  // a scale of zero makes NaN of a masked score
-                                e.x = vis >> k & 1 ? e.x : 0.f;
-                                e.y = vis >> (k + 1) & 1 ? e.y : 0.f;
-                            }
+                            const float2 e = make_float2(sbt_attn::exp2_fast(y.x), sbt_attn::exp2_fast(y.y));
                             sum[j & 1] = add2(sum[j & 1], e);
                             hi[j] = pack2<KIND>(e.x, e.y);
-                            const float2 d = add2(e, unpack2<KIND>(hi[j] ^ 0x80008000u));
-                            lo[j] = pack2<KIND>(d.x, d.y);
+                            if (S::TERMS == 2) {
+                                const float2 d = add2(e, unpack2<KIND>(hi[j] ^ 0x80008000u));
+                                lo[j] = pack2<KIND>(d.x, d.y);
+                            }
                         }
                         tmem_st_x8(s_t + c * 8, hi);
-                        tmem_st_x8(s_t + 32 + c * 8, lo);
+                        if (S::TERMS == 2) tmem_st_x8(s_t + 32 + c * 8, lo);
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_st_wait();
@@ -936,11 +975,11 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
             if (!cut && threadIdx.x == 0) {
                 TreeDesc e = {};
                 if (!whole) {
-                    e.valid = 1, e.b = row.b, e.h = h, e.plane = plane, e.first = c, e.first_slot = first_seg ? 0 : 1;
+                    e.valid = 1, e.b = row.b, e.h = h, e.plane = row.plane, e.first = c, e.first_slot = first_seg ? 0 : 1;
                     e.last = line.warp_of(w.u - t0 + row.tiles - 1);
                 }
                 if (p.desc_by_line)
-                    p.desc[((int64_t)row.b * p.kv_heads + h) * p.planes + plane] = e;
+                    p.desc[((int64_t)row.b * p.kv_heads + h) * p.planes + row.plane] = e;
                 else if (e.valid)
                     p.desc[blockIdx.x] = e;
             }
@@ -949,27 +988,32 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
         }
     }
 
-    // ---- rows of entries that hold no position they could see: zeros, and a log-sum-exp of minus infinity
-    for (int64_t b = c; b < p.batch; b += p.ranges) {
-        const TreeRow row = row_of(p, (int32_t)b, plane, R);
-        if (row.tiles) continue;
-        for (int64_t e = threadIdx.x; e < (int64_t)row.count * p.kv_heads; e += THREADS) {
-            const int32_t h = (int32_t)(e / row.count);
-            const uint32_t rr = (uint32_t)((int64_t)plane * R + e - (int64_t)h * row.count), i = sbt_div(p.group, rr);
-            const int32_t qh = h * (int32_t)p.group.d + (int32_t)(rr - i * p.group.d);
-            uint16_t* const to = reinterpret_cast<uint16_t*>(p.out) + (row.q0 + (int64_t)i) * p.ld_out + qh * p.ld_oh;
-            for (int d = 0; d < p.head_dim; ++d) to[d] = 0;
-            if (p.lse) p.lse[(row.q0 + (int64_t)i) * p.q_heads + qh] = -CUDART_INF_F;
+    // ---- planes that hold no position they could see: zeros, and a log-sum-exp of minus infinity
+    if (warp == 4 * MT)  // (the first warp of the copies is done before the others)
+        for (int64_t b = c; b < p.batch; b += gridDim.x) {
+            TreeRow row = row_of(p, (int32_t)b, R);
+            for (int32_t i = 0; i < p.planes; ++i) {
+                set_plane(p, row, i, R);
+                if (row.tiles) continue;
+                if (p.desc_by_line)
+                    for (int32_t h = lane; h < p.kv_heads; h += 32) p.desc[((int64_t)b * p.kv_heads + h) * p.planes + i].valid = 0;
+                else if (row.count == 0)
+                    break;
+                for (int64_t e = lane; e < (int64_t)row.count * p.kv_heads; e += 32) {
+                    const int32_t h = (int32_t)(e / row.count);
+                    const uint32_t rr = (uint32_t)((int64_t)i * R + e - (int64_t)h * row.count), tok = sbt_div(p.group, rr);
+                    const int32_t qh = h * (int32_t)p.group.d + (int32_t)(rr - tok * p.group.d);
+                    uint16_t* const to = reinterpret_cast<uint16_t*>(p.out) + (row.q0 + (int64_t)tok) * p.ld_out + qh * p.ld_oh;
+                    for (int d = 0; d < p.head_dim; ++d) to[d] = 0;
+                    if (p.lse) p.lse[(row.q0 + (int64_t)tok) * p.q_heads + qh] = -CUDART_INF_F;
+                }
+            }
         }
-        if (p.desc_by_line)
-            for (int32_t h = threadIdx.x; h < p.kv_heads; h += THREADS)
-                p.desc[((int64_t)b * p.kv_heads + h) * p.planes + plane].valid = 0;
-    }
     tc_fence_before();
     __syncthreads();
     if (*abort_flag && p.desc_by_line && threadIdx.x == 0 && !idle)
         for (Walk w = start; w.u < w.end; w.next(w.tiles()))  // what was not finished is not joined
-            if (w.t == 0) p.desc[((int64_t)w.row.b * p.kv_heads + w.h) * p.planes + plane].valid = 0;
+            if (w.t == 0) p.desc[((int64_t)w.row.b * p.kv_heads + w.h) * p.planes + w.row.plane].valid = 0;
     if (warp == WARPS - 1) {
         tc_fence_after();
         tmem_dealloc(tmem, S::COLS);
@@ -982,18 +1026,17 @@ template <int KIND, int DP, int MT>
 __global__ void __launch_bounds__(kJoin) k_tree_join(const TreeAttnParams p, int32_t pieces, int32_t groups) {
     constexpr int R = MT * kRows;
     __shared__ float4 s_o[kJoin];
-    __shared__ float s_l[kJoin];
+    __shared__ float s_l[kJoin], s_top[32];
     griddep_wait();
     const TreeDesc e = p.desc[blockIdx.x / pieces];
     if (!e.valid) return;
-    const TreeRow row = row_of(p, e.b, e.plane, R);
+    TreeRow row = row_of(p, e.b, R);
+    set_plane(p, row, e.plane, R);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quads = kJoin / 32 / groups, rest = blockIdx.x % pieces;
     const int r0 = rest / (DP / 4 / quads) * 32, quad = rest % (DP / 4 / quads) * quads + warp / groups, group = warp % groups;
     if (r0 >= row.count) return;
     const int r = min(r0 + lane, row.count - 1);
-    const int64_t step = 2ll * p.planes;                      // slots between a line's parts
-    const int64_t slot0 = 2 * ((int64_t)e.first * p.planes + e.plane);
-    auto slot = [&](int32_t i) -> int64_t { return slot0 + i * step + (i == 0 ? e.first_slot : 0); };
+    auto slot = [&](int32_t i) -> int64_t { return 2ll * (e.first + i) + (i == 0 ? e.first_slot : 0); };
     const int32_t n = e.last - e.first + 1;
     float top = -CUDART_INF_F;
 #pragma unroll 8
@@ -1008,27 +1051,33 @@ __global__ void __launch_bounds__(kJoin) k_tree_join(const TreeAttnParams p, int
         l += ml.y * a;
         o[0] += x.x * a, o[1] += x.y * a, o[2] += x.z * a, o[3] += x.w * a;
     }
-    if (groups > 1) {
-        s_o[threadIdx.x] = make_float4(o[0], o[1], o[2], o[3]);
-        s_l[threadIdx.x] = l;
-        __syncthreads();
-        if (group) return;
-        for (int i = 1; i < groups; ++i) {
-            const float4 x = s_o[threadIdx.x + 32 * i];
-            l += s_l[threadIdx.x + 32 * i];
-            o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w;
-        }
+    s_o[threadIdx.x] = make_float4(o[0], o[1], o[2], o[3]);
+    s_l[threadIdx.x] = l;
+    if (warp == 0) s_top[lane] = top;
+    __syncthreads();
+    // neighbouring threads write neighbouring vectors of a row
+    const int mine = threadIdx.x / quads, q = threadIdx.x % quads;
+    if (threadIdx.x >= 32 * quads || r0 + mine >= row.count) return;
+    l = 0.f, o[0] = o[1] = o[2] = o[3] = 0.f;
+    for (int i = 0; i < groups; ++i) {
+        const int from = (q * groups + i) * 32 + mine;
+        const float4 x = s_o[from];
+        l += s_l[from];
+        o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w;
     }
-    if (r0 + lane >= row.count) return;
-    const uint32_t rr = (uint32_t)((int64_t)e.plane * R + r), i = sbt_div(p.group, rr);
-    const int32_t qh = e.h * (int32_t)p.group.d + (int32_t)(rr - i * p.group.d);
+    const uint32_t rr = (uint32_t)((int64_t)e.plane * R + r0 + mine), i = sbt_div(p.group, rr);
+    const int32_t qh = e.h * (int32_t)p.group.d + (int32_t)(rr - i * p.group.d), d = (quad - warp / groups + q) * 4;
     const int64_t q_row = row.q0 + (int64_t)i;
     const float inv = sbt_attn::inverse(l);
-    uint16_t* const to = reinterpret_cast<uint16_t*>(p.out) + q_row * p.ld_out + qh * p.ld_oh + quad * 4;
+    uint16_t* const to = reinterpret_cast<uint16_t*>(p.out) + q_row * p.ld_out + qh * p.ld_oh + d;
+    if (p.out_vec && d + 4 <= p.head_dim) {
+        *reinterpret_cast<uint2*>(to) = make_uint2(pack2<KIND>(o[0] * inv, o[1] * inv), pack2<KIND>(o[2] * inv, o[3] * inv));
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (quad * 4 + j < p.head_dim) to[j] = Num<KIND>::put(o[j] * inv);
-    if (quad == 0 && p.lse) p.lse[q_row * p.q_heads + qh] = sbt_attn::log_sum(top, l);
+        for (int j = 0; j < 4; ++j)
+            if (d + j < p.head_dim) to[j] = Num<KIND>::put(o[j] * inv);
+    }
+    if (d == 0 && p.lse) p.lse[q_row * p.q_heads + qh] = sbt_attn::log_sum(s_top[mine], l);
 }
 
 // Blocks that the workspace has room for: two an SM of 128 rows, or one of 256.
@@ -1041,8 +1090,7 @@ sbt_status enqueue(sbt_context* ctx, TreeAttnParams& p, const TreeMaps& maps, vo
     sbt_resident_blocks<k_tree_attention<KIND, DP, MT, TMA>>(ctx, S::THREADS, S::SMEM);
     const int resident = ctx->sm_count * S::BLOCKS;
     p.planes = (int32_t)sbt_cdiv((int64_t)p.max_new * p.group.d, S::R);
-    p.ranges = std::max(1, resident / p.planes);
-    const int64_t blocks = (int64_t)p.ranges * p.planes, lines = (int64_t)p.batch * p.kv_heads * p.planes;
+    const int64_t blocks = resident, lines = (int64_t)p.batch * p.kv_heads * p.planes;
     p.desc_by_line = lines <= blocks;
     p.desc = (TreeDesc*)workspace;
     p.part_ml = (float2*)((char*)workspace + sbt_cdiv(blocks * sizeof(TreeDesc), 256) * 256);
@@ -1051,7 +1099,6 @@ sbt_status enqueue(sbt_context* ctx, TreeAttnParams& p, const TreeMaps& maps, vo
                                                         dim3(S::THREADS), S::SMEM, stream, p, maps.k, maps.v),
                                    "paged_tree_attention launch");
     if (st || (st = sbt_after_launch(ctx, "paged_tree_attention"))) return st;
-    if (p.ranges == 1) return SBT_OK;  // no line is cut
     const int64_t n_desc = p.desc_by_line ? lines : blocks;
     // Few lines are cut into many parts: four warps share a vector's; many lines into two or three.
     const int64_t row_groups = sbt_cdiv(std::min<int64_t>(S::R, (int64_t)p.max_new * p.group.d), 32);

@@ -187,11 +187,13 @@ def tree_attention(q, k, v, table, lens, page_size, scale, cu, max_new, mask=Non
     return out, lse, written, x
 
 
-def tree_attention_bounds(ref, kind, D):
-    """As cache_ref.attention_bounds: probabilities of 16 (bf16) or 22 (fp16) bits, fp16 ones in steps of 2^-33 at least."""
+def tree_attention_bounds(ref, kind, D, terms=2):
+    """As cache_ref.attention_bounds.  Probabilities of two 16-bit numbers have 16 (bf16) or 22 (fp16) bits, those of one
+    are off by half a step (2^-8, 2^-11 of themselves); fp16 ones have steps of 2^-33 of the row's largest at least."""
     out, lse, _, x = ref
     score = (D + 3) * 2.0**-23 * x["mag"]
-    rel = 2 * score + (x["count"] + 64) * 2.0**-23 + {"bf16": 2.0**-16, "f16": 2.0**-21}[kind]
+    p = {"bf16": 2.0**-16, "f16": 2.0**-21}[kind] if terms == 2 else HALF_ULP[kind]
+    rel = 2 * score + (x["count"] + 64) * 2.0**-23 + p
     o = rel[..., None] * x["absv"] + HALF_ULP[kind] * np.abs(out) * 1.01 + TINY[kind]
     if kind == "f16":
         o = o + (x["count"] * 2.0**-34 * x["vmax"])[..., None]

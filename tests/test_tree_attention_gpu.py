@@ -1,7 +1,8 @@
 """GPU parity of sbt_paged_tree_attention with its definition in 64 bits.
 
 Bounds (step_ref.tree_attention_bounds): scores off by D + 3 roundings of their terms, sums over the
-visible positions, probabilities of two 16-bit numbers, one rounding to the type.
+visible positions, probabilities of two 16-bit numbers (one where a key-value head has more than 128 rows of
+up to 128 elements), one rounding to the type.
 """
 import numpy as np
 import pytest
@@ -114,10 +115,13 @@ class Case:
         return ref.tree_attention(ref.f64(self.q), ref.f64(self.view(self.k)), ref.f64(self.view(self.v)), self.table,
                                   self.lens, self.P, self.scale, self.cu, self.max_new, self.mask, self.seq)
 
+    def bounds(self, want):
+        return ref.tree_attention_bounds(want, self.kind, self.D, 1 if self.max_new * self.group > 128 and self.D <= 128 else 2)
+
     def check(self, ctx, **kw):
         got, lse = self.run(ctx, **kw)
         want = self.want()
-        ob, sb = ref.tree_attention_bounds(want, self.kind, self.D)
+        ob, sb = self.bounds(want)
         w = want[2]
         assert (got[~w] == FILL).all() and (lse[~w] == FILL).all()
         none = np.isneginf(want[1])
@@ -224,7 +228,7 @@ def test_infinities_and_nan_among_the_new_tokens(ctx, sizes, group, D, P, where,
         sees[i] = c.mask.view(np.uint32)[i, token // 32] >> (token % 32) & 1
     assert 0 < sees[:n].sum() < n
     got, lse = c.run(ctx)
-    ob, sb = ref.tree_attention_bounds(want, kind, D)
+    ob, sb = c.bounds(want)
     w = want[2] & ~sees
     none = np.isneginf(want[1])
     assert (np.abs(got - want[0]) <= ob)[w].all() and (np.abs(lse - want[1]) <= sb)[w[:, None] & ~none].all()
@@ -250,7 +254,7 @@ def test_infinities_in_the_context_and_queries(ctx, kind):
     assert not np.isfinite(got[:6, :, 5]).any()
     c.q[8, 1, 2] = float("nan")
     got, lse = c.run(ctx)
-    ob, _ = ref.tree_attention_bounds(want, kind, 64)
+    ob, _ = c.bounds(want)
     assert np.isnan(got[8, 1]).all() and np.isnan(lse[8, 1])
     assert (np.abs(got - want[0]) <= ob)[[6, 7, 9]].all() and (np.abs(got - want[0]) <= ob)[8, 0].all()
 
@@ -305,7 +309,7 @@ def test_one_token_is_paged_attention(ctx, kind):
     ws = torch.empty(n, dtype=torch.uint8, device="cuda")
     sbt.paged_attention(ctx, c.q.cuda(), 1024, 128, 5, 8, cache, m, c.scale, out, 1024, 128, lse=l2, seq=seq, workspace=ws,
                         workspace_bytes=n)
-    ob, sb = ref.tree_attention_bounds(c.want(), kind, 128)
+    ob, sb = c.bounds(c.want())
     assert (np.abs(ref.f64(out) - got) <= 2 * ob).all() and (np.abs(ref.f64(l2) - lse) <= 2 * sb).all()
 
 
@@ -345,7 +349,7 @@ def test_offsets_past_32_bits(ctx):
     sbt.paged_tree_attention(ctx, q, 128, 64, c.rows, cu, 2, c.max_new, 2, sbt.kv_cache(big_k, big_v, 1, 64, spread, 64, 64),
                              m, c.scale, out, 128, 64, mask=mask, ld_mask=c.words, seq=seq, workspace=ws, workspace_bytes=n)
     want = c.want()
-    ob, _ = ref.tree_attention_bounds(want, "f16", 64)
+    ob, _ = c.bounds(want)
     assert (np.abs(ref.f64(out) - want[0]) <= ob)[want[2]].all()
 
 
