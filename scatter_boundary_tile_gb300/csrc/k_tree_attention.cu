@@ -69,7 +69,7 @@ sbt_status sbt_launch_tree_attention(sbt_context* ctx, sbt_dtype dtype, const Sb
     p.group = sbt_make_fastdiv((uint32_t)(q_heads / cache->heads));
     p.page_size = sbt_make_fastdiv((uint32_t)map->page_size);
     // (a scale of zero would make NaN of a masked score of minus infinity; 2^-126 of any finite one is as good as zero)
-    p.scale = std::max(fabsf(scale) * 1.4426950408889634f, 0x1p-126f), p.negate = scale < 0.f ? 0x80008000u : 0u;
+    p.scale = std::max(fabsf(scale) * 1.4426950408889634f, 0x1p-126f), p.negate = scale < 0.f;
     p.q_vec = piece(q.p, q.ld, q.ldh, 0, p.head_dim) == 16;
     p.copy_kv = std::min(piece(p.k, p.ld_page, p.ld_slot, p.ld_head, p.head_dim), piece(p.v, 0, 0, 0, p.head_dim));
     p.out_vec = piece(out.p, out.ld, out.ldh, 0, p.head_dim) == 16;

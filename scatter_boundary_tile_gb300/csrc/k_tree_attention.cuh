@@ -74,7 +74,7 @@ struct TreeAttnParams {
     int32_t desc_by_line;                      // descriptors by line (there are no more lines than blocks), else by block
     sbt_fastdiv group, page_size;
     float scale;                               // |scale| log2 e, not zero
-    uint32_t negate;                           // sign bits of two numbers where the scale is negative: on the queries
+    int32_t negate;                            // the scale is negative
     unsigned int* status;
     uint64_t wait_ns;
     int32_t withhold;                          // test hook: no block signals its first tile
@@ -698,10 +698,13 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
             for (int i = 0; i < min(T, 2) && wait(full(slot), full_phase); ++i) scores(k_no + i);
             for (int32_t it = 0; ok && it < T; ++it, ++k_no) {
                 const int buf = (int)(k_no & 1);
-                // V, and the K of two tiles on, which follows it in the ring; then P, which both wait for
-                if (!wait(full(slot), full_phase)) break;
-                if (it + 2 < T && !wait(full(slot + 1 == NS ? 0 : slot + 1), slot + 1 == NS ? full_phase ^ 1 : full_phase)) break;
-                if (!wait(p_ready(m, buf), (uint32_t)(k_no >> 1) & 1)) break;
+                // P, V and the K of two tiles on, which follows V in the ring, a lane each: one wait after another
+                // would cost 200 cycles a piece
+                const bool wrap = slot + 1 == NS;
+                uint32_t bar = p_ready(m, buf), parity = (uint32_t)(k_no >> 1) & 1;
+                if (lane == 1) bar = full(slot), parity = full_phase;
+                if (lane == 2 && it + 2 < T) bar = full(wrap ? 0 : slot + 1), parity = wrap ? full_phase ^ 1 : full_phase;
+                if (!wait(bar, parity)) break;
                 const uint32_t a = tmem + (m * 2 + buf) * kTok, d = tmem + S::O_COL + m * DP;
                 const uint32_t b = v_lo + ring_a + slot * (S::SLOT >> 4);
                 if (elected()) {
@@ -757,15 +760,12 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
                                                                      : make_uint4(0, 0, 0, 0);
 #pragma unroll
                         for (int e = 0; e < BATCH; ++e)
-                            v[e].x ^= p.negate, v[e].y ^= p.negate, v[e].z ^= p.negate, v[e].w ^= p.negate;
-#pragma unroll
-                        for (int e = 0; e < BATCH; ++e)
                             *reinterpret_cast<uint4*>(to + ((e0 + e) / 8) * kRows * 128 + (((e & 7) ^ (r & 7)) << 4)) = v[e];
                     }
                 } else {
                     for (int d = 0; d < DP; ++d)
                         *reinterpret_cast<uint16_t*>(to + (d >> 6) * kRows * 128 + (((d >> 3 & 7) ^ (r & 7)) << 4) + (d & 7) * 2) =
-                            (mine && d < p.head_dim ? sbt_ld(reinterpret_cast<const uint16_t*>(a) + d) : (uint16_t)0) ^ (uint16_t)p.negate;
+                            mine && d < p.head_dim ? sbt_ld(reinterpret_cast<const uint16_t*>(a) + d) : (uint16_t)0;
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(q_full(m));
@@ -807,6 +807,9 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
                     tmem_ld_32x32b_x32(s_t + 32, x[1]);
                     tmem_ld_wait();
                     const int32_t pos0 = (t0 + it) * kTok;
+                    if (p.negate)
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) x[j / 32][j % 32] ^= 0x80000000u;
                     if (on_page != ~0ull || pos0 + kTok > new0) {
                         const uint64_t vis = on_page & sees(pos0);
                         const uint32_t seen[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
