@@ -16,7 +16,9 @@
 // lane's four are neighbours, for the weights and for x alike.
 //
 // Groups.  The products of U k (32, or 16) are summed by the matrix unit and
-// added to the running sums times the group's scale.
+// added to the running sums times the group's scale.  A stage holds 64 k where
+// they are whole groups or part of one, so that waits, copies and addresses are
+// paid once for them.
 //
 // x.  fp16 enters as it is.  bf16 and fp32 are scaled by a power of two to
 // below 2^15, per row and for the k seen so far (as the running maximum of a
@@ -24,8 +26,10 @@
 // numbers; bf16's 8 bits fit in fp16's 11 unless they are below its last step,
 // 2^-39 of the largest.
 //
-// Split.  A block has 256 columns and a share of k, its warps a share each;
-// every warp has a private ring of stages filled by cp.async and waits for no
+// Split.  A block has 256 columns and a share of k; its warps take 128 columns and
+// a share of that k (with 256 columns the sums leave no registers for what is on
+// its way).  Every
+// warp has a private ring of stages filled by cp.async and waits for no
 // other until the end.  A cluster of up to eight blocks shares the k of one
 // tile; warps, then blocks, join in a fixed order through shared memory.
 #include <algorithm>
@@ -39,9 +43,9 @@ namespace {
 using namespace sbt_num;
 using sbt_ptx::griddep_wait;
 
-constexpr int kWarps = 8, kCols = 256, kClusterMost = 8;
+constexpr int kCols = 256, kClusterMost = 8;
 constexpr int kPitch = kCols + 20;  // floats between rows of partial sums: lanes of a half warp meet no bank twice
-constexpr int kFixedStages = 4;     // what a block costs besides its stages, in stages
+constexpr int kFixedRows = 128;     // what a block costs besides its k, in k of a warp
 
 struct MatvecParams {
     const char* x;
@@ -53,14 +57,26 @@ struct MatvecParams {
     int32_t y_kind, ranks, x_vec;
 };
 
-template <int KIND, int U, bool ALIGNED>
+// U: k whose products are summed before they are scaled; SU: such units of a stage.
+template <int U, int SU, int MT, bool ALIGNED>
 struct Shape {
-    static constexpr int ES = sizeof(typename Num<KIND>::T);
-    static constexpr int PITCH = ALIGNED ? 128 : 144;      // bytes of a row of weights in a stage
-    static constexpr int STAGE = U * PITCH + 288;          // and up to 256 + 15 bytes of scales
-    static constexpr int STAGES = (112 << 10) / (kWarps * STAGE);
+    static constexpr int ROWS = U * SU;
+    // 16 rows of x: the sums fill twice the registers, and twelve warps an SM take the place of sixteen
+    static constexpr int WARPS = MT == 1 ? 8 : 12, BLOCKS = MT == 1 ? 2 : 1;
+    static constexpr int CW = 128, KW = WARPS * CW / kCols;  // columns of a warp, warps along k
+    static constexpr int LANE = CW / 16;                   // bytes of a row that a lane takes
+    static constexpr int PITCH = ALIGNED ? CW / 2 : CW / 2 + 16;  // bytes of a row of weights in a stage
+    static constexpr int SCALES = CW + 32;                 // a row of scales, from the 16-byte boundary before it
+    static constexpr int STAGE = ROWS * PITCH + SU * SCALES;
+    static constexpr int MOST = (220 << 10) / (BLOCKS * WARPS * STAGE), STAGES = MOST < 8 ? MOST : 8;
     static constexpr int RING = STAGES * STAGE;
-    static constexpr size_t SMEM = (size_t)kWarps * (RING > 8 * kPitch * 4 ? RING : 8 * kPitch * 4);
+    static constexpr int PART = 8 * kPitch * 4;            // sums of 256 columns
+    static constexpr size_t SMEM = (size_t)WARPS * RING > (size_t)KW * PART ? (size_t)WARPS * RING : (size_t)KW * PART;
+    // Place of byte `c` of row r (aligned rows): lanes that read together, their rows U / 4 apart, meet no bank twice.
+    static __device__ __forceinline__ int place(int r, int c) {
+        const int key = r / (U / 4) & 3;
+        return (r ^ (key & 1)) * 64 + (c ^ (key << 4));
+    }
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
@@ -96,99 +112,149 @@ __device__ __forceinline__ float2 unpack_scales(uint32_t two) {
     return make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u));
 }
 
+// c = a b (+ c).
+template <bool ADD>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    if (ADD)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// KIND: of x.  U: k of a stage.  MT: 8 rows of x each.
-template <int KIND, int U, bool E4M3, int MT, bool ALIGNED>
-__global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 2 : 1) k_matvec(const MatvecParams p) {
-    typedef Shape<KIND, U, ALIGNED> S;
+// KIND: of x.  MT: 8 rows of x each.
+template <int KIND, int U, int SU, bool E4M3, int MT, bool ALIGNED>
+__global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED>::WARPS, Shape<U, SU, MT, ALIGNED>::BLOCKS) k_matvec(const MatvecParams p) {
+    typedef Shape<U, SU, MT, ALIGNED> S;
     typedef typename Num<KIND>::T T;
-    constexpr int STEPS = U / 16, TERMS = KIND == kF32 ? 2 : 1;
+    constexpr int WORDS = S::LANE / 4, TILES = 4 * WORDS;  // of a lane's piece of a row; matrix tiles of a warp
+    constexpr int STEPS = U / 16, ROWS = S::ROWS, TERMS = KIND == kF32 ? 2 : 1;
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int rank = blockIdx.x % p.ranks;
-    const int64_t tile = blockIdx.x / p.ranks, n0 = tile * kCols, tok0 = (int64_t)blockIdx.y * 8 * MT;
-    const int64_t units = p.K / U, workers = (int64_t)kWarps * p.ranks, me = (int64_t)rank * kWarps + warp;
-    const int64_t u0 = units * me / workers, u1 = units * (me + 1) / workers;
+    const int64_t tile = blockIdx.x / p.ranks, tok0 = (int64_t)blockIdx.y * 8 * MT;
+    const int64_t n0 = tile * kCols + warp / S::KW * S::CW;
+    const int64_t stages = p.K / ROWS, workers = (int64_t)S::KW * p.ranks, me = (int64_t)rank * S::KW + warp % S::KW;
+    const int64_t u0 = stages * me / workers, u1 = stages * (me + 1) / workers;
     uint8_t* const ring = smem + warp * S::RING;
     const uint32_t ring_u32 = sbt_ptx::smem_u32(ring);
     griddep_wait();
 
-    // ---- copies: rows of 128 bytes of weights, and the group's 256 scales, nothing past their ends
-    const int w_bytes = (int)min((int64_t)(kCols / 2), (p.N + 1) / 2 - n0 / 2), s_bytes = (int)min((int64_t)kCols, p.N - n0);
-    auto copy = [&](int64_t u, int stage) {
+    // ---- copies: the warp's columns of a stage's rows and its group's scales, nothing past their ends
+    const int w_bytes = (int)max((int64_t)0, min((int64_t)(S::CW / 2), (p.N + 1) / 2 - n0 / 2));
+    const int s_bytes = (int)max((int64_t)0, min((int64_t)S::CW, p.N - n0));
+    constexpr int LPR = S::CW / 32;                       // lanes of a row, 16 bytes each
+    const int copy_c = ALIGNED ? lane % LPR * 16 : lane % (2 * LPR) * 16, copy_r = lane / (ALIGNED ? LPR : 2 * LPR);
+    const int copy_bytes = min(max(w_bytes - copy_c, 0), 16);
+    const uint8_t* copy_w = p.w + n0 / 2 + (u0 * ROWS + copy_r) * p.ld_w;
+    // Rows of scales: one for `per` stages (of which `left` are still to come for the copies and for the sums), or
+    // one for every unit of a stage.
+    const bool each = p.group < ROWS;
+    const int per = each ? 1 : (int)(p.group / ROWS), s_rows = each ? SU : 1;
+    const uint8_t *copy_s = p.s + (each ? u0 * SU : u0 / per) * p.ld_s + n0, *sum_s = copy_s;
+    int copy_left = per - (int)(u0 % per), sum_left = copy_left;
+    const bool s_aligned = (((uintptr_t)p.s | (uintptr_t)p.ld_s) & 15) == 0;
+    // places of this lane's rows of a stage, less what rows STEP apart are apart: they repeat after four
+    constexpr int STEP = 32 / LPR;
+    uint32_t at_place[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) at_place[i] = S::place(i * STEP + copy_r, copy_c) - i * STEP * 64;
+    const int64_t w_step = STEP * p.ld_w;
+    auto copy = [&](int stage) {  // the next stage's
         const uint32_t dst = ring_u32 + stage * S::STAGE;
-        const uint8_t* const src = p.w + u * U * p.ld_w + n0 / 2;
+        const uint8_t* src = copy_w;
+        copy_w += ROWS * p.ld_w;
         if (ALIGNED) {
-            const int c = lane & 7, bytes = min(max(w_bytes - c * 16, 0), 16);
+            if (copy_bytes) {
+                src += copy_c;
 #pragma unroll
-            for (int i = 0; i < U / 4; ++i) {
-                const int r = i * 4 + (lane >> 3);
-                copy16(dst + r * 128 + ((c ^ (((r >> 2) & 3) << 1)) << 4), bytes ? src + r * p.ld_w + c * 16 : p.w, bytes);
-            }
-        } else {
-            const int c = lane & 15;  // nine pieces cover a row from the 16-byte boundary before it
-#pragma unroll 4
-            for (int i = 0; i < U / 2; ++i) {
-                const int r = i * 2 + (lane >> 4);
-                const uint8_t* const a = src + r * p.ld_w;
-                const int shift = (int)((uintptr_t)a & 15), bytes = min(max(shift + w_bytes - c * 16, 0), 16);
-                if (bytes) copy16(dst + r * 144 + c * 16, a - shift + c * 16, bytes);
-            }
-        }
-        const uint8_t* const a = p.s + u * U / p.group * p.ld_s + n0;
-        const int shift = (int)((uintptr_t)a & 15), bytes = min(max(shift + s_bytes - lane * 16, 0), 16);
-        if (bytes) copy16(dst + U * S::PITCH + lane * 16, a - shift + lane * 16, bytes);
-    };
-
-    // ---- x: this lane's four k of each step, of rows tok0 + 8 m + g; the next stage's while this one is used
-    struct Raw {
-        T v[4];
-    };
-    auto load_x = [&](int64_t u, Raw (&r)[STEPS][MT]) {
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int64_t tok = tok0 + m * 8 + g;
-                const T* const a = reinterpret_cast<const T*>(p.x + tok * p.ld_x) + u * U + s * 16 + t * 4;
-                if (u >= u1 || tok >= p.tokens) {
-                    r[s][m] = Raw{};
-                } else if (p.x_vec) {
-                    if constexpr (KIND == kF32)
-                        *reinterpret_cast<uint4*>(&r[s][m]) = sbt_ld(reinterpret_cast<const uint4*>(a));
-                    else
-                        *reinterpret_cast<uint2*>(&r[s][m]) = sbt_ld(reinterpret_cast<const uint2*>(a));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) r[s][m].v[i] = sbt_ld(a + i);
+                for (int i = 0; i < ROWS / STEP; ++i) {
+                    copy16(dst + at_place[i % 4] + i * STEP * 64, src, copy_bytes);
+                    src += w_step;
                 }
             }
+        } else {
+            // one piece more than a row has covers it from the 16-byte boundary before it
+#pragma unroll 4
+            for (int i = 0; i < ROWS / (16 / LPR); ++i) {
+                const int shift = (int)((uintptr_t)src & 15), bytes = min(max(shift + w_bytes - copy_c, 0), 16);
+                if (bytes) copy16(dst + (i * (16 / LPR) + copy_r) * S::PITCH + copy_c, src - shift + copy_c, bytes);
+                src += (16 / LPR) * p.ld_w;
+            }
+        }
+        if (s_aligned) {
+            const int row = lane / 8, at = lane % 8 * 16, bytes = min(max(s_bytes - at, 0), 16);
+            if (row < s_rows && bytes)
+                copy16(dst + ROWS * S::PITCH + row * S::SCALES + at, copy_s + row * p.ld_s + at, bytes);
+        } else {
+            for (int row = 0; row < s_rows; ++row) {
+                const uint8_t* const a = copy_s + row * p.ld_s;
+                const int shift = (int)((uintptr_t)a & 15), bytes = min(max(shift + s_bytes - lane * 16, 0), 16);
+                if (s_bytes && bytes) copy16(dst + ROWS * S::PITCH + row * S::SCALES + lane * 16, a - shift + lane * 16, bytes);
+            }
+        }
+        if (--copy_left == 0) copy_left = per, copy_s += s_rows * p.ld_s;
     };
 
-    float sum[MT][16][4];  // columns g*32 + 2 i, + 1; rows 2 t, + 1 of x
+    // ---- x: this lane's U / 4 neighbouring k of each unit, of rows tok0 + 8 m + g; the next stage's while this one is used
+    constexpr int XK = U / 4;
+    struct alignas(16) Raw {
+        T v[XK];
+    };
+    const T* x_at[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+        x_at[m] = tok0 + m * 8 + g < p.tokens
+                      ? reinterpret_cast<const T*>(p.x + (tok0 + m * 8 + g) * p.ld_x) + u0 * ROWS + t * XK : nullptr;
+    auto load_x = [&](int64_t u, Raw (&r)[SU][MT]) {
+#pragma unroll
+        for (int q = 0; q < SU; ++q)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const T* const a = x_at[m] + q * U;
+                if (u >= u1 || !x_at[m]) {
+                    r[q][m] = Raw{};
+                } else if (p.x_vec) {
+                    if constexpr (sizeof(T) * XK >= 16) {
+#pragma unroll
+                        for (int i = 0; i < (int)sizeof(T) * XK / 16; ++i)
+                            reinterpret_cast<uint4*>(&r[q][m])[i] = sbt_ld(reinterpret_cast<const uint4*>(a) + i);
+                    } else {
+                        *reinterpret_cast<uint2*>(&r[q][m]) = sbt_ld(reinterpret_cast<const uint2*>(a));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < XK; ++i) r[q][m].v[i] = sbt_ld(a + i);
+                }
+            }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            if (x_at[m]) x_at[m] += ROWS;
+    };
+
+    float sum[MT][TILES][4];  // columns g * 2 * TILES + 2 i, + 1; rows 2 t, + 1 of x
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < TILES; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) sum[m][i][k] = 0.f;
     int exponent[MT];  // x of row g enters as x 2^-exponent
 #pragma unroll
     for (int m = 0; m < MT; ++m) exponent[m] = -126;
 
-    Raw raw[STEPS][MT];
+    Raw raw[SU][MT];
     load_x(u0, raw);
 #pragma unroll 1
     for (int i = 0; i < S::STAGES - 1; ++i) {
-        if (u0 + i < u1) copy(u0 + i, i);
+        if (u0 + i < u1) copy(i);
         copy_commit();
     }
     int stage = 0;
@@ -196,31 +262,52 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 2 : 1) k_matvec(const M
     for (int64_t u = u0; u < u1; ++u) {
         copy_wait<S::STAGES - 2>();
         __syncwarp();
-        if (u + S::STAGES - 1 < u1) copy(u + S::STAGES - 1, stage == 0 ? S::STAGES - 1 : stage - 1);
+        if (u + S::STAGES - 1 < u1) copy(stage == 0 ? S::STAGES - 1 : stage - 1);
         copy_commit();
 
         // x as fp16 pairs along k
-        uint32_t b[STEPS][MT][TERMS][2];
+        uint32_t b[SU][STEPS][MT][TERMS][2];
         if constexpr (KIND == kF16) {
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s)
+            for (int q = 0; q < SU; ++q)
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(&raw[s][m]);
-                    b[s][m][0][0] = v.x, b[s][m][0][1] = v.y;
-                }
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int s = 0; s < STEPS; ++s) {
+                        const uint2 v = reinterpret_cast<const uint2*>(&raw[q][m])[s];
+                        b[q][s][m][0][0] = v.x, b[q][s][m][0][1] = v.y;
+                    }
         } else {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                // exponent of the largest finite |x| of the row in this stage
-                int top = 0;
+                // exponent of the largest finite |x| of the row in this stage; magnitudes order as their bits do
+                uint32_t most = 0;
+                if constexpr (KIND == kBF16) {
 #pragma unroll
-                for (int s = 0; s < STEPS; ++s)
+                    for (int q = 0; q < SU; ++q)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int e = (int)(__float_as_uint(Num<KIND>::get(raw[s][m].v[i])) >> 23) & 255;
+                        for (int i = 0; i < XK / 2; ++i)
+                            most = __vmaxu2(most, reinterpret_cast<const uint32_t*>(&raw[q][m])[i] & 0x7FFF7FFFu);
+                    most = max(most & 0xFFFF0000u, most << 16);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < SU; ++q)
+#pragma unroll
+                        for (int i = 0; i < XK; ++i) most = max(most, __float_as_uint(Num<KIND>::get(raw[q][m].v[i])) & 0x7fffffffu);
+                }
+                int top = (int)(most >> 23);
+                if (top == 255) {   // an infinity or NaN: the largest of the others
+                    top = 0;
+#pragma unroll 1
+                    for (int q = 0; q < SU * XK; ++q) {
+                        T one = 0;
+#pragma unroll
+                        for (int i = 0; i < SU * XK; ++i)
+                            if (i == q) one = raw[i / XK][m].v[i % XK];
+                        const int e = (int)(__float_as_uint(Num<KIND>::get(one)) >> 23) & 255;
                         top = max(top, e == 255 ? 0 : e);
                     }
+                }
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const int want = max(top - 127 - 14, -126);
@@ -231,102 +318,110 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 2 : 1) k_matvec(const M
                     const float f0 = power(-__shfl_sync(0xffffffffu, gap, 8 * t));
                     const float f1 = power(-__shfl_sync(0xffffffffu, gap, 8 * t + 4));
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < TILES; ++i) {
                         sum[m][i][0] *= f0, sum[m][i][1] *= f1;
                         sum[m][i][2] *= f0, sum[m][i][3] *= f1;
                     }
                 }
                 const float f = power(-exponent[m]);
 #pragma unroll
-                for (int s = 0; s < STEPS; ++s)
+                for (int q = 0; q < SU; ++q)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float lo = Num<KIND>::get(raw[s][m].v[2 * i]) * f, hi = Num<KIND>::get(raw[s][m].v[2 * i + 1]) * f;
+                    for (int i = 0; i < XK / 2; ++i) {
+                        const float lo = Num<KIND>::get(raw[q][m].v[2 * i]) * f, hi = Num<KIND>::get(raw[q][m].v[2 * i + 1]) * f;
                         const __half2 h = __floats2half2_rn(lo, hi);
-                        b[s][m][0][i] = *reinterpret_cast<const uint32_t*>(&h);
+                        b[q][i / 2][m][0][i % 2] = *reinterpret_cast<const uint32_t*>(&h);
                         if constexpr (TERMS == 2) {
-                            const float2 q = __half22float2(h);
+                            const float2 v = __half22float2(h);
                             // what the first number leaves; nothing of an infinity
-                            const __half2 r = __floats2half2_rn(isinf(lo) ? 0.f : lo - q.x, isinf(hi) ? 0.f : hi - q.y);
-                            b[s][m][TERMS - 1][i] = *reinterpret_cast<const uint32_t*>(&r);
+                            const __half2 r = __floats2half2_rn(isinf(lo) ? 0.f : lo - v.x, isinf(hi) ? 0.f : hi - v.y);
+                            b[q][i / 2][m][TERMS - 1][i % 2] = *reinterpret_cast<const uint32_t*>(&r);
                         }
                     }
             }
         }
         load_x(u + 1, raw);
 
-        // weights: rows 16 s + 4 t + r, columns g*32 .. + 31
-        uint32_t w[STEPS][4][4];
         const uint8_t* const st = ring + stage * S::STAGE;
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * s + 4 * t + r;
-                if (ALIGNED) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(st + row * 128 + ((g ^ (((row >> 2) & 3) << 1)) << 4));
-                    w[s][r][0] = v.x, w[s][r][1] = v.y, w[s][r][2] = v.z, w[s][r][3] = v.w;
-                } else {
-                    const int shift = (int)((uintptr_t)(p.w + (u * U + row) * p.ld_w + n0 / 2) & 15);
-                    const uint32_t* const q = reinterpret_cast<const uint32_t*>(st + row * 144 + g * 16 + (shift & ~3));
-                    uint32_t a = q[0];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t c = q[j + 1];
-                        w[s][r][j] = __funnelshift_r(a, c, (shift & 3) * 8);
-                        a = c;
-                    }
-                }
-            }
-        uint32_t sc[8];
-        {
-            const int shift = (int)((uintptr_t)(p.s + u * U / p.group * p.ld_s + n0) & 15);
-            const uint8_t* const a = st + U * S::PITCH + g * 32;
-            if (shift == 0) {
-                const uint4 v0 = *reinterpret_cast<const uint4*>(a), v1 = *reinterpret_cast<const uint4*>(a + 16);
-                sc[0] = v0.x, sc[1] = v0.y, sc[2] = v0.z, sc[3] = v0.w;
-                sc[4] = v1.x, sc[5] = v1.y, sc[6] = v1.z, sc[7] = v1.w;
-            } else {
-                const uint32_t* const q = reinterpret_cast<const uint32_t*>(a + (shift & ~3));
-                uint32_t c = q[0];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t d = q[j + 1];
-                    sc[j] = __funnelshift_r(c, d, (shift & 3) * 8);
-                    c = d;
-                }
-            }
-        }
-        // a byte of the last words may be past the scales and the weights: columns past N, which nobody reads
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t a[STEPS][4][4];  // [step][fragment][column pair]
+        for (int q = 0; q < SU; ++q) {
+            // weights: rows q U + t U / 4 + 4 s + r, a lane's WORDS words of each
+            uint32_t w[STEPS][4][WORDS];
 #pragma unroll
             for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t lo = w[s][2 * k][j], hi = w[s][2 * k + 1][j];
-                    unpack_e2m1((lo & 0x0F0F0F0Fu) | ((hi << 4) & 0xF0F0F0F0u), a[s][2 * k]);
-                    unpack_e2m1(((lo >> 4) & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u), a[s][2 * k + 1]);
-                }
+                for (int r = 0; r < 4; ++r) {
+                    const int row = q * U + t * XK + 4 * s + r;
+                    if (ALIGNED) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(st + S::place(row, g * S::LANE));
+                        w[s][r][0] = v.x, w[s][r][1] = v.y;
+                    } else {
+                        const int shift = (int)((uintptr_t)(p.w + (u * ROWS + row) * p.ld_w + n0 / 2) & 15);
+                        const uint32_t* const a =
+                            reinterpret_cast<const uint32_t*>(st + row * S::PITCH + g * S::LANE + (shift & ~3));
+                        uint32_t c = a[0];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack_scales<E4M3>(i & 1 ? sc[2 * j + i / 2] >> 16 : sc[2 * j + i / 2]);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int s = 0; s < STEPS; ++s) {
-                        const uint32_t frag[4] = {a[s][0][i], a[s][1][i], a[s][2][i], a[s][3][i]};
-#pragma unroll
-                        for (int q = 0; q < TERMS; ++q) mma(c, frag, b[s][m][q][0], b[s][m][q][1]);
+                        for (int j = 0; j < WORDS; ++j) {
+                            const uint32_t d = a[j + 1];
+                            w[s][r][j] = __funnelshift_r(c, d, (shift & 3) * 8);
+                            c = d;
+                        }
                     }
-                    float(&d)[4] = sum[m][4 * j + i];
-                    d[0] = fmaf(c[0], f.x, d[0]), d[1] = fmaf(c[1], f.x, d[1]);
-                    d[2] = fmaf(c[2], f.y, d[2]), d[3] = fmaf(c[3], f.y, d[3]);
+                }
+            uint32_t sc[2 * WORDS];  // scales of its 8 WORDS columns
+            {
+                const int row = each ? q : 0, shift = (int)((uintptr_t)(sum_s + row * p.ld_s) & 15);
+                const uint8_t* const a = st + ROWS * S::PITCH + row * S::SCALES + g * 2 * S::LANE;
+                if (shift == 0) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(a);
+                    sc[0] = v.x, sc[1] = v.y, sc[2] = v.z, sc[3] = v.w;
+                } else {
+                    const uint32_t* const at = reinterpret_cast<const uint32_t*>(a + (shift & ~3));
+                    uint32_t c = at[0];
+#pragma unroll
+                    for (int j = 0; j < 2 * WORDS; ++j) {
+                        const uint32_t d = at[j + 1];
+                        sc[j] = __funnelshift_r(c, d, (shift & 3) * 8);
+                        c = d;
+                    }
+                }
+            }
+            // a byte of the last words may be past the scales and the weights: columns past N, which nobody reads
+#pragma unroll
+            for (int j = 0; j < WORDS; ++j) {
+                uint32_t a[STEPS][4][4];  // [step][fragment][column pair]
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t lo = w[s][2 * k][j], hi = w[s][2 * k + 1][j];
+                        unpack_e2m1((lo & 0x0F0F0F0Fu) | ((hi << 4) & 0xF0F0F0F0u), a[s][2 * k]);
+                        unpack_e2m1(((lo >> 4) & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u), a[s][2 * k + 1]);
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack_scales<E4M3>(i & 1 ? sc[2 * j + i / 2] >> 16 : sc[2 * j + i / 2]);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        float c[4];
+#pragma unroll
+                        for (int s = 0; s < STEPS; ++s) {
+                            const uint32_t frag[4] = {a[s][0][i], a[s][1][i], a[s][2][i], a[s][3][i]};
+#pragma unroll
+                            for (int v = 0; v < TERMS; ++v)
+                                if (s == 0 && v == 0)
+                                    mma<false>(c, frag, b[q][s][m][v][0], b[q][s][m][v][1]);
+                                else
+                                    mma<true>(c, frag, b[q][s][m][v][0], b[q][s][m][v][1]);
+                        }
+                        float(&d)[4] = sum[m][4 * j + i];
+                        d[0] = fmaf(c[0], f.x, d[0]), d[1] = fmaf(c[1], f.x, d[1]);
+                        d[2] = fmaf(c[2], f.y, d[2]), d[3] = fmaf(c[3], f.y, d[3]);
+                    }
                 }
             }
         }
+        if (--sum_left == 0) sum_left = per, sum_s += s_rows * p.ld_s;
         stage = stage + 1 == S::STAGES ? 0 : stage + 1;
     }
     copy_wait<0>();
@@ -341,45 +436,48 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 2 : 1) k_matvec(const M
             f1 = power(__shfl_sync(0xffffffffu, exponent[m], 8 * t + 4));
         }
         __syncthreads();
-        float* const mine = part + warp * 8 * kPitch;
+        // columns lie 34 floats apart for every 32 of the tile
+        float* const mine = part + warp % S::KW * 8 * kPitch;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int n = g * 34 + 2 * i;
+        for (int i = 0; i < TILES; ++i) {
+            const int col = warp / S::KW * S::CW + g * 2 * TILES + 2 * i, n = (col >> 5) * 34 + (col & 31);
             const float(&d)[4] = sum[m][i];
             *reinterpret_cast<float2*>(mine + (2 * t) * kPitch + n) = make_float2(d[0] * f0, d[2] * f0);
             *reinterpret_cast<float2*>(mine + (2 * t + 1) * kPitch + n) = make_float2(d[1] * f1, d[3] * f1);
         }
         __syncthreads();
-        const int n = threadIdx.x, at = (n >> 5) * 34 + (n & 31);
+        const int n = threadIdx.x, at = (n >> 5) * 34 + (n & 31);  // the first 256 threads take a column each
+        const bool adds = n < kCols;
         float v[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
             v[r] = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) v[r] += part[(w * 8 + r) * kPitch + at];
+            for (int w = 0; w < S::KW && adds; ++w) v[r] += part[(w * 8 + r) * kPitch + at];
         }
         if (p.ranks > 1) {
             __syncthreads();
 #pragma unroll
-            for (int r = 0; r < 8; ++r) part[r * kPitch + at] = v[r];
+            for (int r = 0; r < 8; ++r)
+                if (adds) part[r * kPitch + at] = v[r];
             sbt_ptx::cluster_sync();
         }
         auto put = [&](int r, float x) {
             const int64_t tok = tok0 + m * 8 + r;
-            if (tok >= p.tokens || n0 + n >= p.N) return;
+            if (tok >= p.tokens || !adds || tile * kCols + n >= p.N) return;
             char* const y = p.y + tok * p.ld_y;
             x *= p.alpha;
             if (p.y_kind == kF32)
-                reinterpret_cast<float*>(y)[n0 + n] = x;
+                reinterpret_cast<float*>(y)[tile * kCols + n] = x;
             else
-                reinterpret_cast<uint16_t*>(y)[n0 + n] = p.y_kind == kBF16 ? Num<kBF16>::put(x) : Num<kF16>::put(x);
+                reinterpret_cast<uint16_t*>(y)[tile * kCols + n] = p.y_kind == kBF16 ? Num<kBF16>::put(x) : Num<kF16>::put(x);
         };
         if (p.ranks == 1) {
 #pragma unroll
             for (int r = 0; r < 8; ++r) put(r, v[r]);
         } else {
             const uint32_t from = sbt_ptx::smem_u32(part + at);
-            for (int r = rank; r < 8 && tok0 + m * 8 + r < p.tokens; r += p.ranks) {
+            for (int r = rank; adds && r < 8 && tok0 + m * 8 + r < p.tokens; r += p.ranks) {
                 float x = 0.f;
                 for (int q = 0; q < p.ranks; ++q) {
                     float part_q;
@@ -396,20 +494,22 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 2 : 1) k_matvec(const M
     }
 }
 
-template <int KIND, int U, bool E4M3, int MT, bool ALIGNED>
+template <int KIND, int U, int SU, bool E4M3, int MT, bool ALIGNED>
 sbt_status launch(sbt_context* ctx, MatvecParams& p, cudaStream_t stream) {
-    constexpr auto kern = k_matvec<KIND, U, E4M3, MT, ALIGNED>;
-    constexpr size_t smem = Shape<KIND, U, ALIGNED>::SMEM;
-    const int slots = sbt_resident_blocks<kern>(ctx, 32 * kWarps, smem);
-    const int64_t tiles = sbt_cdiv(p.N, kCols), chunks = sbt_cdiv(p.tokens, 8 * MT), units = p.K / U;
+    constexpr auto kern = k_matvec<KIND, U, SU, E4M3, MT, ALIGNED>;
+    typedef Shape<U, SU, MT, ALIGNED> S;
+    constexpr size_t smem = S::SMEM;
+    const int slots = sbt_resident_blocks<kern>(ctx, 32 * S::WARPS, smem);
+    const int64_t tiles = sbt_cdiv(p.N, kCols), chunks = sbt_cdiv(p.tokens, 8 * MT), stages = p.K / S::ROWS;
     // Blocks per tile: the number with which the last wave's end comes first.
     int64_t best = INT64_MAX;
-    for (int c = 1; c <= kClusterMost && (c == 1 || c * kWarps <= units); ++c) {
-        const int64_t cost = sbt_cdiv(tiles * chunks * c, slots) * (sbt_cdiv(units, (int64_t)c * kWarps) + kFixedStages);
+    for (int c = 1; c <= kClusterMost && (c == 1 || c * S::KW <= stages); ++c) {
+        const int64_t cost = sbt_cdiv(tiles * chunks * c, slots) *
+                             (sbt_cdiv(stages, (int64_t)c * S::KW) * S::ROWS + kFixedRows);
         if (cost < best) best = cost, p.ranks = c;
     }
     if (sbt_status st = sbt_cuda_check(
-            sbt_launch_dependent_cluster(kern, dim3((unsigned)(tiles * p.ranks), (unsigned)chunks), dim3(32 * kWarps),
+            sbt_launch_dependent_cluster(kern, dim3((unsigned)(tiles * p.ranks), (unsigned)chunks), dim3(32 * S::WARPS),
                                          (unsigned)p.ranks, smem, stream, p),
             "matvec_e2m1 launch"))
         return st;
@@ -417,19 +517,21 @@ sbt_status launch(sbt_context* ctx, MatvecParams& p, cudaStream_t stream) {
 }
 
 template <int KIND, int U, bool E4M3, int MT>
-sbt_status pick_aligned(sbt_context* ctx, MatvecParams& p, cudaStream_t stream) {
-    return sbt_aligned16(p.w) && p.ld_w % 16 == 0 ? launch<KIND, U, E4M3, MT, true>(ctx, p, stream)
-                                                  : launch<KIND, U, E4M3, MT, false>(ctx, p, stream);
+sbt_status pick_stage(sbt_context* ctx, MatvecParams& p, cudaStream_t stream) {
+    const bool aligned = sbt_aligned16(p.w) && p.ld_w % 16 == 0;
+    // (neither fp32 nor 16 rows leave registers for 64 k of x)
+    if constexpr (KIND != kF32 && MT == 1)
+        if (p.K % 64 == 0 && (p.group % 64 == 0 || 64 % p.group == 0) && aligned)
+            return launch<KIND, U, 64 / U, E4M3, MT, true>(ctx, p, stream);
+    return aligned ? launch<KIND, U, 1, E4M3, MT, true>(ctx, p, stream) : launch<KIND, U, 1, E4M3, MT, false>(ctx, p, stream);
 }
 
-template <int KIND>
-sbt_status pick(sbt_context* ctx, MatvecParams& p, bool e4m3, cudaStream_t stream) {
-    p.x_vec = ((uintptr_t)p.x | (uintptr_t)p.ld_x) % (KIND == kF32 ? 16 : 8) == 0;
+template <int KIND, bool E4M3>
+sbt_status pick(sbt_context* ctx, MatvecParams& p, cudaStream_t stream) {
     const bool wide = p.group % 32 == 0, two = p.tokens > 8;
-    if (wide && e4m3) return two ? pick_aligned<KIND, 32, true, 2>(ctx, p, stream) : pick_aligned<KIND, 32, true, 1>(ctx, p, stream);
-    if (wide) return two ? pick_aligned<KIND, 32, false, 2>(ctx, p, stream) : pick_aligned<KIND, 32, false, 1>(ctx, p, stream);
-    if (e4m3) return two ? pick_aligned<KIND, 16, true, 2>(ctx, p, stream) : pick_aligned<KIND, 16, true, 1>(ctx, p, stream);
-    return two ? pick_aligned<KIND, 16, false, 2>(ctx, p, stream) : pick_aligned<KIND, 16, false, 1>(ctx, p, stream);
+    p.x_vec = ((uintptr_t)p.x | (uintptr_t)p.ld_x) % (KIND != kF32 && !wide ? 8 : 16) == 0;
+    if (wide) return two ? pick_stage<KIND, 32, E4M3, 2>(ctx, p, stream) : pick_stage<KIND, 32, E4M3, 1>(ctx, p, stream);
+    return two ? pick_stage<KIND, 16, E4M3, 2>(ctx, p, stream) : pick_stage<KIND, 16, E4M3, 1>(ctx, p, stream);
 }
 
 }  // namespace
@@ -446,8 +548,8 @@ sbt_status sbt_launch_matvec(sbt_context* ctx, sbt_dtype dtype, const SbtRows& x
     p.tokens = tokens, p.N = N, p.K = K, p.group = K ? K / K_s : 32;
     p.alpha = alpha, p.y_kind = kind_of(y_dtype);
     switch (kind_of(dtype)) {
-        case kF32: return pick<kF32>(ctx, p, e4m3_scales, stream);
-        case kBF16: return pick<kBF16>(ctx, p, e4m3_scales, stream);
-        default: return pick<kF16>(ctx, p, e4m3_scales, stream);
+        case kF32: return e4m3_scales ? pick<kF32, true>(ctx, p, stream) : pick<kF32, false>(ctx, p, stream);
+        case kBF16: return e4m3_scales ? pick<kBF16, true>(ctx, p, stream) : pick<kBF16, false>(ctx, p, stream);
+        default: return e4m3_scales ? pick<kF16, true>(ctx, p, stream) : pick<kF16, false>(ctx, p, stream);
     }
 }
