@@ -126,25 +126,59 @@ __device__ __forceinline__ float larger(float a, float b) {
     return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
 }
 
-template <int KIND, int W, int NV, bool CODES>
+// SHIFT: rows that start anywhere, but all arrays' at the same place relative to 16 bytes.  Units are counted from the
+// boundary before the row, so that all but its first and last are vectors; the weights are read element by element.
+template <int KIND, int W, int NV, bool CODES, bool SHIFT>
 __global__ void __launch_bounds__(W * NV == 32 ? 512 : 1024) k_add_norm(const NormParams p) {
     typedef Unit<KIND, W> U;
-    constexpr int ES = sizeof(typename Num<KIND>::T), B = W * ES;
+    typedef typename Num<KIND>::T T;
+    constexpr int ES = sizeof(T), B = W * ES;
+    // weights before the sum where registers allow, under it (from L2) otherwise: 16384 x 8192 bf16 to codes 202 and 161 us
+    constexpr bool EARLY = !SHIFT && W * NV < 32;
     __shared__ float s_sum[32][1];
     griddep_wait();
     const int G = p.group, j = threadIdx.x & (G - 1);
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
     if (row >= p.rows) return;  // whole warps: a block of several rows has a warp for each
-    const int units = p.cols / W;
+    const int phase = SHIFT ? (int)((reinterpret_cast<uintptr_t>(p.x + row * p.ld_x) & (B - 1)) / ES) : 0;
+    const int units = SHIFT ? (p.cols + phase + W - 1) / W : p.cols / W;
+    // unit u of an array's row; in the first and the last of a shifted row the elements that there are
+    auto load = [&](U& x, const char* at, int u) {
+        const int e = u * W - phase;
+        if (!SHIFT || (e >= 0 && e + W <= p.cols)) {
+            x.load(at + (int64_t)e * ES);
+        } else {
+            x.zero();
+            for (int k = 0; k < W; ++k)
+                if (e + k >= 0 && e + k < p.cols) reinterpret_cast<T*>(&x)[k] = sbt_ld(reinterpret_cast<const T*>(at) + e + k);
+        }
+    };
+    auto store = [&](char* at, int u, const float* x) {
+        const int e = u * W - phase;
+        if (!SHIFT || (e >= 0 && e + W <= p.cols)) {
+            U::store(at + (int64_t)e * ES, x);
+        } else {
+#pragma unroll
+            for (int k = 0; k < W; ++k)
+                if (e + k >= 0 && e + k < p.cols) reinterpret_cast<T*>(at)[e + k] = Num<KIND>::put(x[k]);
+        }
+    };
+    auto weights = [&](float (&t)[W], int u) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const int e = u * W - phase + k;
+            t[k] = e >= 0 && e < p.cols ? Num<KIND>::get(sbt_ld(reinterpret_cast<const T*>(p.w) + e)) : 0.f;
+        }
+    };
     U a[NV], b[NV], w[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int u = j + i * G;
         a[i].zero(), b[i].zero();
         if (u < units) {
-            a[i].load(p.x + row * p.ld_x + (int64_t)u * B);
-            if (p.r) b[i].load(p.r + row * p.ld_r + (int64_t)u * B);
-            if (p.w) w[i].load(p.w + (int64_t)u * B);
+            load(a[i], p.x + row * p.ld_x, u);
+            if (p.r) load(b[i], p.r + row * p.ld_r, u);
+            if (EARLY && p.w) w[i].load(p.w + (int64_t)u * B);
         }
     }
     float h[NV][W], sum[1] = {0.f};
@@ -160,23 +194,30 @@ __global__ void __launch_bounds__(W * NV == 32 ? 512 : 1024) k_add_norm(const No
 #pragma unroll
         for (int k = 0; k < W; ++k) sum[0] += h[i][k] * h[i][k];
     }
+    if (!EARLY && !SHIFT && p.w)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (j + i * G < units) w[i].load(p.w + (int64_t)(j + i * G) * B);
     row_sums(sum, G, s_sum);
     const float s = 1.f / sqrtf(sum[0] / (float)p.cols + p.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int u = j + i * G;
         const bool ok = u < units;
-        if (ok && p.h) U::store(p.h + row * p.ld_h + (int64_t)u * B, h[i]);
+        if (ok && p.h) store(p.h + row * p.ld_h, u, h[i]);
         if (p.w) {
             float t[W];
-            w[i].get(t);
+            if constexpr (SHIFT)
+                weights(t, u);
+            else
+                w[i].get(t);
 #pragma unroll
             for (int k = 0; k < W; ++k) h[i][k] = h[i][k] * s * t[k];
         } else {
 #pragma unroll
             for (int k = 0; k < W; ++k) h[i][k] *= s;
         }
-        if (ok && p.y) U::store(p.y + row * p.ld_y + (int64_t)u * B, h[i]);
+        if (ok && p.y) store(p.y + row * p.ld_y, u, h[i]);
         if constexpr (CODES) {
             float top = 0.f;
 #pragma unroll
@@ -412,7 +453,7 @@ int threads_for(int64_t units, int most) {
     return g;
 }
 
-template <int KIND, int W, int NV>
+template <int KIND, int W, int NV, bool SHIFT = false>
 sbt_status launch_forward(sbt_context* ctx, NormParams& p, int G, cudaStream_t stream) {
     p.group = G;
     const int threads = std::max(G, 128), per = threads / G;
@@ -420,9 +461,9 @@ sbt_status launch_forward(sbt_context* ctx, NormParams& p, int G, cudaStream_t s
     const int block = G > 32 ? G : threads;
     cudaError_t e;
     if (W == 8 && p.codes)
-        e = sbt_launch_dependent(k_add_norm<KIND, W, NV, W == 8>, dim3((unsigned)grid), dim3(block), 0, stream, p);
+        e = sbt_launch_dependent(k_add_norm<KIND, W, NV, W == 8 && !SHIFT, SHIFT>, dim3((unsigned)grid), dim3(block), 0, stream, p);
     else
-        e = sbt_launch_dependent(k_add_norm<KIND, W, NV, false>, dim3((unsigned)grid), dim3(block), 0, stream, p);
+        e = sbt_launch_dependent(k_add_norm<KIND, W, NV, false, SHIFT>, dim3((unsigned)grid), dim3(block), 0, stream, p);
     if (sbt_status st = sbt_cuda_check(e, "add_rms_norm launch")) return st;
     return sbt_after_launch(ctx, "add_rms_norm");
 }
@@ -438,6 +479,16 @@ sbt_status forward(sbt_context* ctx, NormParams& p, cudaStream_t stream) {
         if (units <= G) return launch_forward<KIND, 8, 1>(ctx, p, G, stream);
         if (units <= 2 * G) return launch_forward<KIND, 8, 2>(ctx, p, G, stream);
         return launch_forward<KIND, 8, 4>(ctx, p, G, stream);
+    }
+    // the same phase everywhere: rows a whole number of vectors apart in all arrays, or equally far and equally placed
+    constexpr int B = 8 * (KIND == kF32 ? 4 : 2);
+    auto like_x = [&](const void* q, int64_t ld) {
+        return !q || (((uintptr_t)q ^ (uintptr_t)p.x) % B == 0 && (ld - p.ld_x) % B == 0);
+    };
+    if (!p.codes && p.cols >= 64 && p.cols <= 8 * 2 * 1024 - 16 && like_x(p.r, p.ld_r) && like_x(p.h, p.ld_h) && like_x(p.y, p.ld_y)) {
+        const int units = p.cols / 8 + 2, G = threads_for(few ? units : sbt_cdiv(units, 2), 1024);
+        if (units <= G) return launch_forward<KIND, 8, 1, true>(ctx, p, G, stream);
+        return launch_forward<KIND, 8, 2, true>(ctx, p, G, stream);
     }
     if (!p.codes && p.cols <= 16 * 1024) {
         const int G = threads_for(sbt_cdiv(p.cols, few ? 4 : 16), 1024);
