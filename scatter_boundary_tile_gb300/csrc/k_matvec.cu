@@ -46,6 +46,7 @@ using sbt_ptx::griddep_wait;
 constexpr int kCols = 256, kClusterMost = 8;
 constexpr int kPitch = kCols + 20;  // floats between rows of partial sums: lanes of a half warp meet no bank twice
 constexpr int kFixedRows = 128;     // what a block costs besides its k, in k of a warp
+constexpr int kLineRows = 144;      // the same of a tile, and of a call, where blocks go from tile to tile
 
 struct MatvecParams {
     const char* x;
@@ -55,23 +56,27 @@ struct MatvecParams {
     int64_t tokens, N, K, group;
     float alpha;
     int32_t y_kind, ranks, x_vec;
+    int64_t items;               // LINE: tiles times eights (or sixteens) of tokens
+    int32_t chunks;
 };
 
 // U: k whose products are summed before they are scaled; SU: such units of a stage.
-template <int U, int SU, int MT, bool ALIGNED>
+template <int U, int SU, int MT, bool ALIGNED, bool LINE>
 struct Shape {
     static constexpr int ROWS = U * SU;
     // 16 rows of x: the sums fill twice the registers, and twelve warps an SM take the place of sixteen
-    static constexpr int WARPS = MT == 1 ? 8 : 12, BLOCKS = MT == 1 ? 2 : 1;
-    static constexpr int CW = 128, KW = WARPS * CW / kCols;  // columns of a warp, warps along k
+    static constexpr int BLOCKS = MT == 1 ? 2 : 1, WARPS = MT == 1 || LINE ? 8 : 12;
+    static constexpr int CW = 128, COLS = LINE ? CW : kCols, KW = WARPS * CW / COLS;  // columns of a warp and a block, warps along k
     static constexpr int LANE = CW / 16;                   // bytes of a row that a lane takes
     static constexpr int PITCH = ALIGNED ? CW / 2 : CW / 2 + 16;  // bytes of a row of weights in a stage
     static constexpr int SCALES = CW + 32;                 // a row of scales, from the 16-byte boundary before it
     static constexpr int STAGE = ROWS * PITCH + SU * SCALES;
-    static constexpr int MOST = (220 << 10) / (BLOCKS * WARPS * STAGE), STAGES = MOST < 8 ? MOST : 8;
+    static constexpr int CHAIN = LINE ? MT * 8 * 33 * 16 : 0;  // the running sums of a tile, 16 bytes of a lane beside another's
+    static constexpr int MOST = ((220 << 10) - CHAIN) / (BLOCKS * WARPS * STAGE), STAGES = MOST < 8 ? MOST : 8;
     static constexpr int RING = STAGES * STAGE;
     static constexpr int PART = 8 * kPitch * 4;            // sums of 256 columns
-    static constexpr size_t SMEM = (size_t)WARPS * RING > (size_t)KW * PART ? (size_t)WARPS * RING : (size_t)KW * PART;
+    static constexpr size_t SMEM = LINE ? (size_t)WARPS * RING + CHAIN
+                                        : (size_t)WARPS * RING > (size_t)KW * PART ? (size_t)WARPS * RING : (size_t)KW * PART;
     // Place of byte `c` of row r (aligned rows): lanes that read together, their rows U / 4 apart, meet no bank twice.
     static __device__ __forceinline__ int place(int r, int c) {
         const int key = r / (U / 4) & 3;
@@ -129,38 +134,58 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// KIND: of x.  MT: 8 rows of x each.
-template <int KIND, int U, int SU, bool E4M3, int MT, bool ALIGNED>
-__global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED>::WARPS, Shape<U, SU, MT, ALIGNED>::BLOCKS) k_matvec(const MatvecParams p) {
-    typedef Shape<U, SU, MT, ALIGNED> S;
+// A warp waits for the one before it, and lets the one after it go on (barriers of two warps).
+__device__ __forceinline__ void chain_wait(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void chain_pass(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); }
+
+// KIND: of x.  MT: 8 rows of x each.  LINE: a block goes from tile to tile.
+template <int KIND, int U, int SU, bool E4M3, int MT, bool ALIGNED, bool LINE>
+__global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED, LINE>::WARPS, Shape<U, SU, MT, ALIGNED, LINE>::BLOCKS)
+    k_matvec(const MatvecParams p) {
+    typedef Shape<U, SU, MT, ALIGNED, LINE> S;
     typedef typename Num<KIND>::T T;
     constexpr int WORDS = S::LANE / 4, TILES = 4 * WORDS;  // of a lane's piece of a row; matrix tiles of a warp
     constexpr int STEPS = U / 16, ROWS = S::ROWS, TERMS = KIND == kF32 ? 2 : 1;
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int rank = blockIdx.x % p.ranks;
-    const int64_t tile = blockIdx.x / p.ranks, tok0 = (int64_t)blockIdx.y * 8 * MT;
-    const int64_t n0 = tile * kCols + warp / S::KW * S::CW;
-    const int64_t stages = p.K / ROWS, workers = (int64_t)S::KW * p.ranks, me = (int64_t)rank * S::KW + warp % S::KW;
+    const int rank = LINE ? 0 : blockIdx.x % p.ranks;
+    const int64_t stages = p.K / ROWS, items = LINE ? p.items : 1;
+    // This warp's stages, of every tile; and a tile's columns and tokens.
+    const int64_t workers = LINE ? S::KW : (int64_t)S::KW * p.ranks, me = (int64_t)rank * S::KW + warp % S::KW;
     const int64_t u0 = stages * me / workers, u1 = stages * (me + 1) / workers;
+    const int todo = (int)(u1 - u0);
+    const int64_t first_item = LINE ? blockIdx.x : 0, step_item = LINE ? gridDim.x : 1;
+    auto columns = [&](int64_t item) {
+        return LINE ? item / p.chunks * S::COLS : (int64_t)(blockIdx.x / p.ranks) * S::COLS + warp / S::KW * S::CW;
+    };
+    auto tokens = [&](int64_t item) { return (LINE ? item % p.chunks : (int64_t)blockIdx.y) * 8 * MT; };
     uint8_t* const ring = smem + warp * S::RING;
     const uint32_t ring_u32 = sbt_ptx::smem_u32(ring);
     griddep_wait();
 
     // ---- copies: the warp's columns of a stage's rows and its group's scales, nothing past their ends
-    const int w_bytes = (int)max((int64_t)0, min((int64_t)(S::CW / 2), (p.N + 1) / 2 - n0 / 2));
-    const int s_bytes = (int)max((int64_t)0, min((int64_t)S::CW, p.N - n0));
     constexpr int LPR = S::CW / 32;                       // lanes of a row, 16 bytes each
     const int copy_c = ALIGNED ? lane % LPR * 16 : lane % (2 * LPR) * 16, copy_r = lane / (ALIGNED ? LPR : 2 * LPR);
-    const int copy_bytes = min(max(w_bytes - copy_c, 0), 16);
-    const uint8_t* copy_w = p.w + n0 / 2 + (u0 * ROWS + copy_r) * p.ld_w;
     // Rows of scales: one for `per` stages (of which `left` are still to come for the copies and for the sums), or
     // one for every unit of a stage.
     const bool each = p.group < ROWS;
     const int per = each ? 1 : (int)(p.group / ROWS), s_rows = each ? SU : 1;
-    const uint8_t *copy_s = p.s + (each ? u0 * SU : u0 / per) * p.ld_s + n0, *sum_s = copy_s;
-    int copy_left = per - (int)(u0 % per), sum_left = copy_left;
     const bool s_aligned = (((uintptr_t)p.s | (uintptr_t)p.ld_s) & 15) == 0;
+    int w_bytes, s_bytes, copy_bytes, copy_left, copy_todo;
+    int64_t copy_item = first_item;
+    const uint8_t *copy_w, *copy_s;
+    const int64_t s_row = each ? u0 * SU : u0 / per;
+    const int s_left = per - (int)(u0 - s_row * per);       // (not for `each`, whose `per` is one)
+    auto copy_start = [&] {
+        const int64_t n0 = columns(copy_item);
+        w_bytes = (int)max((int64_t)0, min((int64_t)(S::CW / 2), (p.N + 1) / 2 - n0 / 2));
+        s_bytes = (int)max((int64_t)0, min((int64_t)S::CW, p.N - n0));
+        copy_bytes = min(max(w_bytes - copy_c, 0), 16);
+        copy_w = p.w + n0 / 2 + (u0 * ROWS + copy_r) * p.ld_w;
+        copy_s = p.s + s_row * p.ld_s + n0;
+        copy_left = each ? 1 : s_left, copy_todo = todo;
+    };
+    copy_start();
     // places of this lane's rows of a stage, less what rows STEP apart are apart: they repeat after four
     constexpr int STEP = 32 / LPR;
     uint32_t at_place[4];
@@ -168,6 +193,12 @@ __global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED>::WARPS, Shape<U
     for (int i = 0; i < 4; ++i) at_place[i] = S::place(i * STEP + copy_r, copy_c) - i * STEP * 64;
     const int64_t w_step = STEP * p.ld_w;
     auto copy = [&](int stage) {  // the next stage's
+        if (copy_todo == 0) {
+            if (!LINE || todo == 0 || copy_item + step_item >= items) return;
+            copy_item += step_item;
+            copy_start();
+        }
+        --copy_todo;
         const uint32_t dst = ring_u32 + stage * S::STAGE;
         const uint8_t* src = copy_w;
         copy_w += ROWS * p.ld_w;
@@ -209,17 +240,30 @@ __global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED>::WARPS, Shape<U
         T v[XK];
     };
     const T* x_at[MT];
+    int x_todo;
+    int64_t x_item = first_item;
+    auto x_start = [&] {
+        const int64_t tok = tokens(x_item) + g;
+        x_todo = todo;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-        x_at[m] = tok0 + m * 8 + g < p.tokens
-                      ? reinterpret_cast<const T*>(p.x + (tok0 + m * 8 + g) * p.ld_x) + u0 * ROWS + t * XK : nullptr;
-    auto load_x = [&](int64_t u, Raw (&r)[SU][MT]) {
+        for (int m = 0; m < MT; ++m)
+            x_at[m] = tok + m * 8 < p.tokens
+                          ? reinterpret_cast<const T*>(p.x + (tok + m * 8) * p.ld_x) + u0 * ROWS + t * XK : nullptr;
+    };
+    x_start();
+    auto load_x = [&](Raw (&r)[SU][MT]) {
+        if (x_todo == 0) {
+            if (!LINE || todo == 0 || x_item + step_item >= items) return;
+            x_item += step_item;
+            x_start();
+        }
+        --x_todo;
 #pragma unroll
         for (int q = 0; q < SU; ++q)
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const T* const a = x_at[m] + q * U;
-                if (u >= u1 || !x_at[m]) {
+                if (!x_at[m]) {
                     r[q][m] = Raw{};
                 } else if (p.x_vec) {
                     if constexpr (sizeof(T) * XK >= 16) {
@@ -239,6 +283,19 @@ __global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED>::WARPS, Shape<U
             if (x_at[m]) x_at[m] += ROWS;
     };
 
+    Raw raw[SU][MT];
+    load_x(raw);
+#pragma unroll 1
+    for (int i = 0; i < S::STAGES - 1; ++i) {
+        copy(i);
+        copy_commit();
+    }
+    int stage = 0;
+#pragma unroll 1
+    for (int64_t item = first_item; item < items; item += step_item) {
+    const int64_t n0 = columns(item), tok0 = tokens(item);
+    const uint8_t* sum_s = p.s + s_row * p.ld_s + n0;
+    int sum_left = each ? 1 : s_left;
     float sum[MT][TILES][4];  // columns g * 2 * TILES + 2 i, + 1; rows 2 t, + 1 of x
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -250,19 +307,11 @@ __global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED>::WARPS, Shape<U
 #pragma unroll
     for (int m = 0; m < MT; ++m) exponent[m] = -126;
 
-    Raw raw[SU][MT];
-    load_x(u0, raw);
 #pragma unroll 1
-    for (int i = 0; i < S::STAGES - 1; ++i) {
-        if (u0 + i < u1) copy(i);
-        copy_commit();
-    }
-    int stage = 0;
-#pragma unroll 1
-    for (int64_t u = u0; u < u1; ++u) {
+    for (int n = todo; n > 0; --n) {
         copy_wait<S::STAGES - 2>();
         __syncwarp();
-        if (u + S::STAGES - 1 < u1) copy(stage == 0 ? S::STAGES - 1 : stage - 1);
+        copy(stage == 0 ? S::STAGES - 1 : stage - 1);
         copy_commit();
 
         // x as fp16 pairs along k
@@ -312,8 +361,8 @@ __global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED>::WARPS, Shape<U
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const int want = max(top - 127 - 14, -126);
                 if (__any_sync(0xffffffffu, want > exponent[m])) {
-                    const int now = max(want, exponent[m]), gap = min(now - exponent[m], 127);
-                    exponent[m] = now;
+                    const int top_e = max(want, exponent[m]), gap = min(top_e - exponent[m], 127);
+                    exponent[m] = top_e;
                     // the rows of the sums are 2 t and 2 t + 1, held by lanes 8 t and 8 t + 4
                     const float f0 = power(-__shfl_sync(0xffffffffu, gap, 8 * t));
                     const float f1 = power(-__shfl_sync(0xffffffffu, gap, 8 * t + 4));
@@ -340,7 +389,7 @@ __global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED>::WARPS, Shape<U
                     }
             }
         }
-        load_x(u + 1, raw);
+        load_x(raw);
 
         const uint8_t* const st = ring + stage * S::STAGE;
 #pragma unroll
@@ -356,7 +405,7 @@ __global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED>::WARPS, Shape<U
                         const uint2 v = *reinterpret_cast<const uint2*>(st + S::place(row, g * S::LANE));
                         w[s][r][0] = v.x, w[s][r][1] = v.y;
                     } else {
-                        const int shift = (int)((uintptr_t)(p.w + (u * ROWS + row) * p.ld_w + n0 / 2) & 15);
+                        const int shift = (int)((uintptr_t)(p.w + ((u1 - n) * ROWS + row) * p.ld_w + n0 / 2) & 15);
                         const uint32_t* const a =
                             reinterpret_cast<const uint32_t*>(st + row * S::PITCH + g * S::LANE + (shift & ~3));
                         uint32_t c = a[0];
@@ -424,9 +473,63 @@ __global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED>::WARPS, Shape<U
         if (--sum_left == 0) sum_left = per, sum_s += s_rows * p.ld_s;
         stage = stage + 1 == S::STAGES ? 0 : stage + 1;
     }
+    // ---- from tile to tile: the warps add their sums to one buffer in their order, each when the one before it has; the
+    // last writes y and lets the first go on.  (A warp passes again only after the next one has waited: all of them
+    // have then added, and the last has let the first go on.)
+    if constexpr (LINE) {
+        float* const buf = reinterpret_cast<float*>(smem + S::WARPS * S::RING);
+        if (warp > 0 || item != first_item) chain_wait(warp > 0 ? warp - 1 : S::KW - 1);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            float f0 = 1.f, f1 = 1.f;
+            if (KIND != kF16) {
+                f0 = power(__shfl_sync(0xffffffffu, exponent[m], 8 * t));
+                f1 = power(__shfl_sync(0xffffffffu, exponent[m], 8 * t + 4));
+            }
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) {
+                const float(&d)[4] = sum[m][i];
+                float4* const at = reinterpret_cast<float4*>(buf) + (m * 8 + i) * 33 + lane;
+                float4 v = make_float4(d[0] * f0, d[1] * f1, d[2] * f0, d[3] * f1);
+                if (warp > 0) {
+                    const float4 w = *at;
+                    v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+                }
+                *at = v;
+            }
+        }
+        __syncwarp();
+        if (warp < S::KW - 1) {
+            chain_pass(warp);
+        } else {
+#pragma unroll 1
+            for (int r = 0; r < 8 * MT && tok0 + r < p.tokens; ++r) {
+                char* const y = p.y + (tok0 + r) * p.ld_y;
+                float v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = 32 * j + lane;
+                    v[j] = p.alpha * buf[((r / 8 * 8 + c % 16 / 2) * 33 + c / 16 * 4 + r % 8 / 2) * 4 + c % 2 * 2 + r % 2];
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t n = n0 + 32 * j + lane;
+                    if (n >= p.N) break;
+                    if (p.y_kind == kF32)
+                        reinterpret_cast<float*>(y)[n] = v[j];
+                    else
+                        reinterpret_cast<uint16_t*>(y)[n] = p.y_kind == kBF16 ? Num<kBF16>::put(v[j]) : Num<kF16>::put(v[j]);
+                }
+            }
+            __syncwarp();
+            if (item + step_item < items) chain_pass(S::KW - 1);
+        }
+        continue;
+    }
     copy_wait<0>();
 
     // ---- the warps' sums, then the blocks': a block finishes every p.ranks-th row
+    const int64_t tile = blockIdx.x / p.ranks;
     float* const part = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -492,25 +595,39 @@ __global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED>::WARPS, Shape<U
             sbt_ptx::cluster_sync();  // nobody leaves, or writes the next rows' sums, while another reads
         }
     }
+    }
 }
 
-template <int KIND, int U, int SU, bool E4M3, int MT, bool ALIGNED>
+template <int KIND, int U, int SU, int SL, bool E4M3, int MT, bool ALIGNED>
 sbt_status launch(sbt_context* ctx, MatvecParams& p, cudaStream_t stream) {
-    constexpr auto kern = k_matvec<KIND, U, SU, E4M3, MT, ALIGNED>;
-    typedef Shape<U, SU, MT, ALIGNED> S;
-    constexpr size_t smem = S::SMEM;
-    const int slots = sbt_resident_blocks<kern>(ctx, 32 * S::WARPS, smem);
+    constexpr auto kern = k_matvec<KIND, U, SU, E4M3, MT, ALIGNED, false>;
+    typedef Shape<U, SU, MT, ALIGNED, false> S;
     const int64_t tiles = sbt_cdiv(p.N, kCols), chunks = sbt_cdiv(p.tokens, 8 * MT), stages = p.K / S::ROWS;
     // Blocks per tile: the number with which the last wave's end comes first.
     int64_t best = INT64_MAX;
     for (int c = 1; c <= kClusterMost && (c == 1 || c * S::KW <= stages); ++c) {
-        const int64_t cost = sbt_cdiv(tiles * chunks * c, slots) *
-                             (sbt_cdiv(stages, (int64_t)c * S::KW) * S::ROWS + kFixedRows);
+        const int64_t waves = sbt_cdiv(tiles * chunks, sbt_resident_clusters<kern>(ctx, 32 * S::WARPS, S::SMEM, c));
+        const int64_t cost = waves * (sbt_cdiv(stages, (int64_t)c * S::KW) * S::ROWS + kFixedRows);
         if (cost < best) best = cost, p.ranks = c;
+    }
+    if constexpr (ALIGNED && MT == 2) {
+        constexpr auto line = k_matvec<KIND, U, SL, E4M3, MT, true, true>;
+        typedef Shape<U, SL, MT, true, true> L;
+        p.items = sbt_cdiv(p.N, L::COLS) * chunks, p.chunks = (int32_t)chunks;
+        const int blocks = sbt_resident_blocks<line>(ctx, 32 * L::WARPS, L::SMEM);
+        const int64_t waves = sbt_cdiv(p.items, blocks);
+        const int64_t cost = waves * (sbt_cdiv(p.K / L::ROWS, L::KW) * L::ROWS + kLineRows) + kLineRows;
+        if (cost * (SL > SU ? 10 : 13) < best * 18) {
+            if (sbt_status st = sbt_cuda_check(sbt_launch_dependent(line, dim3((unsigned)std::min<int64_t>(p.items, blocks)),
+                                                                    dim3(32 * L::WARPS), L::SMEM, stream, p),
+                                               "matvec_e2m1 launch"))
+                return st;
+            return sbt_after_launch(ctx, "matvec_e2m1");
+        }
     }
     if (sbt_status st = sbt_cuda_check(
             sbt_launch_dependent_cluster(kern, dim3((unsigned)(tiles * p.ranks), (unsigned)chunks), dim3(32 * S::WARPS),
-                                         (unsigned)p.ranks, smem, stream, p),
+                                         (unsigned)p.ranks, S::SMEM, stream, p),
             "matvec_e2m1 launch"))
         return st;
     return sbt_after_launch(ctx, "matvec_e2m1");
@@ -519,11 +636,12 @@ sbt_status launch(sbt_context* ctx, MatvecParams& p, cudaStream_t stream) {
 template <int KIND, int U, bool E4M3, int MT>
 sbt_status pick_stage(sbt_context* ctx, MatvecParams& p, cudaStream_t stream) {
     const bool aligned = sbt_aligned16(p.w) && p.ld_w % 16 == 0;
-    // (neither fp32 nor 16 rows leave registers for 64 k of x)
-    if constexpr (KIND != kF32 && MT == 1)
+    // (neither fp32 nor 16 rows beside eleven other warps leave registers for 64 k of x)
+    constexpr int FEW = MT == 1 ? 64 / U : 1;
+    if constexpr (KIND != kF32)
         if (p.K % 64 == 0 && (p.group % 64 == 0 || 64 % p.group == 0) && aligned)
-            return launch<KIND, U, 64 / U, E4M3, MT, true>(ctx, p, stream);
-    return aligned ? launch<KIND, U, 1, E4M3, MT, true>(ctx, p, stream) : launch<KIND, U, 1, E4M3, MT, false>(ctx, p, stream);
+            return launch<KIND, U, FEW, 64 / U, E4M3, MT, true>(ctx, p, stream);
+    return aligned ? launch<KIND, U, 1, 1, E4M3, MT, true>(ctx, p, stream) : launch<KIND, U, 1, 1, E4M3, MT, false>(ctx, p, stream);
 }
 
 template <int KIND, bool E4M3>

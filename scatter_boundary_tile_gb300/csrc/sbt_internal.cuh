@@ -262,6 +262,35 @@ int sbt_resident_blocks(const sbt_context* ctx, int threads, size_t smem) {
     return v;
 }
 
+// Clusters of `ranks` (at most 8) such blocks that the device holds at once; fewer than its blocks make, since a
+// cluster lies within one group of SMs.
+template <auto KERN>
+int sbt_resident_clusters(const sbt_context* ctx, int threads, size_t smem, int ranks) {
+    const int blocks = sbt_resident_blocks<KERN>(ctx, threads, smem);
+    if (ranks == 1) return blocks;
+    static std::atomic<int> known[64][8];
+    std::atomic<int>& n = known[ctx->device & 63][ranks - 1];
+    int v = n.load(std::memory_order_relaxed);
+    if (v == 0) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)ranks;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)ranks);
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&v, (const void*)KERN, &cfg) != cudaSuccess || v < 1) {
+            (void)cudaGetLastError();
+            v = blocks / ranks > 0 ? blocks / ranks : 1;
+        }
+        n.store(v, std::memory_order_relaxed);
+    }
+    return v;
+}
+
 // Checks the launch that was just enqueued and counts it.
 sbt_status sbt_after_launch(sbt_context* ctx, const char* what);
 

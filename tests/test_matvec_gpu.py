@@ -234,3 +234,30 @@ def test_same_bits_and_the_gemm_agrees(ctx):
                           workspace_bytes=need, a_fmt="e4m3", b_fmt="e2m1")
     _, mag = ref.matvec(ref.f64(c.xv), ref.unpack_e2m1(c.packed, 1024, 640, 640), ref.code_values(c.scales, "e8m0"), 32, 1.0)
     assert (np.abs(ref.f64(D) - first) <= 2 * (1024 + 64) * 2.0**-23 * mag).all()
+
+
+# More columns than there are blocks for: a block goes from tile to tile.  The rows of weights are whole multiples of 16
+# bytes, the numbers of columns and the rows of scales are not.
+WIDE = [("bf16", "e8m0", 32), ("f16", "e4m3", 16), ("f32", "e4m3", 32), ("bf16", "e8m0", 160)]
+
+
+@pytest.mark.parametrize("kind,scale,group", WIDE)
+@pytest.mark.parametrize("tokens", [1, 9, 35])
+@pytest.mark.parametrize("K,N", [(320, 40000), (480, 60001), (1280, 39999)])
+def test_many_columns(ctx, K, N, tokens, kind, scale, group):
+    pad = -((N + 1) // 2) % 16
+    Case(K + tokens, kind, tokens, K, N, scale, group, alpha=0.75, pad=(0, pad, N % 2 * 3, N % 2)).check(ctx)
+
+
+@pytest.mark.parametrize("tokens", [2, 16])
+@pytest.mark.parametrize("K", [32, 64, 96])
+def test_many_columns_of_little_k(ctx, K, tokens):
+    """Fewer stages than warps: some of them have nothing to add."""
+    Case(K, "bf16", tokens, K, 80000, out="f32").check(ctx)
+
+
+@pytest.mark.parametrize("tokens", [1, 16])
+def test_many_columns_twice(ctx, tokens):
+    """The order of the sums is fixed."""
+    case = Case(3, "bf16", tokens, 1024, 50016, out="f32")
+    assert np.array_equal(case.run(ctx), case.run(ctx))
