@@ -1029,7 +1029,7 @@ template <int KIND, int DP, int MT>
 __global__ void __launch_bounds__(kJoin) k_tree_join(const TreeAttnParams p, int32_t pieces, int32_t groups) {
     constexpr int R = MT * kRows;
     __shared__ float4 s_o[kJoin];
-    __shared__ float s_l[kJoin], s_top[32];
+    __shared__ float s_l[kJoin], s_top[kJoin];
     griddep_wait();
     const TreeDesc e = p.desc[blockIdx.x / pieces];
     if (!e.valid) return;
@@ -1041,32 +1041,47 @@ __global__ void __launch_bounds__(kJoin) k_tree_join(const TreeAttnParams p, int
     const int r = min(r0 + lane, row.count - 1);
     auto slot = [&](int32_t i) -> int64_t { return 2ll * (e.first + i) + (i == 0 ? e.first_slot : 0); };
     const int32_t n = e.last - e.first + 1;
-    float top = -CUDART_INF_F;
-#pragma unroll 8
-    for (int32_t i = 0; i < n; ++i) top = fmaxf(top, sbt_ld(p.part_ml + slot(i) * R + r).x);
-    const float ts = top == -CUDART_INF_F ? 0.f : top;
-    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int32_t i = group; i < n; i += groups) {
-        const float2 ml = sbt_ld(p.part_ml + slot(i) * R + r);
-        const float4 x = sbt_ld(p.part_o + (slot(i) * (DP / 4) + quad) * R + r);
-        const float a = sbt_attn::exp2_fast(ml.x - ts);
-        l += ml.y * a;
-        o[0] += x.x * a, o[1] += x.y * a, o[2] += x.z * a, o[3] += x.w * a;
+    float top = -CUDART_INF_F, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int BATCH = 8;  // parts on their way at once
+    for (int32_t first = group; first < n; first += BATCH * groups) {
+        float2 ml[BATCH];
+        float4 x[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int32_t i = first + j * groups;
+            ml[j] = make_float2(-CUDART_INF_F, 0.f), x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i >= n) continue;
+            ml[j] = sbt_ld(p.part_ml + slot(i) * R + r);
+            x[j] = sbt_ld(p.part_o + (slot(i) * (DP / 4) + quad) * R + r);
+        }
+        const float was = top;
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) top = fmaxf(top, ml[j].x);
+        const float ts = top == -CUDART_INF_F ? 0.f : top, f = sbt_attn::exp2_fast(was - ts);
+        l *= f, o[0] *= f, o[1] *= f, o[2] *= f, o[3] *= f;
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const float a = sbt_attn::exp2_fast(ml[j].x - ts);
+            l += ml[j].y * a;
+            o[0] += x[j].x * a, o[1] += x[j].y * a, o[2] += x[j].z * a, o[3] += x[j].w * a;
+        }
     }
     s_o[threadIdx.x] = make_float4(o[0], o[1], o[2], o[3]);
     s_l[threadIdx.x] = l;
-    if (warp == 0) s_top[lane] = top;
+    s_top[threadIdx.x] = top;
     __syncthreads();
     // neighbouring threads write neighbouring vectors of a row
     const int mine = threadIdx.x / quads, q = threadIdx.x % quads;
     if (threadIdx.x >= 32 * quads || r0 + mine >= row.count) return;
-    l = 0.f, o[0] = o[1] = o[2] = o[3] = 0.f;
+    l = 0.f, o[0] = o[1] = o[2] = o[3] = 0.f, top = -CUDART_INF_F;
+    for (int i = 0; i < groups; ++i) top = fmaxf(top, s_top[(q * groups + i) * 32 + mine]);
+    const float ts = top == -CUDART_INF_F ? 0.f : top;
     for (int i = 0; i < groups; ++i) {
         const int from = (q * groups + i) * 32 + mine;
         const float4 x = s_o[from];
-        l += s_l[from];
-        o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w;
+        const float a = sbt_attn::exp2_fast(s_top[from] - ts);
+        l += s_l[from] * a;
+        o[0] += x.x * a, o[1] += x.y * a, o[2] += x.z * a, o[3] += x.w * a;
     }
     const uint32_t rr = (uint32_t)((int64_t)e.plane * R + r0 + mine), i = sbt_div(p.group, rr);
     const int32_t qh = e.h * (int32_t)p.group.d + (int32_t)(rr - i * p.group.d), d = (quad - warp / groups + q) * 4;
@@ -1080,7 +1095,7 @@ __global__ void __launch_bounds__(kJoin) k_tree_join(const TreeAttnParams p, int
         for (int j = 0; j < 4; ++j)
             if (d + j < p.head_dim) to[j] = Num<KIND>::put(o[j] * inv);
     }
-    if (d == 0 && p.lse) p.lse[q_row * p.q_heads + qh] = sbt_attn::log_sum(s_top[mine], l);
+    if (d == 0 && p.lse) p.lse[q_row * p.q_heads + qh] = sbt_attn::log_sum(top, l);
 }
 
 // Blocks that the workspace has room for: two an SM of 128 rows, or one of 256.
