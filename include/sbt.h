@@ -1,7 +1,7 @@
 /*
- * sbt.h -- bounds-checked tile movement, a boundary-tile bf16 GEMM and the
- * operators of a paged key-value cache on one NVIDIA GB300 (sm_103a).  C ABI
- * of libsbt.so.
+ * sbt.h -- bounds-checked tile movement, a boundary-tile bf16 GEMM, the
+ * operators of a paged key-value cache and those between a layer's GEMMs on one
+ * NVIDIA GB300 (sm_103a).  C ABI of libsbt.so.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -722,11 +722,13 @@ SBT_API sbt_status sbt_add_rms_norm_backward(sbt_context* ctx, sbt_dtype dtype, 
  *   y[t][n] = alpha * sum_k x[t][k] * B[k][n] * b_scale[k / (K / K_s)][n]
  *
  * for t < tokens, n < N.  dtype: of x; y_dtype: of y, SBT_F32, SBT_BF16 or
- * SBT_F16.  K_s divides K and K / K_s is a multiple of 16; any number of tokens
+ * SBT_F16.  K_s divides K and K / K_s is a multiple of 16; tokens <= 65535 * 8
  * (the weights are read once per 16 of them).  Sums are fp32, in an order that is
  * fixed on one device; a row of x enters the products exactly with SBT_F16, and
  * with SBT_BF16 and SBT_F32 as one and two fp16 numbers scaled by a power of two:
- * off by at most 2^-39 of its largest finite |x| (and, SBT_F32, 2^-21 of itself).  An
+ * off by at most 2^-39 of its largest finite |x| (and, SBT_F32, 2^-21 of itself).
+ * The sums are those of the scaled numbers, the largest below 2^15: group scales from
+ * 2^108 on may take them past fp32's range although the result would not be.  An
  * infinity or NaN in x reaches its own row only; a NaN scale (E8M0 0xFF, E4M3
  * 0x7F and 0xFF) its own column.
  */

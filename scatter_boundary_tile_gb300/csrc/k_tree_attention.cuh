@@ -5,37 +5,47 @@
 // the positions it sees, one pass over the cache keeps a reference m, the sum
 // l = sum 2^(s'_t - m) and the vector o = sum 2^(s'_t - m) v_t (s' = s log2 e).
 // m is the largest score seen when it was last taken; it is taken again, and l
-// and o rescaled, only when a score passes it by 2^kSlack, so a 2^(s' - m) is at
-// most that and o rarely has to be touched outside the matrix unit.  Two such
-// states over disjoint positions join by the rule of the softmax.
+// and o rescaled, only when a score passes it by SLACK (2^8; fp16 2^6), so a
+// 2^(s' - m) is at most that and o rarely has to be touched outside the matrix
+// unit.  Two such states over disjoint positions join by the rule of the softmax.
 //
 // The rows of one sequence and key-value head, n tokens times `group` query
 // heads, go through tcgen05 in tiles of 128: S = Q K^T and O += P V with K and V
 // tiles of 64 positions in shared memory (rows of 128 bytes, swizzled: K read
-// K-major, V MN-major), S, P and O in TMEM.  P enters as the sum of two 16-bit
-// numbers (16 significant bits with bf16, 22 with fp16), since one would add to
-// the output's error as much as the output's own rounding; both take the place
-// of S, so the second costs matrix time only.  fp16 ones are 2^kShift p, so that
-// small ones are not lost among the subnormals.
+// K-major, V MN-major), S, P and O in TMEM; S is double, so that tile k + 1 is
+// multiplied while tile k is in the softmax.  MT = 1: 128 rows, two blocks an SM
+// (the one's softmax runs under the other's products).  MT = 2: planes of 256
+// rows that share each tile of K and V; where a plane has 128 rows or fewer the
+// instructions of the other half are left out.  Entries of more rows have more
+// planes, each a line of its own.
 //
-// Roles.  Three warps copy (cp.async, 16 bytes a lane, from any page order and
-// stride), one thread issues the matrix instructions, and a warp for every 32
-// rows does the softmax, a row a thread.  S is double: while tile k is in the
-// softmax, tile k + 1 is already multiplied.  MT = 1: 128 rows, two blocks an SM
-// (the one's softmax runs under the other's products); MT = 2: 256 rows share a
-// tile of K and V.  More rows go to other blocks, which run at the same time on
-// the same range and find K and V in L2.
+// P.  Few rows wait for memory, and there P is the sum of two 16-bit numbers (16
+// significant bits with bf16, 22 with fp16): one would add to the output's error
+// as much as the output's own rounding.  With MT = 2 the second product would be
+// a third more of the matrix time that bounds the call, and P is one number.
+// fp16 ones are 2^SHIFT p, so that small ones are not lost among the subnormals.
 //
-// Split.  All (sequence, key-value head) lines, cut into tiles, lie on one line
-// on which every block gets an even range; lengths are read on the device.  Rows
-// wholly inside a range are written by their block; of a line cut by range
+// Roles.  A warp for every 32 rows does the softmax, a row a thread: it also
+// reads the row's query into shared memory and writes the row's output.  One warp
+// copies K and V by the tensor copy engine, where pages hold whole boxes and
+// strides are multiples of 16 bytes; otherwise three warps do with cp.async, from
+// any stride and page size.  A warp for every 128 rows issues the products: all
+// of its lanes walk and wait, one issues (an instruction takes ~30 cycles to
+// issue so, 74 from a branch that one lane takes).
+//
+// Split.  All (entry, key-value head, plane) lines, cut into tiles, lie on one
+// line on which every block gets an even range; lengths are read on the device.
+// (Planes in turn on one range: 463 us for the batch below instead of 369 then.)
+// Rows wholly inside a range are written by their block; of a line cut by range
 // borders each block writes its state to the workspace and k_tree_join adds them
 // in the order of the line.
 //
 // A masked position's score is replaced before the softmax, its P is zero.  Its
 // V would still meet that zero: among the new tokens, which one row sees and
-// another does not, infinities and NaN are taken out of the tile and put, after
-// the softmax, on the rows that do see them.
+// another does not, the softmax warps take infinities and NaN out of the tile,
+// and put them, after the last tile, on the rows that do see them.
+//
+// Measured (GB300, bf16 and fp16 alike, 128 elements a head): @ONE@
 //
 // Every wait is bounded; one that runs out sets the device status word, and the
 // kernel drains and returns.
@@ -674,18 +684,20 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
         };
         // S of tile k into buffer k & 1, from the K in `slot`.  The buffer held the P of two tiles ago: that product was
         // issued before, and one thread's instructions run in order.
+        bool live = true;              // there are rows among the 128; where not, the barriers alone are served
         auto scores = [&](int64_t k) {
             const uint32_t b = k_lo + ring_a + slot * (S::SLOT >> 4), d = tmem + (m * 2 + (int)(k & 1)) * kTok;
             if (elected()) {
+                if (live)
 #pragma unroll
-                for (int j = 0; j < DP / 16; ++j) {
-                    const uint32_t qj = ((j / 4) * kRows * 128 + (j % 4) * 32) >> 4;
-                    const uint32_t kj = ((j / 4) * kTok * 128 + (j % 4) * 32) >> 4;
-                    if (j == 0)
-                        mma_ss<false>(d, q_a + qj, b + kj, k_hi, idesc_s);
-                    else
-                        mma_ss<true>(d, q_a + qj, b + kj, k_hi, idesc_s);
-                }
+                    for (int j = 0; j < DP / 16; ++j) {
+                        const uint32_t qj = ((j / 4) * kRows * 128 + (j % 4) * 32) >> 4;
+                        const uint32_t kj = ((j / 4) * kTok * 128 + (j % 4) * 32) >> 4;
+                        if (j == 0)
+                            mma_ss<false>(d, q_a + qj, b + kj, k_hi, idesc_s);
+                        else
+                            mma_ss<true>(d, q_a + qj, b + kj, k_hi, idesc_s);
+                    }
                 tc_commit(s_full(m, (int)(k & 1)));
                 tc_commit(empty(slot));
             }
@@ -695,6 +707,7 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
         for (Walk w = start; ok && w.u < w.end;) {
             const int32_t T = w.tiles();
             if (!wait(q_full(m), q_uses++ & 1)) break;
+            live = MT == 1 || w.row.count > m * kRows;
             for (int i = 0; i < min(T, 2) && wait(full(slot), full_phase); ++i) scores(k_no + i);
             for (int32_t it = 0; ok && it < T; ++it, ++k_no) {
                 const int buf = (int)(k_no & 1);
@@ -708,9 +721,10 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
                 const uint32_t a = tmem + (m * 2 + buf) * kTok, d = tmem + S::O_COL + m * DP;
                 const uint32_t b = v_lo + ring_a + slot * (S::SLOT >> 4);
                 if (elected()) {
+                    if (live)
 #pragma unroll
-                    for (int j = 0; j < S::TERMS * kTok / 16; ++j)  // the first numbers, then the second ones
-                        mma_ts(d, a + j * 8, b + ((j % 4) * 2048 >> 4), v_hi, idesc_o, j > 0 ? 1u : it > 0);
+                        for (int j = 0; j < S::TERMS * kTok / 16; ++j)  // the first numbers, then the second ones
+                            mma_ts(d, a + j * 8, b + ((j % 4) * 2048 >> 4), v_hi, idesc_o, j > 0 ? 1u : it > 0);
                     tc_commit(pv_done(m, buf));
                     tc_commit(empty(slot));
                 }
