@@ -15,8 +15,16 @@
 // and written once.  A row belongs to a power-of-two number of threads, a warp
 // to 1024, which hold it in units of eight neighbouring elements (one 16-byte
 // vector; two in fp32) or, where widths or addresses do not allow vectors, of
-// one element.  Rows too wide for that, and codes without vectors, are read
-// twice by k_add_norm_any and k_add_norm_bwd_any.
+// one element.  Rows that start anywhere, but those of all arrays at the same place
+// relative to 16 bytes, have vectors all the same (SHIFT).  Rows too wide for
+// that, and codes without vectors, are read twice by k_add_norm_any and
+// k_add_norm_bwd_any.
+//
+// Measured (GB300; at the copy rate in brackets): 16384 x 8192 bf16 with the
+// residual to codes 162 us (139), to numbers 152 (119); 16384 x 4096 fp32 157 (119);
+// 333 x 5003 fp16 6.9 us (2.0), element by element 7.2; a single row 5.4, what the
+// host takes for a call.  Gradient, 16384 x 4096 bf16 89 us (79), of which the
+// second launch (the blocks' sums for dw) is 4; 1021 x 1537 fp32 8.9 (3.7).
 #include <algorithm>
 
 #include "sbt_internal.cuh"

