@@ -26,10 +26,10 @@
 // fp16 ones are 2^SHIFT p, so that small ones are not lost among the subnormals.
 //
 // Roles.  A warp for every 32 rows does the softmax, a row a thread: it also
-// reads the row's query into shared memory and writes the row's output.  One warp
-// copies K and V by the tensor copy engine, where pages hold whole boxes and
-// strides are multiples of 16 bytes; otherwise three warps do with cp.async, from
-// any stride and page size.  A warp for every 128 rows issues the products: all
+// reads the row's query into shared memory and writes the row's output.  Two warps
+// copy K and V by the tensor copy engine, where pages hold whole boxes and strides
+// are multiples of 16 bytes; otherwise three warps do with cp.async, from any
+// stride and page size.  A warp for every 128 rows issues the products: all
 // of its lanes walk and wait, one issues (an instruction takes ~30 cycles to
 // issue so, 74 from a branch that one lane takes).
 //
@@ -49,11 +49,12 @@
 // MT = 1: one sequence, 32 tokens on 16384 positions, 32/8 heads, bf16 38 us (10),
 // on 131072 112 (79), on 2048 23: the launches, a cold instruction cache and the
 // join are most of a short call.  MT = 2: 48 sequences, 32 tokens on 8192
-// positions, 64/8 heads, fp16 383 us (240); trees of 1 to 64 tokens on contexts to
-// 8191 339 (130).  There a tile takes ~1900 cycles: a row's chain from its scores
-// to P is one thread's, and two such warps share an SM partition; the products of a
-// tile are ~1280 (scores with 64 columns read Q from shared memory at 3/2 of the
-// time their multiplication takes).
+// positions, 64/8 heads, fp16 390 us (240); trees of 1 to 64 tokens on contexts to
+// 8191 330 (130).  There a tile takes ~1650 cycles, half of a chain over two: scores
+// to P 1280 (two such warps share an SM partition, in step), P seen 260, product
+// and next scores issued 1200 beside the other half's, scores done and seen 580.
+// The products alone are ~1280 (with 64 columns they read Q from shared memory at
+// 3/2 of the time that their multiplication takes).
 //
 // Every wait is bounded; one that runs out sets the device status word, and the
 // kernel drains and returns.
@@ -281,7 +282,7 @@ __device__ __forceinline__ bool special(uint16_t x) {
 
 template <int KIND, int DP, int MT, bool TMA>
 struct TreeShape {
-    static constexpr int WARPS = 4 * MT + (TMA ? 1 : kLoaders / 32) + MT, THREADS = 32 * WARPS;
+    static constexpr int WARPS = 4 * MT + (TMA ? 2 : kLoaders / 32) + MT, THREADS = 32 * WARPS;
     // (registers are bounded for whole warps on each of the SM's four partitions)
     static constexpr int BLOCKS = MT == 1 && DP <= 128 ? 2 : 1;
     static constexpr int R = MT * kRows;
@@ -312,6 +313,7 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
     __shared__ int64_t s_first[THREADS];
     __shared__ TreeRow s_row;
     __shared__ int64_t s_offsets[TMA ? 1 : kLoaders / 32][2 * kTok];
+    __shared__ volatile int s_uses[NS];  // copies by the engine that each slot has taken
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* const q_s = smem;
     uint8_t* const ring = smem + MT * S::Q_TILE;
@@ -338,6 +340,7 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
             mbar_init(q_full(m), kRows), mbar_init(all_done(m), 1);
             for (int b = 0; b < 2; ++b) mbar_init(s_full(m, b), 1), mbar_init(p_ready(m, b), kRows), mbar_init(pv_done(m, b), 1);
         }
+        for (int i = 0; i < NS; ++i) s_uses[i] = 0;
         *abort_flag = 0;
         *s_special = 0;
         fence_mbar_init();
@@ -424,21 +427,25 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
     }
 
     if (idle) {
-    } else if (TMA && warp == 4 * MT) {
+    } else if (TMA && (warp == 4 * MT || warp == 4 * MT + 1)) {
         // ------------------------------------------------------------ copies by the tensor copy engine
+        // One warp copies K and one V: to start a tile's copies takes a warp ~900 cycles (one for both took longer than
+        // the products: 8 trees of 48 tokens on 8192 positions, 32/8 heads of 128, 92 us, and 82 so).
         // A tile is a box of 64 elements and a page's positions (64 at most) for every 128 bytes of its rows; a lane
         // starts one of them.  A page that is not there is a coordinate outside the tensor, which reads as zeros.
+        const bool is_v = warp != 4 * MT;
+        const CUtensorMap* const map = is_v ? &v_map : &k_map;
         const int per_page = min((int)p.page_size.d, kTok), boxes = kTok / per_page * (DP / 64);
         const int mine = lane / (DP / 64), x = lane % (DP / 64) * 64;  // page of the tile, first element
         const uint32_t box_at = smem_u32(ring) + (x / 64) * kTok * 128 + mine * per_page * 128;
         int slot = 0, tile_no = 0;
         uint32_t phase = 1;  // the first pass finds the slots empty
         bool ok = true;
-        int64_t items = 0;
         for (Walk w = start; ok && w.u < w.end;) {
             const TreeRow& row = w.row;
             const int32_t T = w.tiles();
-            int32_t page[4], at[4];    // of four tiles, by their numbers modulo 4: pages are asked for two tiles ahead
+            // pages are asked for four tiles ahead: of four tiles, by their numbers modulo 4
+            int32_t page[4], at[4];
             auto look_up = [&](int32_t it, int32_t& page, int32_t& at) {
                 const int32_t pos = (w.t + it) * kTok + mine * per_page;
                 page = -1, at = 0;
@@ -448,57 +455,55 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
                     page = sbt_ld(p.table + (int64_t)row.seq * p.ld_table + j);
                 }
             };
-            auto tile = [&](const CUtensorMap* map, int32_t page, int32_t at) {
+            auto skip = [&](int slots) {  // three at most, less than there are
+                slot += slots;
+                if (slot >= NS) slot -= NS, phase ^= 1;
+            };
+            auto tile = [&](int32_t page, int32_t at) {
                 if (!__all_sync(0xffffffffu, mbar_wait_bounded(empty(slot), phase, p.wait_ns, abort_flag, p.status, kCodeTreeLoad))) {
                     ok = false;
                     return;
                 }
                 // the test hook's first tile is neither announced nor started
-                const bool withheld = p.withhold && items == 0;
-                if (lane == 0 && !withheld) mbar_arrive_expect_tx(full(slot), S::SLOT);
+                const bool withheld = p.withhold && !is_v && tile_no == 0;
+                if (lane == 0 && !withheld) {
+                    s_uses[slot] = s_uses[slot] + 1;
+                    mbar_arrive_expect_tx(full(slot), S::SLOT);
+                }
                 __syncwarp();
                 if (lane < boxes && !withheld)
                     tma_load_4d(box_at + slot * S::SLOT, map, x, at, w.h, page >= 0 && page < p.n_pages ? page : -1, full(slot));
-                ++items;
-                if (++slot == NS) slot = 0, phase ^= 1;
             };
-            auto k_tile = [&](int32_t page, int32_t at) {
-                uint64_t bits = 0;
-                if (lane < boxes && x == 0 && page >= 0 && page < p.n_pages)
-                    bits = (per_page == kTok ? ~0ull : (1ull << per_page) - 1) << (mine * per_page);
-                const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)bits);
-                const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32));
-                if (lane == 0) s_bits[tile_no & (kBits - 1)] = lo | (uint64_t)hi << 32;
-                ++tile_no;
-                __syncwarp();
-                tile(&k_map, page, at);
-            };
-            // K runs two tiles ahead of V, as the products do
 #pragma unroll
             for (int i = 0; i < 4; ++i) look_up(i, page[i], at[i]);
-            k_tile(page[0], at[0]);
-            if (ok && T > 1) k_tile(page[1], at[1]);
+            // the slots go to K K V K V .. K V V: K runs two tiles ahead of V, as the products do
+            if (is_v) skip(T > 1 ? 2 : 1);
             for (int32_t it0 = 0; ok && it0 < T; it0 += 4)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int32_t it = it0 + i;
                     if (ok && it < T) {
-                        tile(&v_map, page[i], at[i]);
+                        if (!is_v) {
+                            uint64_t bits = 0;
+                            if (lane < boxes && x == 0 && page[i] >= 0 && page[i] < p.n_pages)
+                                bits = (per_page == kTok ? ~0ull : (1ull << per_page) - 1) << (mine * per_page);
+                            const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)bits);
+                            const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32));
+                            if (lane == 0) s_bits[tile_no & (kBits - 1)] = lo | (uint64_t)hi << 32;
+                            __syncwarp();
+                        }
+                        tile(page[i], at[i]);
+                        ++tile_no;
                         look_up(it + 4, page[i], at[i]);
-                        if (ok && it + 2 < T) k_tile(page[(i + 2) & 3], at[(i + 2) & 3]);
+                        const bool last = it + 1 == T;
+                        if (is_v)
+                            skip(it + 2 >= T ? 1 : 2);
+                        else
+                            skip(last ? (T == 1 ? 2 : 3) : it == 0 ? 1 : 2);
                     }
                 }
             w.next(T);
         }
-        // copies in flight land before the block leaves
-        for (int64_t i = 0; i < items && i < NS; ++i) {
-            if (slot == 0) slot = NS, phase ^= 1;
-            --slot;
-            const uint64_t t0 = globaltimer();
-            while (!(p.withhold && items <= NS && i == items - 1) && !mbar_try_wait(full(slot), phase ^ 1) && globaltimer() - t0 < p.wait_ns) {
-            }
-        }
-        __syncwarp();
     } else if (!TMA && warp >= 4 * MT && warp < WARPS - MT) {
         // ------------------------------------------------------------ copies by lanes
         const int tid = threadIdx.x - 4 * MT * 32;
@@ -1036,6 +1041,12 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
         }
     tc_fence_before();
     __syncthreads();
+    if (TMA && *abort_flag && warp == 4 * MT)  // copies in flight land before the block leaves
+        for (int i = 0; i < NS; ++i) {
+            const uint64_t t0 = globaltimer();
+            while (s_uses[i] > 0 && !mbar_try_wait(full(i), (s_uses[i] - 1) & 1) && globaltimer() - t0 < p.wait_ns) {
+            }
+        }
     if (*abort_flag && p.desc_by_line && threadIdx.x == 0 && !idle)
         for (Walk w = start; w.u < w.end; w.next(w.tiles()))  // what was not finished is not joined
             if (w.t == 0) p.desc[((int64_t)w.row.b * p.kv_heads + w.h) * p.planes + w.row.plane].valid = 0;
