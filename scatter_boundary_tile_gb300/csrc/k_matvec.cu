@@ -617,7 +617,8 @@ sbt_status launch(sbt_context* ctx, MatvecParams& p, cudaStream_t stream) {
     constexpr auto kern = k_matvec<KIND, U, SU, E4M3, MT, ALIGNED, false>;
     typedef Shape<U, SU, MT, ALIGNED, false> S;
     const int64_t tiles = sbt_cdiv(p.N, kCols), chunks = sbt_cdiv(p.tokens, 8 * MT), stages = p.K / S::ROWS;
-    // Blocks per tile: the number with which the last wave's end comes first.
+    // Blocks per tile: the number with which the last wave's end comes first.  (Clusters are counted as they fit groups of
+    // SMs: by blocks alone 16 tiles of 16 tokens took eight each, 22 us instead of 15.)
     int64_t best = INT64_MAX;
     for (int c = 1; c <= kClusterMost && (c == 1 || c * S::KW <= stages); ++c) {
         const int64_t waves = sbt_cdiv(tiles * chunks, sbt_resident_clusters<kern>(ctx, 32 * S::WARPS, S::SMEM, c));
@@ -625,6 +626,9 @@ sbt_status launch(sbt_context* ctx, MatvecParams& p, cudaStream_t stream) {
         if (cost < best) best = cost, p.ranks = c;
     }
     if constexpr (ALIGNED && MT == 2) {
+        // A row of k of 128 columns costs a warp 1.8 times as long among twelve as among eight with two units a stage, and
+        // 1.4 times as long with one.  16 tokens bf16, K 4096, by blocks and from tile to tile: N 8192 16 and 21 us, 16384
+        // 24 and 21, 28672 36 and 37, 40960 70 and 52, 100000 112 and 103; K 2048, N 20000 22 and 25.
         constexpr auto line = k_matvec<KIND, U, SL, E4M3, MT, true, true>;
         typedef Shape<U, SL, MT, true, true> L;
         p.items = sbt_cdiv(p.N, L::COLS) * chunks, p.chunks = (int32_t)chunks;
