@@ -307,192 +307,244 @@ __global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED, LINE>::WARPS, S
     int stage = 0;
 #pragma unroll 1
     for (int64_t item = first_item; item < items; item += step_item) {
-    const int64_t n0 = columns(item), tok0 = tokens(item);
-    const uint8_t* sum_s = p.s + s_row * p.ld_s + n0;
-    int sum_left = each ? 1 : s_left;
-    float sum[MT][TILES][4];  // columns g * 2 * TILES + 2 i, + 1; rows 2 t, + 1 of x
+        const int64_t n0 = columns(item), tok0 = tokens(item);
+        const uint8_t* sum_s = p.s + s_row * p.ld_s + n0;
+        int sum_left = each ? 1 : s_left;
+        float sum[MT][TILES][4];  // columns g * 2 * TILES + 2 i, + 1; rows 2 t, + 1 of x
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < TILES; ++i)
+            for (int i = 0; i < TILES; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sum[m][i][k] = 0.f;
-    int exponent[MT];  // x of row g enters as x 2^-exponent
+                for (int k = 0; k < 4; ++k) sum[m][i][k] = 0.f;
+        int exponent[MT];  // x of row g enters as x 2^-exponent
 #pragma unroll
-    for (int m = 0; m < MT; ++m) exponent[m] = -126;
+        for (int m = 0; m < MT; ++m) exponent[m] = -126;
 
 #pragma unroll 1
-    for (int n = todo; n > 0; --n) {
-        copy_wait<S::STAGES - 2>();
-        __syncwarp();
-        copy(stage == 0 ? S::STAGES - 1 : stage - 1);
-        copy_commit();
+        for (int n = todo; n > 0; --n) {
+            copy_wait<S::STAGES - 2>();
+            __syncwarp();
+            copy(stage == 0 ? S::STAGES - 1 : stage - 1);
+            copy_commit();
 
-        // x as fp16 pairs along k
-        uint32_t b[SU][STEPS][MT][TERMS][2];
-        if constexpr (KIND == kF16) {
-#pragma unroll
-            for (int q = 0; q < SU; ++q)
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int s = 0; s < STEPS; ++s) {
-                        const uint2 v = reinterpret_cast<const uint2*>(&raw[q][m])[s];
-                        b[q][s][m][0][0] = v.x, b[q][s][m][0][1] = v.y;
-                    }
-        } else {
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                // exponent of the largest finite |x| of the row in this stage; magnitudes order as their bits do
-                uint32_t most = 0;
-                if constexpr (KIND == kBF16) {
-#pragma unroll
-                    for (int q = 0; q < SU; ++q)
-#pragma unroll
-                        for (int i = 0; i < XK / 2; ++i)
-                            most = __vmaxu2(most, reinterpret_cast<const uint32_t*>(&raw[q][m])[i] & 0x7FFF7FFFu);
-                    most = max(most & 0xFFFF0000u, most << 16);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < SU; ++q)
-#pragma unroll
-                        for (int i = 0; i < XK; ++i) most = max(most, __float_as_uint(Num<KIND>::get(raw[q][m].v[i])) & 0x7fffffffu);
-                }
-                int top = (int)(most >> 23);
-                if (top == 255) {   // an infinity or NaN: the largest of the others
-                    top = 0;
-#pragma unroll 1
-                    for (int q = 0; q < SU * XK; ++q) {
-                        T one = 0;
-#pragma unroll
-                        for (int i = 0; i < SU * XK; ++i)
-                            if (i == q) one = raw[i / XK][m].v[i % XK];
-                        const int e = (int)(__float_as_uint(Num<KIND>::get(one)) >> 23) & 255;
-                        top = max(top, e == 255 ? 0 : e);
-                    }
-                }
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int want = max(top - 127 - 14, -126);
-                if (__any_sync(0xffffffffu, want > exponent[m])) {
-                    const int top_e = max(want, exponent[m]), gap = min(top_e - exponent[m], 127);
-                    exponent[m] = top_e;
-                    // the rows of the sums are 2 t and 2 t + 1, held by lanes 8 t and 8 t + 4
-                    const float f0 = power(-__shfl_sync(0xffffffffu, gap, 8 * t));
-                    const float f1 = power(-__shfl_sync(0xffffffffu, gap, 8 * t + 4));
-#pragma unroll
-                    for (int i = 0; i < TILES; ++i) {
-                        sum[m][i][0] *= f0, sum[m][i][1] *= f1;
-                        sum[m][i][2] *= f0, sum[m][i][3] *= f1;
-                    }
-                }
-                const float f = power(-exponent[m]);
+            // x as fp16 pairs along k
+            uint32_t b[SU][STEPS][MT][TERMS][2];
+            if constexpr (KIND == kF16) {
 #pragma unroll
                 for (int q = 0; q < SU; ++q)
 #pragma unroll
-                    for (int i = 0; i < XK / 2; ++i) {
-                        const float lo = Num<KIND>::get(raw[q][m].v[2 * i]) * f, hi = Num<KIND>::get(raw[q][m].v[2 * i + 1]) * f;
-                        const __half2 h = __floats2half2_rn(lo, hi);
-                        b[q][i / 2][m][0][i % 2] = *reinterpret_cast<const uint32_t*>(&h);
-                        if constexpr (TERMS == 2) {
-                            const float2 v = __half22float2(h);
-                            // what the first number leaves; nothing of an infinity
-                            const __half2 r = __floats2half2_rn(isinf(lo) ? 0.f : lo - v.x, isinf(hi) ? 0.f : hi - v.y);
-                            b[q][i / 2][m][TERMS - 1][i % 2] = *reinterpret_cast<const uint32_t*>(&r);
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int s = 0; s < STEPS; ++s) {
+                            const uint2 v = reinterpret_cast<const uint2*>(&raw[q][m])[s];
+                            b[q][s][m][0][0] = v.x, b[q][s][m][0][1] = v.y;
+                        }
+            } else {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    // exponent of the largest finite |x| of the row in this stage; magnitudes order as their bits do
+                    uint32_t most = 0;
+                    if constexpr (KIND == kBF16) {
+#pragma unroll
+                        for (int q = 0; q < SU; ++q)
+#pragma unroll
+                            for (int i = 0; i < XK / 2; ++i)
+                                most = __vmaxu2(most, reinterpret_cast<const uint32_t*>(&raw[q][m])[i] & 0x7FFF7FFFu);
+                        most = max(most & 0xFFFF0000u, most << 16);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < SU; ++q)
+#pragma unroll
+                            for (int i = 0; i < XK; ++i) most = max(most, __float_as_uint(Num<KIND>::get(raw[q][m].v[i])) & 0x7fffffffu);
+                    }
+                    int top = (int)(most >> 23);
+                    if (top == 255) {   // an infinity or NaN: the largest of the others
+                        top = 0;
+#pragma unroll 1
+                        for (int q = 0; q < SU * XK; ++q) {
+                            T one = 0;
+#pragma unroll
+                            for (int i = 0; i < SU * XK; ++i)
+                                if (i == q) one = raw[i / XK][m].v[i % XK];
+                            const int e = (int)(__float_as_uint(Num<KIND>::get(one)) >> 23) & 255;
+                            top = max(top, e == 255 ? 0 : e);
                         }
                     }
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const int want = max(top - 127 - 14, -126);
+                    if (__any_sync(0xffffffffu, want > exponent[m])) {
+                        const int top_e = max(want, exponent[m]), gap = min(top_e - exponent[m], 127);
+                        exponent[m] = top_e;
+                        // the rows of the sums are 2 t and 2 t + 1, held by lanes 8 t and 8 t + 4
+                        const float f0 = power(-__shfl_sync(0xffffffffu, gap, 8 * t));
+                        const float f1 = power(-__shfl_sync(0xffffffffu, gap, 8 * t + 4));
+#pragma unroll
+                        for (int i = 0; i < TILES; ++i) {
+                            sum[m][i][0] *= f0, sum[m][i][1] *= f1;
+                            sum[m][i][2] *= f0, sum[m][i][3] *= f1;
+                        }
+                    }
+                    const float f = power(-exponent[m]);
+#pragma unroll
+                    for (int q = 0; q < SU; ++q)
+#pragma unroll
+                        for (int i = 0; i < XK / 2; ++i) {
+                            const float lo = Num<KIND>::get(raw[q][m].v[2 * i]) * f, hi = Num<KIND>::get(raw[q][m].v[2 * i + 1]) * f;
+                            const __half2 h = __floats2half2_rn(lo, hi);
+                            b[q][i / 2][m][0][i % 2] = *reinterpret_cast<const uint32_t*>(&h);
+                            if constexpr (TERMS == 2) {
+                                const float2 v = __half22float2(h);
+                                // what the first number leaves; nothing of an infinity
+                                const __half2 r = __floats2half2_rn(isinf(lo) ? 0.f : lo - v.x, isinf(hi) ? 0.f : hi - v.y);
+                                b[q][i / 2][m][TERMS - 1][i % 2] = *reinterpret_cast<const uint32_t*>(&r);
+                            }
+                        }
+                }
             }
-        }
-        load_x(raw);
+            load_x(raw);
 
-        const uint8_t* const st = ring + stage * S::STAGE;
+            const uint8_t* const st = ring + stage * S::STAGE;
 #pragma unroll
-        for (int q = 0; q < SU; ++q) {
-            // weights: rows q U + t U / 4 + 4 s + r, a lane's WORDS words of each
-            uint32_t w[STEPS][4][WORDS];
+            for (int q = 0; q < SU; ++q) {
+                // weights: rows q U + t U / 4 + 4 s + r, a lane's WORDS words of each
+                uint32_t w[STEPS][4][WORDS];
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s)
+                for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = q * U + t * XK + 4 * s + r;
-                    if (ALIGNED) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(st + S::place(row, g * S::LANE));
-                        w[s][r][0] = v.x, w[s][r][1] = v.y;
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = q * U + t * XK + 4 * s + r;
+                        if (ALIGNED) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(st + S::place(row, g * S::LANE));
+                            w[s][r][0] = v.x, w[s][r][1] = v.y;
+                        } else {
+                            const int shift = (int)((uintptr_t)(p.w + ((u1 - n) * ROWS + row) * p.ld_w + n0 / 2) & 15);
+                            const uint32_t* const a =
+                                reinterpret_cast<const uint32_t*>(st + row * S::PITCH + g * S::LANE + (shift & ~3));
+                            uint32_t c = a[0];
+#pragma unroll
+                            for (int j = 0; j < WORDS; ++j) {
+                                const uint32_t d = a[j + 1];
+                                w[s][r][j] = __funnelshift_r(c, d, (shift & 3) * 8);
+                                c = d;
+                            }
+                        }
+                    }
+                uint32_t sc[2 * WORDS];  // scales of its 8 WORDS columns
+                {
+                    const int row = each ? q : 0, shift = (int)((uintptr_t)(sum_s + row * p.ld_s) & 15);
+                    const uint8_t* const a = st + ROWS * S::PITCH + row * S::SCALES + g * 2 * S::LANE;
+                    if (shift == 0) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(a);
+                        sc[0] = v.x, sc[1] = v.y, sc[2] = v.z, sc[3] = v.w;
                     } else {
-                        const int shift = (int)((uintptr_t)(p.w + ((u1 - n) * ROWS + row) * p.ld_w + n0 / 2) & 15);
-                        const uint32_t* const a =
-                            reinterpret_cast<const uint32_t*>(st + row * S::PITCH + g * S::LANE + (shift & ~3));
-                        uint32_t c = a[0];
+                        const uint32_t* const at = reinterpret_cast<const uint32_t*>(a + (shift & ~3));
+                        uint32_t c = at[0];
 #pragma unroll
-                        for (int j = 0; j < WORDS; ++j) {
-                            const uint32_t d = a[j + 1];
-                            w[s][r][j] = __funnelshift_r(c, d, (shift & 3) * 8);
+                        for (int j = 0; j < 2 * WORDS; ++j) {
+                            const uint32_t d = at[j + 1];
+                            sc[j] = __funnelshift_r(c, d, (shift & 3) * 8);
                             c = d;
                         }
                     }
                 }
-            uint32_t sc[2 * WORDS];  // scales of its 8 WORDS columns
-            {
-                const int row = each ? q : 0, shift = (int)((uintptr_t)(sum_s + row * p.ld_s) & 15);
-                const uint8_t* const a = st + ROWS * S::PITCH + row * S::SCALES + g * 2 * S::LANE;
-                if (shift == 0) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(a);
-                    sc[0] = v.x, sc[1] = v.y, sc[2] = v.z, sc[3] = v.w;
-                } else {
-                    const uint32_t* const at = reinterpret_cast<const uint32_t*>(a + (shift & ~3));
-                    uint32_t c = at[0];
+                // a byte of the last words may be past the scales and the weights: columns past N, which nobody reads
 #pragma unroll
-                    for (int j = 0; j < 2 * WORDS; ++j) {
-                        const uint32_t d = at[j + 1];
-                        sc[j] = __funnelshift_r(c, d, (shift & 3) * 8);
-                        c = d;
-                    }
-                }
-            }
-            // a byte of the last words may be past the scales and the weights: columns past N, which nobody reads
+                for (int j = 0; j < WORDS; ++j) {
+                    uint32_t a[STEPS][4][4];  // [step][fragment][column pair]
 #pragma unroll
-            for (int j = 0; j < WORDS; ++j) {
-                uint32_t a[STEPS][4][4];  // [step][fragment][column pair]
+                    for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-                for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t lo = w[s][2 * k][j], hi = w[s][2 * k + 1][j];
-                        unpack_e2m1((lo & 0x0F0F0F0Fu) | ((hi << 4) & 0xF0F0F0F0u), a[s][2 * k]);
-                        unpack_e2m1(((lo >> 4) & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u), a[s][2 * k + 1]);
-                    }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = unpack_scales<E4M3>(i & 1 ? sc[2 * j + i / 2] >> 16 : sc[2 * j + i / 2]);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        float c[4];
-#pragma unroll
-                        for (int s = 0; s < STEPS; ++s) {
-                            const uint32_t frag[4] = {a[s][0][i], a[s][1][i], a[s][2][i], a[s][3][i]};
-#pragma unroll
-                            for (int v = 0; v < TERMS; ++v)
-                                if (s == 0 && v == 0)
-                                    mma<false>(c, frag, b[q][s][m][v][0], b[q][s][m][v][1]);
-                                else
-                                    mma<true>(c, frag, b[q][s][m][v][0], b[q][s][m][v][1]);
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t lo = w[s][2 * k][j], hi = w[s][2 * k + 1][j];
+                            unpack_e2m1((lo & 0x0F0F0F0Fu) | ((hi << 4) & 0xF0F0F0F0u), a[s][2 * k]);
+                            unpack_e2m1(((lo >> 4) & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u), a[s][2 * k + 1]);
                         }
-                        float(&d)[4] = sum[m][4 * j + i];
-                        d[0] = fmaf(c[0], f.x, d[0]), d[1] = fmaf(c[1], f.x, d[1]);
-                        d[2] = fmaf(c[2], f.y, d[2]), d[3] = fmaf(c[3], f.y, d[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = unpack_scales<E4M3>(i & 1 ? sc[2 * j + i / 2] >> 16 : sc[2 * j + i / 2]);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            float c[4];
+#pragma unroll
+                            for (int s = 0; s < STEPS; ++s) {
+                                const uint32_t frag[4] = {a[s][0][i], a[s][1][i], a[s][2][i], a[s][3][i]};
+#pragma unroll
+                                for (int v = 0; v < TERMS; ++v)
+                                    if (s == 0 && v == 0)
+                                        mma<false>(c, frag, b[q][s][m][v][0], b[q][s][m][v][1]);
+                                    else
+                                        mma<true>(c, frag, b[q][s][m][v][0], b[q][s][m][v][1]);
+                            }
+                            float(&d)[4] = sum[m][4 * j + i];
+                            d[0] = fmaf(c[0], f.x, d[0]), d[1] = fmaf(c[1], f.x, d[1]);
+                            d[2] = fmaf(c[2], f.y, d[2]), d[3] = fmaf(c[3], f.y, d[3]);
+                        }
                     }
                 }
             }
+            if (--sum_left == 0) sum_left = per, sum_s += s_rows * p.ld_s;
+            stage = stage + 1 == S::STAGES ? 0 : stage + 1;
         }
-        if (--sum_left == 0) sum_left = per, sum_s += s_rows * p.ld_s;
-        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
-    }
-    // ---- from tile to tile: the warps add their sums to one buffer in their order, each when the one before it has; the
-    // last writes y and lets the first go on.  (A warp passes again only after the next one has waited: all of them
-    // have then added, and the last has let the first go on.)
-    if constexpr (LINE) {
-        float* const buf = reinterpret_cast<float*>(smem + S::WARPS * S::RING);
-        if (warp > 0 || item != first_item) chain_wait(warp > 0 ? warp - 1 : S::KW - 1);
+        // ---- from tile to tile: the warps add their sums to one buffer in their order, each when the one before it has; the
+        // last writes y and lets the first go on.  (A warp passes again only after the next one has waited: all of them
+        // have then added, and the last has let the first go on.)
+        if constexpr (LINE) {
+            float* const buf = reinterpret_cast<float*>(smem + S::WARPS * S::RING);
+            if (warp > 0 || item != first_item) chain_wait(warp > 0 ? warp - 1 : S::KW - 1);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                float f0 = 1.f, f1 = 1.f;
+                if (KIND != kF16) {
+                    f0 = power(__shfl_sync(0xffffffffu, exponent[m], 8 * t));
+                    f1 = power(__shfl_sync(0xffffffffu, exponent[m], 8 * t + 4));
+                }
+#pragma unroll
+                for (int i = 0; i < TILES; ++i) {
+                    const float(&d)[4] = sum[m][i];
+                    float4* const at = reinterpret_cast<float4*>(buf) + (m * 8 + i) * 33 + lane;
+                    float4 v = make_float4(d[0] * f0, d[1] * f1, d[2] * f0, d[3] * f1);
+                    if (warp > 0) {
+                        const float4 w = *at;
+                        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+                    }
+                    *at = v;
+                }
+            }
+            __syncwarp();
+            if (warp < S::KW - 1) {
+                chain_pass(warp);
+            } else {
+#pragma unroll 1
+                for (int r = 0; r < 8 * MT && tok0 + r < p.tokens; ++r) {
+                    char* const y = p.y + (tok0 + r) * p.ld_y;
+                    float v[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int c = 32 * j + lane;
+                        v[j] = p.alpha * buf[((r / 8 * 8 + c % 16 / 2) * 33 + c / 16 * 4 + r % 8 / 2) * 4 + c % 2 * 2 + r % 2];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int64_t n = n0 + 32 * j + lane;
+                        if (n >= p.N) break;
+                        if (p.y_kind == kF32)
+                            reinterpret_cast<float*>(y)[n] = v[j];
+                        else
+                            reinterpret_cast<uint16_t*>(y)[n] = p.y_kind == kBF16 ? Num<kBF16>::put(v[j]) : Num<kF16>::put(v[j]);
+                    }
+                }
+                __syncwarp();
+                if (item + step_item < items) chain_pass(S::KW - 1);
+            }
+            continue;
+        }
+        copy_wait<0>();
+
+        // ---- the warps' sums, then the blocks': a block finishes every p.ranks-th row
+        const int64_t tile = blockIdx.x / p.ranks;
+        float* const part = reinterpret_cast<float*>(smem);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             float f0 = 1.f, f1 = 1.f;
@@ -500,115 +552,63 @@ __global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED, LINE>::WARPS, S
                 f0 = power(__shfl_sync(0xffffffffu, exponent[m], 8 * t));
                 f1 = power(__shfl_sync(0xffffffffu, exponent[m], 8 * t + 4));
             }
+            __syncthreads();
+            // columns lie 34 floats apart for every 32 of the tile
+            float* const mine = part + warp % S::KW * 8 * kPitch;
 #pragma unroll
             for (int i = 0; i < TILES; ++i) {
+                const int col = warp / S::KW * S::CW + g * 2 * TILES + 2 * i, n = (col >> 5) * 34 + (col & 31);
                 const float(&d)[4] = sum[m][i];
-                float4* const at = reinterpret_cast<float4*>(buf) + (m * 8 + i) * 33 + lane;
-                float4 v = make_float4(d[0] * f0, d[1] * f1, d[2] * f0, d[3] * f1);
-                if (warp > 0) {
-                    const float4 w = *at;
-                    v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
-                }
-                *at = v;
+                *reinterpret_cast<float2*>(mine + (2 * t) * kPitch + n) = make_float2(d[0] * f0, d[2] * f0);
+                *reinterpret_cast<float2*>(mine + (2 * t + 1) * kPitch + n) = make_float2(d[1] * f1, d[3] * f1);
             }
-        }
-        __syncwarp();
-        if (warp < S::KW - 1) {
-            chain_pass(warp);
-        } else {
-#pragma unroll 1
-            for (int r = 0; r < 8 * MT && tok0 + r < p.tokens; ++r) {
-                char* const y = p.y + (tok0 + r) * p.ld_y;
-                float v[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int c = 32 * j + lane;
-                    v[j] = p.alpha * buf[((r / 8 * 8 + c % 16 / 2) * 33 + c / 16 * 4 + r % 8 / 2) * 4 + c % 2 * 2 + r % 2];
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int64_t n = n0 + 32 * j + lane;
-                    if (n >= p.N) break;
-                    if (p.y_kind == kF32)
-                        reinterpret_cast<float*>(y)[n] = v[j];
-                    else
-                        reinterpret_cast<uint16_t*>(y)[n] = p.y_kind == kBF16 ? Num<kBF16>::put(v[j]) : Num<kF16>::put(v[j]);
-                }
-            }
-            __syncwarp();
-            if (item + step_item < items) chain_pass(S::KW - 1);
-        }
-        continue;
-    }
-    copy_wait<0>();
-
-    // ---- the warps' sums, then the blocks': a block finishes every p.ranks-th row
-    const int64_t tile = blockIdx.x / p.ranks;
-    float* const part = reinterpret_cast<float*>(smem);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        float f0 = 1.f, f1 = 1.f;
-        if (KIND != kF16) {
-            f0 = power(__shfl_sync(0xffffffffu, exponent[m], 8 * t));
-            f1 = power(__shfl_sync(0xffffffffu, exponent[m], 8 * t + 4));
-        }
-        __syncthreads();
-        // columns lie 34 floats apart for every 32 of the tile
-        float* const mine = part + warp % S::KW * 8 * kPitch;
-#pragma unroll
-        for (int i = 0; i < TILES; ++i) {
-            const int col = warp / S::KW * S::CW + g * 2 * TILES + 2 * i, n = (col >> 5) * 34 + (col & 31);
-            const float(&d)[4] = sum[m][i];
-            *reinterpret_cast<float2*>(mine + (2 * t) * kPitch + n) = make_float2(d[0] * f0, d[2] * f0);
-            *reinterpret_cast<float2*>(mine + (2 * t + 1) * kPitch + n) = make_float2(d[1] * f1, d[3] * f1);
-        }
-        __syncthreads();
-        const int n = threadIdx.x, at = (n >> 5) * 34 + (n & 31);  // the first 256 threads take a column each
-        const bool adds = n < kCols;
-        float v[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            v[r] = 0.f;
-#pragma unroll
-            for (int w = 0; w < S::KW && adds; ++w) v[r] += part[(w * 8 + r) * kPitch + at];
-        }
-        if (p.ranks > 1) {
             __syncthreads();
+            const int n = threadIdx.x, at = (n >> 5) * 34 + (n & 31);  // the first 256 threads take a column each
+            const bool adds = n < kCols;
+            float v[8];
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (adds) part[r * kPitch + at] = v[r];
-            sbt_ptx::cluster_sync();
-        }
-        auto put = [&](int r, float x) {
-            const int64_t tok = tok0 + m * 8 + r;
-            if (tok >= p.tokens || !adds || tile * kCols + n >= p.N) return;
-            char* const y = p.y + tok * p.ld_y;
-            x *= p.alpha;
-            if (p.y_kind == kF32)
-                reinterpret_cast<float*>(y)[tile * kCols + n] = x;
-            else
-                reinterpret_cast<uint16_t*>(y)[tile * kCols + n] = p.y_kind == kBF16 ? Num<kBF16>::put(x) : Num<kF16>::put(x);
-        };
-        if (p.ranks == 1) {
+            for (int r = 0; r < 8; ++r) {
+                v[r] = 0.f;
 #pragma unroll
-            for (int r = 0; r < 8; ++r) put(r, v[r]);
-        } else {
-            const uint32_t from = sbt_ptx::smem_u32(part + at);
-            for (int r = rank; adds && r < 8 && tok0 + m * 8 + r < p.tokens; r += p.ranks) {
-                float x = 0.f;
-                for (int q = 0; q < p.ranks; ++q) {
-                    float part_q;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                 : "=f"(part_q)
-                                 : "r"(sbt_ptx::mapa_shared(from + r * kPitch * 4, q)));
-                    x += part_q;
-                }
-                put(r, x);
+                for (int w = 0; w < S::KW && adds; ++w) v[r] += part[(w * 8 + r) * kPitch + at];
             }
-            __syncwarp();
-            sbt_ptx::cluster_sync();  // nobody leaves, or writes the next rows' sums, while another reads
+            if (p.ranks > 1) {
+                __syncthreads();
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (adds) part[r * kPitch + at] = v[r];
+                sbt_ptx::cluster_sync();
+            }
+            auto put = [&](int r, float x) {
+                const int64_t tok = tok0 + m * 8 + r;
+                if (tok >= p.tokens || !adds || tile * kCols + n >= p.N) return;
+                char* const y = p.y + tok * p.ld_y;
+                x *= p.alpha;
+                if (p.y_kind == kF32)
+                    reinterpret_cast<float*>(y)[tile * kCols + n] = x;
+                else
+                    reinterpret_cast<uint16_t*>(y)[tile * kCols + n] = p.y_kind == kBF16 ? Num<kBF16>::put(x) : Num<kF16>::put(x);
+            };
+            if (p.ranks == 1) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) put(r, v[r]);
+            } else {
+                const uint32_t from = sbt_ptx::smem_u32(part + at);
+                for (int r = rank; adds && r < 8 && tok0 + m * 8 + r < p.tokens; r += p.ranks) {
+                    float x = 0.f;
+                    for (int q = 0; q < p.ranks; ++q) {
+                        float part_q;
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                     : "=f"(part_q)
+                                     : "r"(sbt_ptx::mapa_shared(from + r * kPitch * 4, q)));
+                        x += part_q;
+                    }
+                    put(r, x);
+                }
+                __syncwarp();
+                sbt_ptx::cluster_sync();  // nobody leaves, or writes the next rows' sums, while another reads
+            }
         }
-    }
     }
 }
 
