@@ -510,10 +510,27 @@ sbt_status forward(sbt_context* ctx, NormParams& p, cudaStream_t stream) {
     return sbt_after_launch(ctx, "add_rms_norm");
 }
 
+// The gradient's forms: rows in registers as vectors or element by element (threads a row), or the general one.
+constexpr int kVectorCols = 8 * 2 * 512, kElementCols = 8 * 512;
+int vector_threads(int32_t cols) { return threads_for(sbt_cdiv(cols / 8, 2), 512); }
+int element_threads(int32_t cols) { return threads_for(sbt_cdiv(cols, 8), 512); }
+// Rows of partial sums for dw.  512 threads an SM: the registers of two rows' loads and of the sums for dw.
+int register_parts(const sbt_context* ctx, int64_t rows, int G) {
+    return (int)std::min<int64_t>(rows, std::max<int64_t>(1, (int64_t)ctx->sm_count * std::max(1, 512 / G)));
+}
+int general_parts(const sbt_context* ctx, int64_t rows, int32_t cols) {
+    return (int)std::min<int64_t>(rows, std::max<int64_t>(1, 4 * ctx->sm_count / sbt_cdiv(cols, kAnyThreads)));
+}
+// The most that a call of these extents writes: addresses and strides say which form it takes.
+int most_parts(const sbt_context* ctx, int64_t rows, int32_t cols) {
+    int n = 0;
+    if (cols % 8 == 0 && cols <= kVectorCols) n = register_parts(ctx, rows, vector_threads(cols));
+    return std::max(n, cols <= kElementCols ? register_parts(ctx, rows, element_threads(cols)) : general_parts(ctx, rows, cols));
+}
+
 template <int KIND, int W, int NV>
 sbt_status launch_backward(sbt_context* ctx, NormBwdParams& p, int G, cudaStream_t stream) {
-    // 512 threads an SM: the registers of two rows' loads and of the sums for dw
-    p.parts = (int)std::min<int64_t>(p.rows, (int64_t)ctx->sm_count * std::max(1, 512 / G));
+    p.parts = register_parts(ctx, p.rows, G);
     if (sbt_status st = sbt_cuda_check(sbt_launch_dependent(k_add_norm_bwd<KIND, W, NV>, dim3(p.parts), dim3(G), 0,
                                                             stream, p),
                                        "add_rms_norm_backward launch"))
@@ -528,11 +545,11 @@ sbt_status backward(sbt_context* ctx, NormBwdParams& p, cudaStream_t stream) {
     sbt_status st = SBT_OK;
     if (p.rows == 0) {
         p.parts = 0;
-    } else if (vec && p.cols <= 8 * 2 * 512) {
-        const int units = p.cols / 8, G = threads_for(sbt_cdiv(units, 2), 512);
+    } else if (vec && p.cols <= kVectorCols) {
+        const int units = p.cols / 8, G = vector_threads(p.cols);
         st = units <= G ? launch_backward<KIND, 8, 1>(ctx, p, G, stream) : launch_backward<KIND, 8, 2>(ctx, p, G, stream);
-    } else if (p.cols <= 8 * 512) {
-        const int G = threads_for(sbt_cdiv(p.cols, 8), 512);
+    } else if (p.cols <= kElementCols) {
+        const int G = element_threads(p.cols);
         st = p.cols <= 4 * G ? launch_backward<KIND, 1, 4>(ctx, p, G, stream)
                              : launch_backward<KIND, 1, 8>(ctx, p, G, stream);
     } else {
@@ -542,7 +559,7 @@ sbt_status backward(sbt_context* ctx, NormBwdParams& p, cudaStream_t stream) {
             (st = sbt_after_launch(ctx, "add_rms_norm_backward")))
             return st;
         const int64_t blocks = sbt_cdiv(p.cols, kAnyThreads);
-        p.parts = (int)std::min<int64_t>(p.rows, std::max<int64_t>(1, 4 * ctx->sm_count / blocks));
+        p.parts = general_parts(ctx, p.rows, p.cols);
         if ((st = sbt_cuda_check(sbt_launch_dependent(k_add_norm_bwd_any<KIND>, dim3((unsigned)blocks, p.parts),
                                                       dim3(kAnyThreads), 0, stream, p),
                                  "add_rms_norm_backward launch")) == SBT_OK)
@@ -581,10 +598,12 @@ sbt_status sbt_launch_add_norm(sbt_context* ctx, sbt_dtype dtype, const SbtRows&
     }
 }
 
-// The parts of dw, then the general path's numbers per row.
+// The parts of dw, then the general form's numbers per row, which rows that fit registers without vectors never need.
+static size_t parts_bytes(const sbt_context* ctx, int64_t rows, int32_t cols) {
+    return (size_t)sbt_cdiv((int64_t)most_parts(ctx, rows, cols) * cols * 4, 256) * 256;
+}
 size_t sbt_add_norm_bwd_bytes(const sbt_context* ctx, int64_t rows, int32_t cols) {
-    const int64_t parts = std::min<int64_t>(rows, 16 * (int64_t)ctx->sm_count);
-    return (size_t)sbt_cdiv(parts * cols * 4, 256) * 256 + (size_t)rows * sizeof(float2);
+    return parts_bytes(ctx, rows, cols) + (cols > kElementCols ? (size_t)rows * sizeof(float2) : 0);
 }
 
 sbt_status sbt_launch_add_norm_bwd(sbt_context* ctx, sbt_dtype dtype, const SbtRows& gy, const SbtRows& gh,
@@ -598,9 +617,8 @@ sbt_status sbt_launch_add_norm_bwd(sbt_context* ctx, sbt_dtype dtype, const SbtR
     p.dx = (char*)const_cast<void*>(dx.p), p.ld_dx = dx.ld * es;
     p.w = (const char*)w, p.dw = dw;
     p.rows = rows, p.cols = cols, p.eps = eps;
-    const int64_t parts = std::min<int64_t>(rows, 16 * (int64_t)ctx->sm_count);
     p.partial = (float*)workspace;
-    p.stats = (float2*)((char*)workspace + sbt_cdiv(parts * cols * 4, 256) * 256);
+    p.stats = (float2*)((char*)workspace + parts_bytes(ctx, rows, cols));
     switch (kind_of(dtype)) {
         case kF32: return backward<kF32>(ctx, p, stream);
         case kBF16: return backward<kBF16>(ctx, p, stream);
