@@ -375,7 +375,8 @@ __global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED, LINE>::WARPS, S
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     const int want = max(top - 127 - 14, -126);
                     if (__any_sync(0xffffffffu, want > exponent[m])) {
-                        const int top_e = max(want, exponent[m]), gap = min(top_e - exponent[m], 127);
+                        // (2^-126 at least, for more: finite sums count for nothing then, and infinities stay what they are)
+                        const int top_e = max(want, exponent[m]), gap = min(top_e - exponent[m], 126);
                         exponent[m] = top_e;
                         // the rows of the sums are 2 t and 2 t + 1, held by lanes 8 t and 8 t + 4
                         const float f0 = power(-__shfl_sync(0xffffffffu, gap, 8 * t));
