@@ -639,11 +639,9 @@ SBT_API sbt_status sbt_tree_plan(sbt_context* ctx, const int32_t* parents, const
  *   t = L - n + j, t >= 0, j < n   and bit j of its mask row set (j <= i where mask is NULL).
  * Scores, out and lse are those of sbt_paged_attention over these positions;
  * lse is dense fp32 [rows][q_heads] or NULL.  Products and sums are fp32; a
- * probability enters the second product as the sum of two 16-bit numbers (16
- * significant bits with SBT_BF16, 22 with SBT_F16) where max_new * (q_heads /
- * cache->heads) <= 128 or head_dim > 128, and as one (8 and 11 bits) otherwise,
- * where that product bounds the call; with SBT_F16 in steps of 2^-33 of the
- * row's largest one at least.  A token that
+ * probability enters the second product as the sum of two 16-bit numbers, 16
+ * (SBT_BF16) and 22 (SBT_F16) significant bits, with SBT_F16 in steps of 2^-33 of
+ * the row's largest one at least.  A token that
  * sees nothing gets zeros and minus infinity.  Contents at positions that no
  * token of the entry sees are never read.  An entry with more than max_new
  * tokens, or with rows outside [0, rows), is left out; rows of no entry and of

@@ -19,10 +19,11 @@
 // instructions of the other half are left out.  Entries of more rows have more
 // planes, each a line of its own.
 //
-// P.  Few rows wait for memory, and there P is the sum of two 16-bit numbers (16
-// significant bits with bf16, 22 with fp16): one would add to the output's error
-// as much as the output's own rounding.  With MT = 2 the second product would be
-// a third more of the matrix time that bounds the call, and P is one number.
+// P is the sum of two 16-bit numbers (16 significant bits with bf16, 22 with fp16),
+// as in the attention of single tokens: one would add to the output's error as much
+// as the output's own rounding.  Where planes of 256 rows are full the second costs
+// 12 to 25 % (48 sequences of 64/8 heads, fp16: trees of 1 to 64 tokens 324 and 364 us
+// with one and two, 32 tokens 362 and 436, 64 tokens 705 and 880), elsewhere nothing.
 // fp16 ones are 2^SHIFT p, so that small ones are not lost among the subnormals.
 //
 // Roles.  A warp for every 32 rows does the softmax, a row a thread: it also
@@ -286,7 +287,6 @@ struct TreeShape {
     // (registers are bounded for whole warps on each of the SM's four partitions)
     static constexpr int BLOCKS = MT == 1 && DP <= 128 ? 2 : 1;
     static constexpr int R = MT * kRows;
-    static constexpr int TERMS = MT == 1 ? 2 : 1;               // 16-bit numbers of a probability, see the head of the file
     static constexpr uint32_t Q_TILE = kRows * DP * 2, SLOT = kTok * DP * 2;
     static constexpr uint32_t MOST = (BLOCKS == 2 ? 113 : 227) * 1024 - 8192 - 1536 - MT * Q_TILE;
     static constexpr int SLOTS = MOST / SLOT < 8 ? MOST / SLOT : 8;
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
                 if (elected()) {
                     if (live)
 #pragma unroll
-                        for (int j = 0; j < S::TERMS * kTok / 16; ++j)  // the first numbers, then the second ones
+                        for (int j = 0; j < 2 * kTok / 16; ++j)  // the first numbers, then the second ones
                             mma_ts(d, a + j * 8, b + ((j % 4) * 2048 >> 4), v_hi, idesc_o, j > 0 ? 1u : it > 0);
                     tc_commit(pv_done(m, buf));
                     tc_commit(empty(slot));
@@ -886,13 +886,11 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
                             const float2 e = make_float2(sbt_attn::exp2_fast(y.x), sbt_attn::exp2_fast(y.y));
                             sum[j & 1] = add2(sum[j & 1], e);
                             hi[j] = pack2<KIND>(e.x, e.y);
-                            if (S::TERMS == 2) {
-                                const float2 d = add2(e, unpack2<KIND>(hi[j] ^ 0x80008000u));
-                                lo[j] = pack2<KIND>(d.x, d.y);
-                            }
+                            const float2 d = add2(e, unpack2<KIND>(hi[j] ^ 0x80008000u));
+                            lo[j] = pack2<KIND>(d.x, d.y);
                         }
                         tmem_st_x8(s_t + c * 8, hi);
-                        if (S::TERMS == 2) tmem_st_x8(s_t + 32 + c * 8, lo);
+                        tmem_st_x8(s_t + 32 + c * 8, lo);
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_st_wait();
