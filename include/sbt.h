@@ -651,7 +651,7 @@ SBT_API sbt_status sbt_tree_plan(sbt_context* ctx, const int32_t* parents, const
  * sbt_tree_plan writes it (tokens from 32 ld_mask on are seen by none).
  * 1 <= head_dim <= 256, cache->heads divides q_heads, max_new * (q_heads /
  * cache->heads) < 2^24.  workspace as for sbt_paged_attention; its size depends
- * on neither the batch nor the lengths.
+ * on neither the batch nor the lengths, and serves every smaller max_new.
  */
 SBT_API sbt_status sbt_paged_tree_attention_workspace_size(sbt_context* ctx, int32_t max_new, int32_t q_heads,
                                                            int32_t kv_heads, int32_t head_dim, size_t* bytes);

@@ -41,13 +41,11 @@ sbt_status encode(sbt_context* ctx, CUtensorMap* map, const void* base, const sb
 
 }  // namespace
 
-size_t sbt_tree_attention_workspace_bytes(const sbt_context* ctx, int32_t max_new, int32_t q_heads, int32_t kv_heads,
-                                          int32_t head_dim) {
-    const int dp = padded(head_dim);
-    const int64_t rows = (int64_t)max_new * (q_heads / kv_heads);
-    const int mt = two_tiles(rows, dp) ? 2 : 1;
-    const int64_t R = (int64_t)mt * kRows, blocks = part_blocks(ctx, mt);
-    return (size_t)(sbt_cdiv(blocks * sizeof(TreeDesc), 256) * 256 + 2 * blocks * R * (sizeof(float2) + dp * sizeof(float)));
+// For two blocks of 128 rows an SM or one of 256, whose parts take the same room: a workspace serves any max_new.
+size_t sbt_tree_attention_workspace_bytes(const sbt_context* ctx, int32_t head_dim) {
+    const int64_t blocks = 2 * (int64_t)ctx->sm_count;
+    return (size_t)(sbt_cdiv(blocks * sizeof(TreeDesc), 256) * 256 +
+                    2 * blocks * kRows * (sizeof(float2) + padded(head_dim) * sizeof(float)));
 }
 
 sbt_status sbt_launch_tree_attention(sbt_context* ctx, sbt_dtype dtype, const SbtHeadRows& q, int32_t rows,

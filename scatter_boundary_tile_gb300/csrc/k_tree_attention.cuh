@@ -1130,9 +1130,6 @@ __global__ void __launch_bounds__(kJoin) k_tree_join(const TreeAttnParams p, int
     if (d == 0 && p.lse) p.lse[q_row * p.q_heads + qh] = sbt_attn::log_sum(top, l);
 }
 
-// Blocks that the workspace has room for: two an SM of 128 rows, or one of 256.
-inline int64_t part_blocks(const sbt_context* ctx, int mt) { return (int64_t)ctx->sm_count * (mt == 1 ? 2 : 1); }
-
 template <int KIND, int DP, int MT, bool TMA>
 sbt_status enqueue(sbt_context* ctx, TreeAttnParams& p, const TreeMaps& maps, void* workspace, cudaStream_t stream) {
     typedef TreeShape<KIND, DP, MT, TMA> S;

@@ -390,7 +390,7 @@ sbt_status sbt_paged_tree_attention_workspace_size(sbt_context* ctx, int32_t max
     const char* const w = "paged_tree_attention_workspace_size";
     SBT_REQUIRE(ctx && bytes, "paged_tree_attention_workspace_size: NULL argument");
     SBT_TRY(check_tree(max_new, q_heads, kv_heads, head_dim, w));
-    *bytes = sbt_tree_attention_workspace_bytes(ctx, max_new, q_heads, kv_heads, head_dim);
+    *bytes = sbt_tree_attention_workspace_bytes(ctx, head_dim);
     return SBT_OK;
 }
 
@@ -418,8 +418,7 @@ sbt_status sbt_paged_tree_attention(sbt_context* ctx, sbt_dtype dtype, const voi
     SBT_REQUIRE_ALIGNED(seq, 4, "paged_tree_attention: seq is not 4-byte aligned");
     SBT_REQUIRE_ALIGNED(mask, 4, "paged_tree_attention: mask is not 4-byte aligned");
     SBT_REQUIRE_ALIGNED(lse, 4, "paged_tree_attention: lse is not 4-byte aligned");
-    SBT_TRY(check_workspace(workspace, workspace_bytes,
-                            sbt_tree_attention_workspace_bytes(ctx, max_new, q_heads, cache->heads, cache->head_dim), w));
+    SBT_TRY(check_workspace(workspace, workspace_bytes, sbt_tree_attention_workspace_bytes(ctx, cache->head_dim), w));
     SBT_TRY(sbt_use_device(ctx));
     return sbt_launch_tree_attention(ctx, dtype, rq, rows, cu, batch, max_new, q_heads, cache, map, seq, scale, mask,
                                      ld_mask, ro, lse, workspace, (cudaStream_t)stream);

@@ -223,8 +223,7 @@ sbt_status sbt_launch_tree_attention(sbt_context* ctx, sbt_dtype dtype, const Sb
                                      const sbt_kv_cache* cache, const sbt_page_map* map, const int32_t* seq,
                                      float scale, const int32_t* mask, int64_t ld_mask, const SbtHeadRows& out,
                                      float* lse, void* workspace, cudaStream_t stream);
-size_t sbt_tree_attention_workspace_bytes(const sbt_context* ctx, int32_t max_new, int32_t q_heads, int32_t kv_heads,
-                                          int32_t head_dim);
+size_t sbt_tree_attention_workspace_bytes(const sbt_context* ctx, int32_t head_dim);
 
 // Operators of a decoding layer around the attention (k_add_norm.cu, k_matvec.cu).
 // Rows of a matrix, element stride.
