@@ -15,8 +15,8 @@ int piece(const void* a, int64_t ld0, int64_t ld1, int64_t ld2, int32_t head_dim
     return x % 16 == 0 ? 16 : x % 8 == 0 ? 8 : x % 4 == 0 ? 4 : 2;
 }
 
-// The tensor copy engine takes the pages where they hold whole boxes (8, 16, 32 or a multiple of 64 positions) and
-// every stride and address is a multiple of 16 bytes.
+// The tensor copy engine takes the pages where they hold whole boxes (8, 16, 32 or a multiple of 64 positions), every
+// stride and address is a multiple of 16 bytes, and the driver makes both maps; lanes copy them otherwise.
 bool map_ok(const sbt_context* ctx, const sbt_kv_cache* c, const sbt_page_map* m) {
     const int32_t P = m->page_size;
     if (ctx->path == SBT_PATH_SCALAR || ctx->path == SBT_PATH_VECTOR) return false;
@@ -26,17 +26,15 @@ bool map_ok(const sbt_context* ctx, const sbt_kv_cache* c, const sbt_page_map* m
            stride(m->n_pages, c->ld_page);
 }
 
-sbt_status encode(sbt_context* ctx, CUtensorMap* map, const void* base, const sbt_kv_cache* c, const sbt_page_map* m) {
+bool encode(sbt_context* ctx, CUtensorMap* map, const void* base, const sbt_kv_cache* c, const sbt_page_map* m) {
     auto bytes = [](int64_t n, int64_t ld) { return (cuuint64_t)(n == 1 ? 16 : ld * 2); };
     const cuuint64_t dims[4] = {(cuuint64_t)c->head_dim, (cuuint64_t)m->page_size, (cuuint64_t)c->heads,
                                 (cuuint64_t)m->n_pages};
     const cuuint64_t strides[3] = {bytes(m->page_size, c->ld_slot), bytes(c->heads, c->ld_head), bytes(m->n_pages, c->ld_page)};
     const cuuint32_t box[4] = {64, (cuuint32_t)std::min(m->page_size, kTok), 1, 1}, step[4] = {1, 1, 1, 1};
-    const CUresult r = ctx->encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), dims, strides, box,
-                                         step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return sbt_fail(SBT_ERR_TENSOR_MAP, "cuTensorMapEncodeTiled failed (" + std::to_string((int)r) + ")");
-    return SBT_OK;
+    return ctx->encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), dims, strides, box, step,
+                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -74,11 +72,7 @@ sbt_status sbt_launch_tree_attention(sbt_context* ctx, sbt_dtype dtype, const Sb
     p.status = ctx->status, p.wait_ns = ctx->wait_limit_ns;
     p.withhold = ctx->test_hook == SBT_TEST_WITHHOLD_LOAD;
     TreeMaps maps = {};
-    maps.use = map_ok(ctx, cache, map);
-    if (maps.use) {
-        if (sbt_status st = encode(ctx, &maps.k, cache->k, cache, map)) return st;
-        if (sbt_status st = encode(ctx, &maps.v, cache->v, cache, map)) return st;
-    }
+    maps.use = map_ok(ctx, cache, map) && encode(ctx, &maps.k, cache->k, cache, map) && encode(ctx, &maps.v, cache->v, cache, map);
     const int dp = padded(p.head_dim);
     if (dp > 128)
         return dtype == SBT_BF16 ? wide<kBF16>(ctx, p, maps, workspace, stream) : wide<kF16>(ctx, p, maps, workspace, stream);
