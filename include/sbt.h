@@ -642,8 +642,10 @@ SBT_API sbt_status sbt_tree_plan(sbt_context* ctx, const int32_t* parents, const
  * probability enters the second product as the sum of two 16-bit numbers, 16
  * (SBT_BF16) and 22 (SBT_F16) significant bits, with SBT_F16 in steps of 2^-33 of
  * the row's largest one at least.  A token that
- * sees nothing gets zeros and minus infinity.  Contents at positions that no
- * token of the entry sees are never read.  An entry with more than max_new
+ * sees nothing gets zeros and minus infinity.  Contents at positions that a token
+ * does not see reach none of its results, whatever they are; but all slots of the
+ * pages that hold the entry's positions may be read, those past the length too,
+ * so nothing may write them at the same time.  An entry with more than max_new
  * tokens, or with rows outside [0, rows), is left out; rows of no entry and of
  * entries left out are not written.
  *
