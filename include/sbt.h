@@ -601,7 +601,11 @@ SBT_API sbt_status sbt_pages_compact(sbt_context* ctx, const sbt_page_map* map, 
  * call here reads it) and of tokens whose sequence is outside [0, n_seq); in
  * positions and slots where the position is negative or at 2^31 or more; in
  * slots where the position has no page; in last where the entry has no token or
- * its last one is past the capacity.  slots needs n_pages * page_size <= 2^31.
+ * its last one is past the capacity.  An entry that the capacity cuts has places
+ * for its first tokens, at their positions, and none for the others, which its
+ * sequence then lacks; sbt_paged_tree_attention would take those places for the
+ * sequence's last tokens, so choose a capacity for all tokens, or give the attention
+ * a seq outside [0, n_seq) for that entry.  slots needs n_pages * page_size <= 2^31.
  * map->refs is not needed, map->lens only where start is NULL.
  */
 SBT_API sbt_status sbt_pages_slots(sbt_context* ctx, const sbt_page_map* map, const int32_t* n_new, int32_t batch,
@@ -633,8 +637,9 @@ SBT_API sbt_status sbt_tree_plan(sbt_context* ctx, const int32_t* parents, const
  *
  * Entry b's tokens are the rows cu[b] .. cu[b+1] - 1 of q and out, n of them; with
  * L the length of sequence s = seq[b] (b where seq is NULL), token j of the entry
- * stands at position L - n + j.  Token i sees the positions t of its sequence on
- * a page of the pool with
+ * stands at position L - n + j: all n of them have to be there, so an entry that
+ * sbt_pages_slots has cut at its capacity is not one to attend.  Token i sees the
+ * positions t of its sequence on a page of the pool with
  *   0 <= t < L - n                 (what was held before), or
  *   t = L - n + j, t >= 0, j < n   and bit j of its mask row set (j <= i where mask is NULL).
  * Scores, out and lse are those of sbt_paged_attention over these positions;
