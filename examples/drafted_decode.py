@@ -6,6 +6,8 @@ Prompts are read in one step: slot maps from the requests' lengths, the residual
 GEMM over 4-bit weights, norm and rotation of queries and keys, append to the pages, attention of all new tokens.  Then
 each step appends a small tree of drafted tokens per sequence (the norm's 16-bit output and matrix-vector products over
 the same weights), attends with the trees' masks, keeps one path of each tree and gives the other tokens' places back.
+The output projection reads the attention's 16-bit numbers, of which no call makes codes, so it is a matrix-vector
+product in both kinds of step (for a prompt it passes over the weights once per 16 tokens).
 """
 import os
 import sys
@@ -19,7 +21,7 @@ BLOCK = 32  # columns per scale of the codes, and weights per scale
 
 
 class DraftedLayer:
-    """Weights, cache and page state of one layer; `n_seq` sequences of up to `max_len` tokens, `most` new ones a step."""
+    """Weights, cache and page state of one layer; `n_seq` sequences of up to `max_len` tokens, up to `most` new ones a step."""
 
     def __init__(self, ctx, d_model=256, q_heads=8, kv_heads=2, dim=64, page_size=16, n_seq=3, max_len=256, n_pages=60,
                  most=200, seed=0):
@@ -92,14 +94,18 @@ class DraftedLayer:
         sbt.add_rms_norm(self.ctx, x, c, rows, c, weight=self.weight, r=r, h_out=h, **ld, y=y, ld_y=c)
         return h, y, None
 
-    def step(self, x, r, m, parents=None, coded=False):
-        """New tokens of all sequences, in the order of their slots: rows x of the layer's input, r of the residual stream."""
+    def step(self, x, r, m, parents=None, coded=False, most=None):
+        """New tokens of all sequences, in the order of their slots: rows x of the layer's input, r of the residual stream.
+
+        `most`: no sequence has more new tokens (the layer's own limit where it is not given); the attention shares its
+        blocks out by it, and the masks are as wide."""
+        most = most or self.most
         rows, hq, hk, d = x.shape[0], self.hq, self.hk, self.d
         h, y, codes = self.norm(x, r, coded)
         qkv = self.project(y, self.w_in, self.s_in, codes)
         turned, mask, words = m["positions"], None, 0
         if parents is not None:  # a token's place in its tree turns it, its place in the cache is its own
-            turned, words = self.empty(rows, dtype=torch.int32), -(-self.most // 32)
+            turned, words = self.empty(rows, dtype=torch.int32), -(-most // 32)
             mask = self.empty(rows, words, dtype=torch.int32)
             sbt.tree_plan(self.ctx, parents, m["cu"], self.n_seq, rows, mask=mask, ld_mask=words,
                           positions=m["positions"], turned=turned)
@@ -110,11 +116,11 @@ class DraftedLayer:
         sbt.qk_norm_rope(self.ctx, None, 0, 0, k, hk * d, d, rows, 0, hk, d, m["positions"], None, None, 0, 0,
                          v=at(hq + hk), ld_v=ld, ld_vh=d, cache=self.cache, map=self.map, seq=m["seq"], dtype="bf16")
         heads = torch.zeros_like(q)
-        sbt.paged_tree_attention(self.ctx, q, hq * d, d, rows, m["cu"], self.n_seq, self.most, hq, self.cache, self.map,
+        sbt.paged_tree_attention(self.ctx, q, hq * d, d, rows, m["cu"], self.n_seq, most, hq, self.cache, self.map,
                                  d**-0.5, heads, hq * d, d, mask=mask, ld_mask=words, workspace=self.attn_ws,
                                  workspace_bytes=self.attn_ws.numel())
         out = self.project(heads.view(rows, -1), self.w_out, self.s_out)
-        return out, h, dict(q=q, k=k, qkv=qkv, heads=heads, mask=mask, turned=turned)
+        return out, h, dict(q=q, k=k, qkv=qkv, heads=heads, mask=mask, turned=turned, out=out, h=h)
 
     def record(self, saw, m, x, r, parents=None):
         """What a step read and computed, and the cache as it was then."""
@@ -148,7 +154,7 @@ def run(ctx, steps=4, seed=1, log=None):
     layer.grow(n_new)
     m = layer.slots(n_new, sum(prompt))
     x, r = rnd(sum(prompt)), rnd(sum(prompt))
-    _, _, saw = layer.step(x, r, m, coded=True)
+    _, _, saw = layer.step(x, r, m, coded=True, most=max(prompt))
     records = [layer.record(saw, m, x, r)]
     n, b = len(TREE), layer.n_seq
     n_new, parents = i32([n] * b), i32(TREE * b)
@@ -157,7 +163,7 @@ def run(ctx, steps=4, seed=1, log=None):
         layer.grow(n_new)
         m = layer.slots(n_new, n * b)
         x, r = rnd(n * b), rnd(n * b)
-        _, _, saw = layer.step(x, r, m, parents=parents)
+        _, _, saw = layer.step(x, r, m, parents=parents, most=n)
         records.append(layer.record(saw, m, x, r, parents))
         rows = torch.tensor([n * i + j for i in range(b) for j in PATH], device="cuda")
         to = torch.tensor([n * i + j for i in range(b) for j in range(len(PATH))], device="cuda")
