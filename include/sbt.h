@@ -678,7 +678,8 @@ SBT_API sbt_status sbt_paged_tree_attention(sbt_context* ctx, sbt_dtype dtype, c
  * per row of `cols` elements, in fp32 (weight NULL: 1); h_out and y get h and y,
  * each rounded once, and codes (where given) y in 8 bits with a scale per block
  * of columns, which is what sbt_gemm_block_scaled reads as A and a_scale with
- * K_s = cols / block:
+ * K_s = cols / block (a mean of squares past fp32's range makes y zero; one of zero
+ * with eps = 0 divides by zero):
  *
  *   scales[row][j] = 2^e, the least power of two (2^-124 at least; 1 for a block of
  *                    zeros) with which no |y| of columns j*block .. (j+1)*block - 1

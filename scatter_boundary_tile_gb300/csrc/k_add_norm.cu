@@ -23,8 +23,10 @@
 // Measured (GB300; at the copy rate in brackets): 16384 x 8192 bf16 with the
 // residual to codes 162 us (139), to numbers 152 (119); 16384 x 4096 fp32 157 (119);
 // 333 x 5003 fp16 6.9 us (2.0), element by element 7.2; a single row 5.4, what the
-// host takes for a call.  Gradient, 16384 x 4096 bf16 89 us (79), of which the
-// second launch (the blocks' sums for dw) is 4; 1021 x 1537 fp32 8.9 (3.7).
+// host takes for a call (2.0 in a graph).  Gradient, 16384 x 4096 bf16 89 us (79), of
+// which the second launch (the blocks' sums for dw) is 4; 1021 x 1537 fp32 8.6 (3.7).
+// The forms that read twice, element by element, bf16: 4096 x 20480 252 us (99),
+// gradient of 8192 x 16384 665 (159), of 16384 x 4097 340 (79).
 #include <algorithm>
 
 #include "sbt_internal.cuh"

@@ -6,8 +6,9 @@
 // rate an SM has to turn ~47 of them a clock into numbers and multiply them for
 // up to 16 rows.  The products run on mma.sync m16n8k16 (fp16 in, fp32 sums):
 // 16 columns of w by 8 rows of x, 16 k.  E2M1 is exact in fp16 and has a
-// conversion of two codes at once; a tcgen05 tile would want the weights as
-// fp16 in shared memory, written there by the same instructions and read again.
+// conversion of two codes at once; a tcgen05 tile in fp16 would want the weights
+// in shared memory, written there by the same instructions and read again.  (One of
+// E2M1 codes with block scales and x as a sum of E4M3 codes has not been tried.)
 //
 // A column's neighbour lies in the same byte, but the conversion and the matrix
 // instruction want pairs along k: two bytes of rows k and k + 1 trade nibbles
@@ -43,7 +44,8 @@
 // Measured (GB300), weights at copy rate in brackets: 1 token bf16, 4096 x 4096
 // 8.3 us (1.3: launch, first copies and two joins are its time), 5 tokens fp16,
 // 28672 x 8192 with E4M3 scales per 16 41 us (19.5), 8 tokens fp16, 131072 x 4096
-// 71 us (43), 16 tokens fp16 99, bf16 118, with unaligned scales 123.  The ALU pipe
+// 71 us (43), 16 tokens fp16 99, bf16 118, with unaligned scales 123; fp32 x, 65536 x
+// 4096, 1 and 8 tokens 58 us (21; bf16 42), 16 tokens 105 (bf16 70).  The ALU pipe
 // (50 to 60 % busy) and dependent instructions bound the large ones: 21
 // instructions for 256 weights with 8 tokens, 32 with 16 of bf16.
 #include <algorithm>

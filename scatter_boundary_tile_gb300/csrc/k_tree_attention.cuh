@@ -36,7 +36,8 @@
 //
 // Split.  All (entry, key-value head, plane) lines, cut into tiles, lie on one
 // line on which every block gets an even range; lengths are read on the device.
-// (Planes in turn on one range: 463 us for the batch below instead of 369 then.)
+// (Planes in turn on one range: 463 us for the batch below instead of 369, one number
+// per probability.)
 // Rows wholly inside a range are written by their block; of a line cut by range
 // borders each block writes its state to the workspace and k_tree_join adds them
 // in the order of the line.
@@ -48,14 +49,15 @@
 //
 // Measured (GB300, 128 elements a head; the cache at the copy rate in brackets).
 // MT = 1: one sequence, 32 tokens on 16384 positions, 32/8 heads, bf16 38 us (10),
-// on 131072 112 (79), on 2048 23: the launches, a cold instruction cache and the
+// on 131072 114 (79), on 2048 25: the launches, a cold instruction cache and the
 // join are most of a short call.  MT = 2: 48 sequences, 32 tokens on 8192
-// positions, 64/8 heads, fp16 390 us (240); trees of 1 to 64 tokens on contexts to
-// 8191 330 (130).  There a tile takes ~1650 cycles, half of a chain over two: scores
-// to P 1280 (two such warps share an SM partition, in step), P seen 260, product
-// and next scores issued 1200 beside the other half's, scores done and seen 580.
-// The products alone are ~1280 (with 64 columns they read Q from shared memory at
-// 3/2 of the time that their multiplication takes).
+// positions, 64/8 heads, fp16 450 us (246); trees of 1 to 64 tokens on contexts to
+// 8191 385 (130).  There a tile takes ~1900 cycles, the round of the warp that issues
+// the products: P seen 270, product issued 540, next scores 860, beside the other
+// half's.  The softmax, 1180 cycles from scores to P, waits for it (one number per
+// probability: 1650 cycles, and it waits for the softmax).  The products alone are
+// ~1540 by their sizes (with 64 columns they read Q from shared memory at 3/2 of the
+// time that their multiplication takes).
 //
 // Every wait is bounded; one that runs out sets the device status word, and the
 // kernel drains and returns.
@@ -430,7 +432,8 @@ __global__ void __launch_bounds__((TreeShape<KIND, DP, MT, TMA>::WARPS + 3) / 4 
     } else if (TMA && (warp == 4 * MT || warp == 4 * MT + 1)) {
         // ------------------------------------------------------------ copies by the tensor copy engine
         // One warp copies K and one V: to start a tile's copies takes a warp ~900 cycles (one for both took longer than
-        // the products: 8 trees of 48 tokens on 8192 positions, 32/8 heads of 128, 92 us, and 82 so).
+        // the products: 8 trees of 48 tokens on 8192 positions, 32/8 heads of 128, 92 us, and 82 so; but 48 of 32 tokens,
+        // 64/8 heads in fp16, 383 and 393; both with one number per probability).
         // A tile is a box of 64 elements and a page's positions (64 at most) for every 128 bytes of its rows; a lane
         // starts one of them.  A page that is not there is a coordinate outside the tensor, which reads as zeros.
         const bool is_v = warp != 4 * MT;
