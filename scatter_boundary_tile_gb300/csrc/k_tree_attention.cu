@@ -64,8 +64,8 @@ sbt_status sbt_launch_tree_attention(sbt_context* ctx, sbt_dtype dtype, const Sb
     p.max_len = (int32_t)std::min<int64_t>((int64_t)map->max_pages * map->page_size, INT32_MAX - 1023);
     p.group = sbt_make_fastdiv((uint32_t)(q_heads / cache->heads));
     p.page_size = sbt_make_fastdiv((uint32_t)map->page_size);
-    // (a scale of zero would make NaN of a masked score of minus infinity; 2^-126 of any finite one is as good as zero)
-    p.scale = std::max(fabsf(scale) * 1.4426950408889634f, 0x1p-126f), p.negate = scale < 0.f;
+    // (a scale of zero would make NaN of a masked score of minus infinity; 2^-149 of any finite one is 2^-21 at most)
+    p.scale = std::max(fabsf(scale) * 1.4426950408889634f, 0x1p-149f), p.negate = scale < 0.f;
     p.q_vec = piece(q.p, q.ld, q.ldh, 0, p.head_dim) == 16;
     p.copy_kv = std::min(piece(p.k, p.ld_page, p.ld_slot, p.ld_head, p.head_dim), piece(p.v, 0, 0, 0, p.head_dim));
     p.out_vec = piece(out.p, out.ld, out.ldh, 0, p.head_dim) == 16;
