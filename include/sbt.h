@@ -707,7 +707,8 @@ SBT_API sbt_status sbt_add_rms_norm(sbt_context* ctx, sbt_dtype dtype, const voi
 /*
  * Gradient of sbt_add_rms_norm at h (its h_out, or x where there is no r): with
  * gy the gradient of y and gh that of h_out (NULL: zero), dx gets the gradient
- * of h, which is that of x and of r, in `dtype`, and dweight (fp32 [cols],
+ * of h, which is that of x and of r (a row that was added to all, with a stride of
+ * zero, has the sum of dx over the rows), in `dtype`, and dweight (fp32 [cols],
  * required exactly where weight is given) the weight's, summed over the rows in
  * fp32 in an order that is fixed on one device.  dx may be gy, gh or h (same
  * stride).  workspace as elsewhere, of
