@@ -50,6 +50,7 @@
 // instructions for 256 weights with 8 tokens, 32 with 16 of bf16.
 #include <algorithm>
 
+#include "matvec_copies.h"
 #include "sbt_internal.cuh"
 #include "sbt_num.cuh"
 #include "tc_ptx.cuh"
@@ -194,9 +195,9 @@ __global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED, LINE>::WARPS, S
     const int s_left = per - (int)(u0 - s_row * per);       // (not for `each`, whose `per` is one)
     auto copy_start = [&] {
         const int64_t n0 = columns(copy_item);
-        w_bytes = (int)max((int64_t)0, min((int64_t)(S::CW / 2), (p.N + 1) / 2 - n0 / 2));
-        s_bytes = (int)max((int64_t)0, min((int64_t)S::CW, p.N - n0));
-        copy_bytes = min(max(w_bytes - copy_c, 0), 16);
+        w_bytes = sbt_matvec::bytes_of((p.N + 1) / 2, n0 / 2, S::CW / 2);
+        s_bytes = sbt_matvec::bytes_of(p.N, n0, S::CW);
+        copy_bytes = sbt_matvec::piece_of(w_bytes, 0, copy_c);
         copy_w = p.w + n0 / 2 + (u0 * ROWS + copy_r) * p.ld_w;
         copy_s = p.s + s_row * p.ld_s + n0;
         copy_left = each ? 1 : s_left, copy_todo = todo;
@@ -231,20 +232,20 @@ __global__ void __launch_bounds__(32 * Shape<U, SU, MT, ALIGNED, LINE>::WARPS, S
             // one piece more than a row has covers it from the 16-byte boundary before it
 #pragma unroll 4
             for (int i = 0; i < ROWS / (16 / LPR); ++i) {
-                const int shift = (int)((uintptr_t)src & 15), bytes = min(max(shift + w_bytes - copy_c, 0), 16);
+                const int shift = (int)((uintptr_t)src & 15), bytes = sbt_matvec::piece_of(w_bytes, shift, copy_c);
                 if (bytes) copy16(dst + (i * (16 / LPR) + copy_r) * S::PITCH + copy_c, src - shift + copy_c, bytes);
                 src += (16 / LPR) * p.ld_w;
             }
         }
         if (s_aligned) {
-            const int row = lane / 8, at = lane % 8 * 16, bytes = min(max(s_bytes - at, 0), 16);
+            const int row = lane / 8, at = lane % 8 * 16, bytes = sbt_matvec::piece_of(s_bytes, 0, at);
             if (row < s_rows && bytes)
                 copy16(dst + ROWS * S::PITCH + row * S::SCALES + at, copy_s + row * p.ld_s + at, bytes);
         } else {
             for (int row = 0; row < s_rows; ++row) {
                 const uint8_t* const a = copy_s + row * p.ld_s;
-                const int shift = (int)((uintptr_t)a & 15), bytes = min(max(shift + s_bytes - lane * 16, 0), 16);
-                if (s_bytes && bytes) copy16(dst + ROWS * S::PITCH + row * S::SCALES + lane * 16, a - shift + lane * 16, bytes);
+                const int shift = (int)((uintptr_t)a & 15), bytes = sbt_matvec::piece_of(s_bytes, shift, lane * 16);
+                if (bytes) copy16(dst + ROWS * S::PITCH + row * S::SCALES + lane * 16, a - shift + lane * 16, bytes);
             }
         }
         if (--copy_left == 0) copy_left = per, copy_s += s_rows * p.ld_s;
